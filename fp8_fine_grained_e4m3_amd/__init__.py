@@ -55,6 +55,12 @@ EXPORTED = (
     "dg_pack_ue8m0_scales_k_grouped",
     "dg_fp8_gemm_nt_workspace_bytes",
     "dg_fp8_gemm_nt_noalloc",
+    "dg_fp8_kv_cache_write",
+    "dg_fp8_kv_cache_read",
+    "dg_fp8_tree_attention",
+    "dg_fp8_tree_attention_workspace_bytes",
+    "dg_fp8_moe_few_tokens",
+    "dg_fp8_moe_few_tokens_workspace_bytes",
 )
 DG_CAST_POW2_SCALE = 1
 
@@ -121,6 +127,19 @@ def load_library(path: Optional[str] = None):
     for name in ("dg_fp8_gemm_nt_ue8m0", "dg_m_grouped_fp8_gemm_nt_contiguous_ue8m0",
                  "dg_m_grouped_fp8_gemm_nt_masked_ue8m0", "dg_pack_ue8m0_scales"):
         getattr(lib, name).restype = I
+    F = ctypes.c_float
+    lib.dg_fp8_kv_cache_write.argtypes = [P, P, I, I64, I64, P, P, P, P, P, I64, I64, I64, I64, I64, P]
+    lib.dg_fp8_kv_cache_read.argtypes = [P, P, P, P, P, P, P, I, I64, I64, I64, I64, I64, P]
+    lib.dg_fp8_tree_attention.argtypes = [P, I64, P, P, P, P, P, P, P, P, P, P, F, I64, I64, I64, I64,
+                                          I64, I64, I64, I64, P, I64, P]
+    lib.dg_fp8_moe_few_tokens.argtypes = [P, P, P, P, P, P, P, P, I, I64, I64, I64, I64, I64, P, I64, P]
+    for name in ("dg_fp8_kv_cache_write", "dg_fp8_kv_cache_read", "dg_fp8_tree_attention",
+                 "dg_fp8_moe_few_tokens"):
+        getattr(lib, name).restype = I
+    lib.dg_fp8_tree_attention_workspace_bytes.argtypes = [I64] * 7
+    lib.dg_fp8_tree_attention_workspace_bytes.restype = I64
+    lib.dg_fp8_moe_few_tokens_workspace_bytes.argtypes = [I64] * 4
+    lib.dg_fp8_moe_few_tokens_workspace_bytes.restype = I64
     if path is None:
         _lib = lib
     return lib
@@ -568,4 +587,251 @@ def pack_ue8m0_scales_k_grouped(sf: torch.Tensor, k_sizes: Sequence[int]) -> tor
         _check(load_library().dg_pack_ue8m0_scales_k_grouped(
             _ptr(sf), ks.ctypes.data_as(ctypes.c_void_p), _ptr(out), len(ks), MN, KB * 128,
             _stream(sf)))
+    return out
+
+
+# ---- few tokens at a time: FP8 cache, tree attention, mixture of experts ---------------------
+
+def make_fp8_kv_cache(num_pages: int, num_kv_heads: int, page_size: int, head_dim: int, device=None):
+    """An empty paged FP8 cache: ((k codes, k scales), (v codes, v scales)),
+    codes uint8 [num_pages, num_kv_heads, page_size, head_dim], scales fp32
+    [num_pages, num_kv_heads, page_size].  page_size is a power of two from 16
+    to 4096, head_dim 64, 128 or 256."""
+    shape = (num_pages, num_kv_heads, page_size, head_dim)
+    device = torch.cuda.current_device() if device is None else device
+    return tuple((torch.zeros(shape, dtype=torch.uint8, device=device),
+                  torch.ones(shape[:3], dtype=torch.float32, device=device)) for _ in range(2))
+
+
+def _cache(cache):
+    """The cache's four tensors, checked, and its sizes."""
+    (kc, ks), (vc, vs) = cache
+    kc, vc, ks, vs = _fp8(kc, "k codes"), _fp8(vc, "v codes"), _f32(ks, "k scales"), _f32(vs, "v scales")
+    if kc.dim() != 4 or kc.shape != vc.shape or ks.shape != kc.shape[:3] or vs.shape != kc.shape[:3]:
+        raise ValueError(f"cache shapes: codes {tuple(kc.shape)} {tuple(vc.shape)}, scales {tuple(ks.shape)} "
+                         f"{tuple(vs.shape)}, want [pages, heads, page_size, head_dim] and its first three")
+    return kc, ks, vc, vs, kc.shape
+
+
+def _rows(t: torch.Tensor, name: str) -> torch.Tensor:
+    """Device rows whose last two dimensions are dense and whose tokens are evenly spaced."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.numel() and (t.stride(-1) != 1 or (t.shape[-2] > 1 and t.stride(-2) != t.shape[-1])):
+        raise ValueError(f"{name}: heads and head_dim must be dense, strides are {t.stride()}")
+    return t
+
+
+def _token_stride(t: torch.Tensor) -> int:
+    """Elements between tokens; what a single token has there says nothing."""
+    dense = t.shape[-1] * t.shape[-2]
+    return t.stride(-3) if t.shape[-3] > 1 else dense
+
+
+def _same_device(first: torch.Tensor, *others):
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+
+
+_ROW_TYPES = {torch.bfloat16: DG_BF16, torch.float32: DG_F32}
+
+
+def fp8_kv_cache_write(k: torch.Tensor, v: torch.Tensor, cache, slots: torch.Tensor):
+    """Quantises k, v [T, H, D] (bf16 or fp32; tokens may be strided, as in a
+    slice of a fused projection) into the cache's slots (int32 [T], page *
+    page_size + offset; a slot outside the cache stores nothing).  One fp32
+    scale per token and head.  Changes and returns the cache
+    (make_fp8_kv_cache)."""
+    kc, ks, vc, vs, (P, H, page, D) = _cache(cache)
+    k, v, slots = _rows(k, "k"), _rows(v, "v"), _i32(slots, "slots")
+    if k.dtype not in _ROW_TYPES or v.dtype != k.dtype:
+        raise TypeError(f"k and v must both be bfloat16 or float32, got {k.dtype} and {v.dtype}")
+    T = slots.shape[0] if slots.dim() == 1 else -1
+    if tuple(k.shape) != (T, H, D) or v.shape != k.shape:
+        raise ValueError(f"shape mismatch: k {tuple(k.shape)} v {tuple(v.shape)} slots {tuple(slots.shape)}, "
+                         f"the cache has {H} heads of {D}")
+    _same_device(kc, ks, vc, vs, k, v, slots)
+    with torch.cuda.device(kc.device):
+        _check(load_library().dg_fp8_kv_cache_write(
+            k.data_ptr(), v.data_ptr(), _ROW_TYPES[k.dtype], _token_stride(k), _token_stride(v),
+            slots.data_ptr(), kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), T, H, D, P, page,
+            _stream(kc)))
+    return cache
+
+
+def fp8_kv_cache_read(cache, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
+                      out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None):
+    """The keys and values at slots (int32 [T]) of the cache as (k, v) [T, H, D]
+    of dtype (bfloat16 or float32), or into out; a slot outside the cache gives
+    zeros."""
+    kc, ks, vc, vs, (P, H, page, D) = _cache(cache)
+    slots = _i32(slots, "slots")
+    if slots.dim() != 1:
+        raise ValueError(f"slots must be [T], got {tuple(slots.shape)}")
+    T = slots.shape[0]
+    if out is None:
+        if dtype not in _ROW_TYPES:
+            raise TypeError(f"dtype must be bfloat16 or float32, got {dtype}")
+        k = torch.empty((T, H, D), dtype=dtype, device=kc.device)
+        v = torch.empty_like(k)
+    else:
+        k, v = _dev(out[0], "out k"), _dev(out[1], "out v")
+        if k.dtype not in _ROW_TYPES or v.dtype != k.dtype:
+            raise TypeError(f"out must both be bfloat16 or float32, got {k.dtype} and {v.dtype}")
+        if tuple(k.shape) != (T, H, D) or v.shape != k.shape:
+            raise ValueError(f"out shapes {tuple(k.shape)} {tuple(v.shape)}, want {(T, H, D)}")
+    _same_device(kc, ks, vc, vs, slots, k, v)
+    with torch.cuda.device(kc.device):
+        _check(load_library().dg_fp8_kv_cache_read(
+            kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), slots.data_ptr(), k.data_ptr(),
+            v.data_ptr(), _ROW_TYPES[k.dtype], T, H, D, P, page, _stream(kc)))
+    return k, v
+
+
+def _workspace(given: Optional[torch.Tensor], need: int, device):
+    """The caller's workspace, or one of torch's allocator for this call; (tensor, address, bytes)."""
+    if given is None:
+        if need == 0:
+            return None, 0, 0
+        given = torch.empty(need, dtype=torch.uint8, device=device)
+    elif given.dtype != torch.uint8:
+        raise TypeError("workspace must be uint8")
+    return _dev(given, "workspace"), given.data_ptr(), given.numel()
+
+
+def get_fp8_tree_attention_workspace_bytes(B: int, N: int, Hq: int, num_kv_heads: int, head_dim: int,
+                                           page_size: int, max_pages: int) -> int:
+    """Workspace bytes a tree attention call of these sizes needs (0: none)."""
+    return int(load_library().dg_fp8_tree_attention_workspace_bytes(B, N, Hq, num_kv_heads, head_dim,
+                                                                    page_size, max_pages))
+
+
+def make_fp8_tree_attention_workspace(q: torch.Tensor, cache, page_table: torch.Tensor) -> torch.Tensor:
+    """A workspace for fp8_tree_attention calls with arguments of these shapes.
+    Stream-ordered calls may share it."""
+    B, N, Hq, D = q.shape
+    _, H, page, _ = cache[0][0].shape
+    need = get_fp8_tree_attention_workspace_bytes(B, N, Hq, H, D, page, page_table.shape[1])
+    return torch.empty(need, dtype=torch.uint8, device=q.device)
+
+
+def fp8_tree_attention(q: torch.Tensor, cache, page_table: torch.Tensor, context_lens: torch.Tensor,
+                       tree_lens: Optional[torch.Tensor] = None, tree_mask: Optional[torch.Tensor] = None,
+                       scale: Optional[float] = None,
+                       out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
+                       workspace: Optional[torch.Tensor] = None):
+    """Attention of drafted tokens q [B, N, Hq, D] (bf16; tokens may be strided)
+    over the FP8 cache.  page_table int32 [B, max_pages]; request b has
+    context_lens[b] tokens in the cache, then its tree_lens[b] (int32 [B], N
+    when None) drafted ones.  tree_mask int64 [B, N, ceil(N/64)]: bit j % 64 of
+    word j / 64 of token i lets it see drafted token j (None: a chain, j <= i);
+    every context token is seen.  scale defaults to D ** -0.5.  Returns (o bf16
+    like q, lse fp32 [B, N, Hq]), or fills out; rows past a tree's end, and rows
+    that see nothing, are 0 and -inf.  workspace: a uint8 buffer
+    (make_fp8_tree_attention_workspace); when None, one is allocated for the
+    call."""
+    kc, ks, vc, vs, (P, H, page, D) = _cache(cache)
+    q = _rows(q, "q")
+    if q.dtype != torch.bfloat16:
+        raise TypeError(f"q must be bfloat16, got {q.dtype}")
+    if q.dim() != 4 or q.shape[3] != D:
+        raise ValueError(f"q {tuple(q.shape)} must be [B, N, Hq, {D}]")
+    B, N, Hq, _ = q.shape
+    stride = _token_stride(q) if N > 1 or B <= 1 else q.stride(0)
+    if B > 1 and q.stride(0) != N * stride:
+        raise ValueError(f"q: tokens must be evenly spaced over requests, strides are {q.stride()}")
+    table, ctx = _i32(page_table, "page_table"), _i32(context_lens, "context_lens")
+    if table.dim() != 2 or table.shape[0] != B or tuple(ctx.shape) != (B,):
+        raise ValueError(f"page_table {tuple(table.shape)} and context_lens {tuple(ctx.shape)} must be "
+                         f"[{B}, max_pages] and [{B}]")
+    if tree_lens is not None and tuple(_i32(tree_lens, "tree_lens").shape) != (B,):
+        raise ValueError(f"tree_lens {tuple(tree_lens.shape)} must be [{B}]")
+    if tree_mask is not None:
+        if tree_mask.dtype != torch.int64:
+            raise TypeError(f"tree_mask must be int64, got {tree_mask.dtype}")
+        if tuple(_dev(tree_mask, "tree_mask").shape) != (B, N, (N + 63) // 64):
+            raise ValueError(f"tree_mask {tuple(tree_mask.shape)} must be {(B, N, (N + 63) // 64)}")
+    if out is None:
+        o = torch.empty((B, N, Hq, D), dtype=torch.bfloat16, device=q.device)
+        lse = torch.empty((B, N, Hq), dtype=torch.float32, device=q.device)
+    else:
+        o, lse = _dev(out[0], "out"), _f32(out[1], "lse")
+        if o.dtype != torch.bfloat16:
+            raise TypeError("out must be bfloat16")
+        if o.shape != q.shape or tuple(lse.shape) != (B, N, Hq):
+            raise ValueError(f"out shapes {tuple(o.shape)} {tuple(lse.shape)}, want {tuple(q.shape)} and {(B, N, Hq)}")
+    need = get_fp8_tree_attention_workspace_bytes(B, N, Hq, H, D, page, table.shape[1])
+    workspace, ws, ws_bytes = _workspace(workspace, need, q.device)
+    _same_device(q, kc, ks, vc, vs, table, ctx, tree_lens, tree_mask, o, lse, workspace)
+    with torch.cuda.device(q.device):
+        _check(load_library().dg_fp8_tree_attention(
+            q.data_ptr(), stride, kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(),
+            table.data_ptr(), ctx.data_ptr(), 0 if tree_lens is None else tree_lens.data_ptr(),
+            0 if tree_mask is None else tree_mask.data_ptr(), o.data_ptr(), lse.data_ptr(),
+            D ** -0.5 if scale is None else scale, B, N, Hq, H, D, P, page, table.shape[1], ws, ws_bytes,
+            _stream(q)))
+    return o, lse
+
+
+def get_fp8_moe_few_tokens_workspace_bytes(T: int, topk: int, E: int, I: int) -> int:
+    """Workspace bytes a few-token mixture-of-experts call of these sizes needs."""
+    return int(load_library().dg_fp8_moe_few_tokens_workspace_bytes(T, topk, E, I))
+
+
+def make_fp8_moe_few_tokens_workspace(x: torch.Tensor, w2: Tuple[torch.Tensor, torch.Tensor],
+                                      topk_ids: torch.Tensor) -> torch.Tensor:
+    """A workspace for fp8_moe_few_tokens calls with arguments of these shapes.
+    Stream-ordered calls may share it."""
+    E, _, I = w2[0].shape
+    need = get_fp8_moe_few_tokens_workspace_bytes(topk_ids.shape[0], topk_ids.shape[1], E, I)
+    return torch.empty(need, dtype=torch.uint8, device=x.device)
+
+
+def fp8_moe_few_tokens(x: torch.Tensor, w1: Tuple[torch.Tensor, torch.Tensor],
+                       w2: Tuple[torch.Tensor, torch.Tensor], topk_ids: torch.Tensor,
+                       topk_weights: torch.Tensor, out: Optional[torch.Tensor] = None,
+                       dtype: torch.dtype = torch.bfloat16,
+                       workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """A mixture-of-experts layer for x bf16 [T, H], T <= 256:
+    y[t] = sum_j topk_weights[t, j] * W2_e (silu(W1_e[:I] x[t]) * (W1_e[I:] x[t])),
+    e = topk_ids[t, j] (int32 [T, topk]; ids outside [0, E) take no part).
+    w1 = (W1 e4m3 [E, 2I, H], fp32 [E, 2I/128, H/128]), w2 = (W2 e4m3 [E, H, I],
+    fp32 [E, H/128, I/128]), as per_block_cast_to_fp8 makes them; H and I are
+    multiples of 128.  Returns y [T, H] of dtype (bfloat16 or float32), or fills
+    out.  workspace: a uint8 buffer (make_fp8_moe_few_tokens_workspace); when
+    None, one is allocated for the call."""
+    x = _dev(x, "x")
+    if x.dtype != torch.bfloat16:
+        raise TypeError(f"x must be bfloat16, got {x.dtype}")
+    W1, S1, W2, S2 = _fp8(w1[0], "W1"), _f32(w1[1], "S1"), _fp8(w2[0], "W2"), _f32(w2[1], "S2")
+    ids, weights = _i32(topk_ids, "topk_ids"), _f32(topk_weights, "topk_weights")
+    if x.dim() != 2 or W1.dim() != 3 or W2.dim() != 3 or ids.dim() != 2:
+        raise ValueError("x and topk_ids must be 2-D, W1 and W2 3-D")
+    T, H = x.shape
+    E, H2, I = W2.shape
+    if H2 != H or tuple(W1.shape) != (E, 2 * I, H) or ids.shape[0] != T or weights.shape != ids.shape:
+        raise ValueError(f"shape mismatch: x {tuple(x.shape)} W1 {tuple(W1.shape)} W2 {tuple(W2.shape)} "
+                         f"topk_ids {tuple(ids.shape)} topk_weights {tuple(weights.shape)}")
+    if tuple(S1.shape) != (E, 2 * I // 128, H // 128) or tuple(S2.shape) != (E, H // 128, I // 128):
+        raise ValueError(f"scale shapes: S1 {tuple(S1.shape)} S2 {tuple(S2.shape)}, want "
+                         f"{(E, 2 * I // 128, H // 128)} and {(E, H // 128, I // 128)}")
+    if out is None:
+        if dtype not in _ROW_TYPES:
+            raise TypeError(f"dtype must be bfloat16 or float32, got {dtype}")
+        out = torch.empty((T, H), dtype=dtype, device=x.device)
+    else:
+        out = _dev(out, "out")
+        if out.dtype not in _ROW_TYPES:
+            raise TypeError(f"out must be bfloat16 or float32, got {out.dtype}")
+        if out.shape != x.shape:
+            raise ValueError(f"out {tuple(out.shape)} must be {tuple(x.shape)}")
+    need = get_fp8_moe_few_tokens_workspace_bytes(T, ids.shape[1], E, I)
+    workspace, ws, ws_bytes = _workspace(workspace, need, x.device)
+    _same_device(x, W1, S1, W2, S2, ids, weights, out, workspace)
+    with torch.cuda.device(x.device):
+        _check(load_library().dg_fp8_moe_few_tokens(
+            x.data_ptr(), W1.data_ptr(), S1.data_ptr(), W2.data_ptr(), S2.data_ptr(), ids.data_ptr(),
+            weights.data_ptr(), out.data_ptr(), _ROW_TYPES[out.dtype], T, ids.shape[1], E, H, I, ws, ws_bytes,
+            _stream(x)))
     return out

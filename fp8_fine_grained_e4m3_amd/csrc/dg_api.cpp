@@ -2,11 +2,13 @@
 // CU-count cap, error reporting, and dispatch to the kernels.
 #include "../../include/dg.h"
 #include "dg_internal.h"
+#include "serve_internal.h"
 
 #include <hip/hip_runtime.h>
 
 #include <atomic>
 #include <climits>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -617,6 +619,264 @@ dg_status dg_fp8_mqa_logits(const uint8_t* q, const uint8_t* kv, const float* kv
     dg_status st = current_device(dev, info);
     if (st != DG_OK) return st;
     hipError_t e = dg::launch_mqa(p, reinterpret_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(DG_ERR_HIP, "kernel launch: %s", hipGetErrorString(e));
+    return ok();
+}
+
+// ---- few tokens at a time ---------------------------------------------------------
+
+static bool cache_page_ok(int64_t page_size) {
+    return page_size >= 16 && page_size <= 4096 && (page_size & (page_size - 1)) == 0;
+}
+
+static bool cache_dim_ok(int64_t D) { return D == 64 || D == 128 || D == 256; }
+
+static dg_status check_cache(const dg::KvCache& c) {
+    const uint8_t *k_codes = c.k_codes, *v_codes = c.v_codes;
+    const float *k_sf = c.k_sf, *v_sf = c.v_sf;
+    REQUIRE_PTR(k_codes, 16);
+    REQUIRE_PTR(k_sf, 16);
+    REQUIRE_PTR(v_codes, 16);
+    REQUIRE_PTR(v_sf, 16);
+    return DG_OK;
+}
+
+static dg_status check_cache_sizes(const dg::KvCache& c) {
+    REQUIRE(c.H >= 0 && c.num_pages >= 0, "negative size (H=%lld num_pages=%lld)", (long long)c.H,
+            (long long)c.num_pages);
+    REQUIRE(cache_dim_ok(c.D), "D=%lld must be 64, 128 or 256", (long long)c.D);
+    REQUIRE(cache_page_ok(c.page_size), "page_size=%lld must be a power of two from 16 to 4096",
+            (long long)c.page_size);
+    REQUIRE(c.H <= 65535, "H=%lld too large", (long long)c.H);
+    REQUIRE(c.num_pages <= INT_MAX / c.page_size, "num_pages * page_size must stay below 2^31");
+    return DG_OK;
+}
+
+// Whether [p, p + n) stays clear of the cache's four arrays.
+static bool clear_of_cache(const dg::KvCache& c, const void* p, int64_t n) {
+    const int64_t rows = c.num_pages * c.H * c.page_size;
+    return disjoint(p, n, c.k_codes, rows * c.D) && disjoint(p, n, c.v_codes, rows * c.D) &&
+           disjoint(p, n, c.k_sf, rows * 4) && disjoint(p, n, c.v_sf, rows * 4);
+}
+
+static dg_status kv_cache_copy(dg::KvCopy p, dg_dtype dtype, bool write, void* stream) {
+    dg_status st = check_cache_sizes(p.cache);
+    if (st != DG_OK) return st;
+    REQUIRE(p.T >= 0, "negative size (T=%lld)", (long long)p.T);
+    REQUIRE(dtype == DG_BF16 || dtype == DG_F32, "dtype must be DG_BF16 or DG_F32");
+    const int64_t H = p.cache.H, D = p.cache.D, size = dtype == DG_F32 ? 4 : 2;
+    REQUIRE(p.T <= INT_MAX, "T=%lld too large", (long long)p.T);
+    REQUIRE(p.k_stride >= H * D && p.v_stride >= H * D && p.k_stride <= kOffsetLimit && p.v_stride <= kOffsetLimit,
+            "k_stride=%lld and v_stride=%lld must be from H * D = %lld to 2^31", (long long)p.k_stride,
+            (long long)p.v_stride, (long long)(H * D));
+    REQUIRE(p.k_stride * size % 16 == 0 && p.v_stride * size % 16 == 0,
+            "k_stride and v_stride must be multiples of 16 bytes");
+    if (p.T == 0 || H == 0) return ok();
+    REQUIRE(p.cache.num_pages >= 1, "num_pages=0: the cache is empty");
+    const void *k = p.k, *v = p.v;
+    const int32_t* slots = p.slots;
+    REQUIRE_PTR(k, 16);
+    REQUIRE_PTR(v, 16);
+    REQUIRE_PTR(slots, 16);
+    st = check_cache(p.cache);
+    if (st != DG_OK) return st;
+    REQUIRE(p.T <= INT_MAX / H, "T * H must stay below 2^31");
+    const int64_t kn = ((p.T - 1) * p.k_stride + H * D) * size, vn = ((p.T - 1) * p.v_stride + H * D) * size;
+    REQUIRE(clear_of_cache(p.cache, k, kn) && clear_of_cache(p.cache, v, vn) &&
+                clear_of_cache(p.cache, slots, 4 * p.T),
+            "k, v or slots overlap the cache");
+    if (write) {
+        const dg::KvCache& c = p.cache;
+        const int64_t rows = c.num_pages * H * c.page_size;
+        REQUIRE(disjoint(c.k_codes, rows * D, c.v_codes, rows * D) && disjoint(c.k_sf, rows * 4, c.v_sf, rows * 4) &&
+                    disjoint(c.k_codes, rows * D, c.k_sf, rows * 4) && disjoint(c.k_codes, rows * D, c.v_sf, rows * 4) &&
+                    disjoint(c.v_codes, rows * D, c.k_sf, rows * 4) && disjoint(c.v_codes, rows * D, c.v_sf, rows * 4),
+                "the cache's arrays overlap");
+    } else {
+        REQUIRE(disjoint(k, kn, v, vn) && disjoint(k, kn, slots, 4 * p.T) && disjoint(v, vn, slots, 4 * p.T),
+                "k, v and slots must not overlap");
+    }
+    p.f32 = dtype == DG_F32;
+    int dev = 0;
+    DeviceInfo info;
+    st = current_device(dev, info);
+    if (st != DG_OK) return st;
+    hipStream_t on = reinterpret_cast<hipStream_t>(stream);
+    hipError_t e = write ? dg::launch_kv_cache_write(p, on) : dg::launch_kv_cache_read(p, on);
+    if (e != hipSuccess) return fail(DG_ERR_HIP, "kernel launch: %s", hipGetErrorString(e));
+    return ok();
+}
+
+dg_status dg_fp8_kv_cache_write(const void* k, const void* v, dg_dtype dtype, int64_t k_stride,
+                                int64_t v_stride, const int32_t* slots, uint8_t* k_codes,
+                                float* k_sf, uint8_t* v_codes, float* v_sf, int64_t T, int64_t H,
+                                int64_t D, int64_t num_pages, int64_t page_size, void* stream) {
+    dg::KvCopy p{};
+    p.cache = dg::KvCache{k_codes, k_sf, v_codes, v_sf, num_pages, H, page_size, D};
+    p.slots = slots;
+    p.k = const_cast<void*>(k); p.v = const_cast<void*>(v);
+    p.k_stride = k_stride; p.v_stride = v_stride; p.T = T;
+    return kv_cache_copy(p, dtype, true, stream);
+}
+
+dg_status dg_fp8_kv_cache_read(const uint8_t* k_codes, const float* k_sf, const uint8_t* v_codes,
+                               const float* v_sf, const int32_t* slots, void* k, void* v,
+                               dg_dtype dtype, int64_t T, int64_t H, int64_t D, int64_t num_pages,
+                               int64_t page_size, void* stream) {
+    dg::KvCopy p{};
+    p.cache = dg::KvCache{const_cast<uint8_t*>(k_codes), const_cast<float*>(k_sf),
+                          const_cast<uint8_t*>(v_codes), const_cast<float*>(v_sf),
+                          num_pages, H, page_size, D};
+    p.slots = slots;
+    p.k = k; p.v = v;
+    p.k_stride = p.v_stride = H > 0 && H <= 65535 && cache_dim_ok(D) ? H * D : 0;
+    p.T = T;
+    return kv_cache_copy(p, dtype, false, stream);
+}
+
+// What the sizes of a tree attention call have to be; "" where they are right.
+static const char* tree_attn_sizes_wrong(int64_t B, int64_t N, int64_t Hq, int64_t H, int64_t D,
+                                         int64_t page_size, int64_t max_pages) {
+    if (B < 0 || N < 0 || Hq < 0 || H < 1 || max_pages < 1) return "B, N, Hq >= 0, H >= 1 and max_pages >= 1 are needed";
+    if (!cache_dim_ok(D)) return "D must be 64, 128 or 256";
+    if (!cache_page_ok(page_size)) return "page_size must be a power of two from 16 to 4096";
+    if (H > 65535 || Hq > 65535 || Hq % H != 0) return "Hq must be a multiple of H, both at most 65535";
+    if (max_pages > (1LL << 30) / page_size) return "max_pages * page_size must be at most 2^30";
+    if (N >= (1LL << 20) || N * Hq >= (1LL << 20)) return "N * Hq must stay below 2^20";
+    if (B > (1LL << 20) || B * H > (1LL << 20)) return "B * H must be at most 2^20";
+    return "";
+}
+
+int64_t dg_fp8_tree_attention_workspace_bytes(int64_t B, int64_t N, int64_t Hq, int64_t H,
+                                              int64_t D, int64_t page_size, int64_t max_pages) {
+    if (B <= 0 || N <= 0 || Hq <= 0 || *tree_attn_sizes_wrong(B, N, Hq, H, D, page_size, max_pages)) return 0;
+    return dg::tree_attn_workspace_bytes(B, N, Hq, H, D, max_pages, page_size);
+}
+
+dg_status dg_fp8_tree_attention(const void* q, int64_t q_stride, const uint8_t* k_codes,
+                                const float* k_sf, const uint8_t* v_codes, const float* v_sf,
+                                const int32_t* page_table, const int32_t* context_lens,
+                                const int32_t* tree_lens, const uint64_t* tree_mask, void* o,
+                                float* lse, float scale, int64_t B, int64_t N, int64_t Hq,
+                                int64_t H, int64_t D, int64_t num_pages, int64_t page_size,
+                                int64_t max_pages, void* workspace, int64_t workspace_bytes,
+                                void* stream) {
+    const char* wrong = tree_attn_sizes_wrong(B, N, Hq, H, D, page_size, max_pages);
+    REQUIRE(!*wrong, "%s (B=%lld N=%lld Hq=%lld H=%lld D=%lld page_size=%lld max_pages=%lld)", wrong,
+            (long long)B, (long long)N, (long long)Hq, (long long)H, (long long)D, (long long)page_size,
+            (long long)max_pages);
+    REQUIRE(num_pages >= 1 && num_pages <= INT_MAX / page_size,
+            "num_pages=%lld: num_pages * page_size must be from page_size to 2^31", (long long)num_pages);
+    REQUIRE(q_stride >= Hq * D && q_stride % 8 == 0 && q_stride <= kOffsetLimit,
+            "q_stride=%lld must be a multiple of 8 from Hq * D = %lld to 2^31", (long long)q_stride,
+            (long long)(Hq * D));
+    REQUIRE(std::isfinite(scale), "scale is not finite");
+    if (B == 0 || N == 0 || Hq == 0) return ok();
+    dg::TreeAttnProblem p{};
+    p.cache = dg::KvCache{const_cast<uint8_t*>(k_codes), const_cast<float*>(k_sf),
+                          const_cast<uint8_t*>(v_codes), const_cast<float*>(v_sf),
+                          num_pages, H, page_size, D};
+    REQUIRE_PTR(q, 16);
+    dg_status st = check_cache(p.cache);
+    if (st != DG_OK) return st;
+    REQUIRE_PTR(page_table, 16);
+    REQUIRE_PTR(context_lens, 16);
+    if (tree_lens) REQUIRE_PTR(tree_lens, 16);
+    if (tree_mask) REQUIRE_PTR(tree_mask, 16);
+    REQUIRE_PTR(o, 16);
+    REQUIRE_PTR(lse, 16);
+    const int64_t need = dg::tree_attn_workspace_bytes(B, N, Hq, H, D, max_pages, page_size);
+    REQUIRE(workspace_bytes >= need, "workspace_bytes=%lld < %lld needed for these sizes",
+            (long long)workspace_bytes, (long long)need);
+    if (need > 0) REQUIRE_PTR(workspace, 16);
+    const int64_t tokens = B * N, on = tokens * Hq * D * 2, ln = tokens * Hq * 4,
+                  qn = ((tokens - 1) * q_stride + Hq * D) * 2;
+    const struct { const void* p; int64_t n; } in[] = {
+        {q, qn}, {page_table, B * max_pages * 4}, {context_lens, B * 4},
+        {tree_lens, tree_lens ? B * 4 : 0}, {tree_mask, tree_mask ? tokens * ((N + 63) / 64) * 8 : 0}},
+                 out[] = {{o, on}, {lse, ln}, {workspace, need}};
+    for (int i = 0; i < 3; ++i) {
+        if (out[i].n == 0) continue;
+        REQUIRE(clear_of_cache(p.cache, out[i].p, out[i].n), "o, lse or workspace overlaps the cache");
+        for (const auto& x : in)
+            REQUIRE(x.n == 0 || disjoint(out[i].p, out[i].n, x.p, x.n), "o, lse or workspace overlaps an input");
+        for (int j = 0; j < i; ++j)
+            REQUIRE(disjoint(out[i].p, out[i].n, out[j].p, out[j].n), "o, lse and workspace overlap");
+    }
+    p.q = static_cast<const uint16_t*>(q); p.q_stride = q_stride;
+    p.page_table = page_table; p.context_lens = context_lens;
+    p.tree_lens = tree_lens; p.tree_mask = tree_mask;
+    p.o = static_cast<uint16_t*>(o); p.lse = lse; p.scale = scale;
+    p.B = B; p.N = N; p.Hq = Hq; p.max_pages = max_pages;
+    p.workspace = workspace;
+    int dev = 0;
+    DeviceInfo info;
+    st = current_device(dev, info);
+    if (st != DG_OK) return st;
+    hipError_t e = dg::launch_tree_attn(p, reinterpret_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(DG_ERR_HIP, "kernel launch: %s", hipGetErrorString(e));
+    return ok();
+}
+
+static const char* moe_few_sizes_wrong(int64_t T, int64_t topk, int64_t E, int64_t I) {
+    if (T < 0 || T > dg::kMoeMaxTokens) return "T must be from 0 to 256";
+    if (topk < 1 || topk > dg::kMoeMaxTopk) return "topk must be from 1 to 16";
+    if (E < 1 || E > dg::kMoeMaxExperts) return "E must be from 1 to 1024";
+    if (I < 128 || I % 128 != 0 || I > (1 << 17)) return "I must be a multiple of 128 up to 2^17";
+    return "";
+}
+
+int64_t dg_fp8_moe_few_tokens_workspace_bytes(int64_t T, int64_t topk, int64_t E, int64_t I) {
+    if (*moe_few_sizes_wrong(T, topk, E, I) || T == 0) return 0;
+    return dg::moe_few_workspace_bytes(T, topk, E, I);
+}
+
+dg_status dg_fp8_moe_few_tokens(const void* x, const uint8_t* w1, const float* s1,
+                                const uint8_t* w2, const float* s2, const int32_t* topk_ids,
+                                const float* topk_weights, void* y, dg_dtype y_dtype, int64_t T,
+                                int64_t topk, int64_t E, int64_t H, int64_t I, void* workspace,
+                                int64_t workspace_bytes, void* stream) {
+    const char* wrong = moe_few_sizes_wrong(T, topk, E, I);
+    REQUIRE(!*wrong, "%s (T=%lld topk=%lld E=%lld I=%lld)", wrong, (long long)T, (long long)topk,
+            (long long)E, (long long)I);
+    REQUIRE(H >= 128 && H % 128 == 0 && H <= (1 << 17), "H=%lld must be a multiple of 128 up to 2^17",
+            (long long)H);
+    REQUIRE(y_dtype == DG_BF16 || y_dtype == DG_F32, "y_dtype must be DG_BF16 or DG_F32");
+    if (T == 0) return ok();
+    REQUIRE_PTR(x, 16);
+    REQUIRE_PTR(w1, 16);
+    REQUIRE_PTR(s1, 16);
+    REQUIRE_PTR(w2, 16);
+    REQUIRE_PTR(s2, 16);
+    REQUIRE_PTR(topk_ids, 16);
+    REQUIRE_PTR(topk_weights, 16);
+    REQUIRE_PTR(y, 16);
+    const int64_t need = dg::moe_few_workspace_bytes(T, topk, E, I);
+    REQUIRE(workspace != nullptr, "workspace is NULL: %lld bytes are needed "
+            "(dg_fp8_moe_few_tokens_workspace_bytes)", (long long)need);
+    REQUIRE_PTR(workspace, 16);
+    REQUIRE(workspace_bytes >= need, "workspace_bytes=%lld < %lld needed for these sizes",
+            (long long)workspace_bytes, (long long)need);
+    const int64_t yn = T * H * (y_dtype == DG_F32 ? 4 : 2);
+    const struct { const void* p; int64_t n; } in[] = {
+        {x, T * H * 2}, {w1, E * 2 * I * H}, {s1, E * (2 * I / 128) * (H / 128) * 4}, {w2, E * H * I},
+        {s2, E * (H / 128) * (I / 128) * 4}, {topk_ids, T * topk * 4}, {topk_weights, T * topk * 4}};
+    for (const auto& b : in)
+        REQUIRE(disjoint(y, yn, b.p, b.n) && disjoint(workspace, need, b.p, b.n),
+                "y or workspace overlaps an input");
+    REQUIRE(disjoint(y, yn, workspace, need), "y and workspace overlap");
+    dg::MoeFewProblem p{};
+    p.x = static_cast<const uint16_t*>(x);
+    p.w1 = w1; p.s1 = s1; p.w2 = w2; p.s2 = s2;
+    p.ids = topk_ids; p.weights = topk_weights;
+    p.y = y; p.out_f32 = y_dtype == DG_F32;
+    p.T = T; p.topk = topk; p.E = E; p.H = H; p.I = I;
+    p.workspace = workspace;
+    int dev = 0;
+    DeviceInfo info;
+    dg_status st = current_device(dev, info);
+    if (st != DG_OK) return st;
+    hipError_t e = dg::launch_moe_few(p, reinterpret_cast<hipStream_t>(stream));
     if (e != hipSuccess) return fail(DG_ERR_HIP, "kernel launch: %s", hipGetErrorString(e));
     return ok();
 }

@@ -1,0 +1,49 @@
+// Device helpers on e4m3 codes and bf16 fragments shared by the few-token
+// kernels (gfx950 only).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace dg {
+
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
+typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
+
+// Two e4m3 bytes of a word (the low or the high half) as two bf16: exact,
+// every e4m3 value is a bf16 value.
+template <bool HIGH>
+__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t w) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HIGH));
+}
+
+// Eight consecutive e4m3 bytes as an MFMA fragment of eight bf16.
+__device__ __forceinline__ bf16x8_t e4m3x8_to_bf16x8(uint32_t lo, uint32_t hi) {
+    u32x4_t r;
+    r.x = e4m3x2_to_bf16x2<false>(lo);
+    r.y = e4m3x2_to_bf16x2<true>(lo);
+    r.z = e4m3x2_to_bf16x2<false>(hi);
+    r.w = e4m3x2_to_bf16x2<true>(hi);
+    return __builtin_bit_cast(bf16x8_t, r);
+}
+
+// Two fp32 as two bf16 in a word, each rounded to nearest even.
+__device__ __forceinline__ uint32_t f32x2_to_bf16x2(float a, float b) {
+    bf16x2_t r;
+    r.x = (__bf16)a;
+    r.y = (__bf16)b;
+    return __builtin_bit_cast(uint32_t, r);
+}
+
+// 16 rows x 32 K of bf16 by 16 columns x 32 K, added to acc: lane l passes
+// eight K values of row (and of column) l & 15, the same ones for both
+// operands; it gets out[4 * (l >> 4) + i][l & 15], i = 0..3.
+__device__ __forceinline__ f32x4_t mfma_bf16(bf16x8_t rows, bf16x8_t cols, f32x4_t acc) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(rows, cols, acc, 0, 0, 0);
+}
+
+}  // namespace dg

@@ -429,6 +429,131 @@ dg_status dg_fp8_mqa_logits(const uint8_t* q, const uint8_t* kv, const float* kv
                             float* logits, int64_t S, int64_t S_kv, int64_t H, int64_t D,
                             int clean_logits, void* stream);
 
+/*
+ * Few tokens at a time: the FP8 key/value cache, attention for drafted tokens
+ * over it, and a mixture-of-experts layer.  The conventions above hold (device
+ * pointers, 16-byte alignment, stream, errors, no allocation, no
+ * synchronisation); calls may be captured into a HIP graph.
+ *
+ * The cache is paged.  For the keys and for the values:
+ *   codes [num_pages, H, page_size, D]  e4m3
+ *   sf    [num_pages, H, page_size]     fp32, one scale per token and head
+ * with value = code * sf.  H is the number of key/value heads, D is 64, 128 or
+ * 256, page_size a power of two from 16 to 4096, num_pages * page_size < 2^31.
+ * A token's place is its slot, page * page_size + offset.
+ */
+
+/*
+ * Quantises T tokens' keys and values into their slots.  For each row of D
+ * values (one token, one head):
+ *   s    = max |x| / 448 in fp32, correctly rounded; 1 where that is 0
+ *   code = the e4m3 value nearest to clamp(x / s, -448, 448), x / s the
+ *          correctly rounded fp32 quotient, ties to the even mantissa
+ * A row that holds a NaN or an infinity gets the scale NaN and codes 0: it
+ * reads as NaN, and tokens that do not see it are not touched by it.
+ *   k, v     [T, H, D]  DG_BF16 or DG_F32, k_stride / v_stride elements from
+ *                       token to token (a slice of a fused projection will do),
+ *                       16-byte multiples; heads and D dense
+ *   slots    [T]        int32; a slot outside [0, num_pages * page_size) marks
+ *                       a token that is not stored.  A slot given twice in one
+ *                       call leaves either token's values, in whole codes.
+ * One kernel launch.
+ */
+dg_status dg_fp8_kv_cache_write(const void* k, const void* v, dg_dtype dtype,
+                                int64_t k_stride, int64_t v_stride, const int32_t* slots,
+                                uint8_t* k_codes, float* k_sf, uint8_t* v_codes, float* v_sf,
+                                int64_t T, int64_t H, int64_t D, int64_t num_pages,
+                                int64_t page_size, void* stream);
+
+/*
+ * Reads T slots back: k[t, h, :] = code * sf in fp32, rounded once for
+ * DG_BF16; a slot outside the cache gives zeros.
+ *   k, v  [T, H, D] of dtype, dense.
+ * One kernel launch.
+ */
+dg_status dg_fp8_kv_cache_read(const uint8_t* k_codes, const float* k_sf,
+                               const uint8_t* v_codes, const float* v_sf, const int32_t* slots,
+                               void* k, void* v, dg_dtype dtype,
+                               int64_t T, int64_t H, int64_t D, int64_t num_pages,
+                               int64_t page_size, void* stream);
+
+/*
+ * Attention of the drafted tokens of B requests over the cache.  Request b has
+ * c = context_lens[b] tokens in the cache and a tree of n = tree_lens[b] <= N
+ * drafted tokens, whose keys and values are in the cache too, tree token j at
+ * position c + j.  Position p lies in page page_table[b, p / page_size] at
+ * offset p % page_size.  Token i < n sees every position below c, and c + j for
+ * each j < n whose bit is set in its mask.  With N = 1 this is decode attention.
+ *   S_p = scale * (q . k_p),  o = sum_p softmax(S)_p v_p,  lse = ln sum_p exp S_p
+ * A token that sees nothing, and every token i >= n, gets o = 0, lse = -inf.
+ *   q            [B, N, Hq, D]  bf16, q_stride elements from token to token
+ *                               (a multiple of 8, request to request N times
+ *                               that); Hq % H == 0, query head hq reads key
+ *                               head hq / (Hq / H)
+ *   page_table   [B, max_pages] int32; a page outside [0, num_pages) hides its
+ *                               positions.  Entries past a request's last
+ *                               token are not used.
+ *   context_lens [B]            int32, clamped to [0, max_pages * page_size]
+ *   tree_lens    [B]            int32, clamped to [0, N]; NULL: all N
+ *   tree_mask    [B, N, ceil(N/64)]  64-bit words; bit j % 64 of word j / 64
+ *                               of token i: it sees token j.  NULL: a chain
+ *                               (j <= i).
+ *   o            [B, N, Hq, D]  bf16, rounded once from fp32 sums
+ *   lse          [B, N, Hq]     fp32
+ * Tree positions past max_pages * page_size are not seen.  Codes 0x7F and 0xFF
+ * (NaN) are not allowed at positions below c + n; dg_fp8_kv_cache_write never
+ * makes them, and past c + n the cache may hold anything.
+ * Rules: max_pages >= 1, max_pages * page_size <= 2^30, N * Hq < 2^20.
+ * workspace: dg_fp8_tree_attention_workspace_bytes of the same sizes (0 where
+ * the keys are not split over workgroups; never initialised), not shared by
+ * calls that may overlap.  A size has one order of sums whatever the lengths
+ * of the other requests.  One or two kernel launches.
+ */
+dg_status dg_fp8_tree_attention(const void* q, int64_t q_stride,
+                                const uint8_t* k_codes, const float* k_sf,
+                                const uint8_t* v_codes, const float* v_sf,
+                                const int32_t* page_table, const int32_t* context_lens,
+                                const int32_t* tree_lens, const uint64_t* tree_mask,
+                                void* o, float* lse, float scale,
+                                int64_t B, int64_t N, int64_t Hq, int64_t H, int64_t D,
+                                int64_t num_pages, int64_t page_size, int64_t max_pages,
+                                void* workspace, int64_t workspace_bytes, void* stream);
+/* A function of the sizes alone (no HIP call); 0 for sizes that are rejected. */
+int64_t dg_fp8_tree_attention_workspace_bytes(int64_t B, int64_t N, int64_t Hq, int64_t H,
+                                              int64_t D, int64_t page_size, int64_t max_pages);
+
+/*
+ * A whole mixture-of-experts layer for a few tokens:
+ *   y[t] = sum_j topk_weights[t, j] * W2_e (silu(W1_e[:I] x[t]) * (W1_e[I:] x[t])),
+ *   e = topk_ids[t, j]
+ * where W1_e, W2_e are an expert's e4m3 weights with their block scales (the B
+ * operands of the M-grouped NT GEMMs, as dg_per_block_cast_to_fp8 makes them).
+ * x is taken as it is (bf16, not quantised) and sums and the hidden values are
+ * kept to 16 bits of mantissa or more (fp32's for a DG_F32 y).
+ *   x            [T, H]       bf16
+ *   w1           [E, 2I, H]   e4m3: I gate rows, then I up rows
+ *   s1           [E, 2I/128, H/128]  fp32
+ *   w2           [E, H, I]    e4m3
+ *   s2           [E, H/128, I/128]   fp32
+ *   topk_ids     [T, topk]    int32; an id outside [0, E) takes no part (an
+ *                             expert elsewhere, a dropped slot); a token with
+ *                             none gets y = 0.  An id twice in a token counts
+ *                             with the sum of its weights.
+ *   topk_weights [T, topk]    fp32
+ *   y            [T, H]       DG_BF16 (rounded once) or DG_F32
+ * Rules: T <= 256, 1 <= topk <= 16, 1 <= E <= 1024, H and I multiples of 128 up
+ * to 2^17.
+ * workspace: dg_fp8_moe_few_tokens_workspace_bytes(T, topk, E, I), never
+ * initialised, not shared by calls that may overlap.  Two kernel launches.
+ */
+dg_status dg_fp8_moe_few_tokens(const void* x, const uint8_t* w1, const float* s1,
+                                const uint8_t* w2, const float* s2, const int32_t* topk_ids,
+                                const float* topk_weights, void* y, dg_dtype y_dtype,
+                                int64_t T, int64_t topk, int64_t E, int64_t H, int64_t I,
+                                void* workspace, int64_t workspace_bytes, void* stream);
+/* A function of the sizes alone (no HIP call); 0 for sizes that are rejected. */
+int64_t dg_fp8_moe_few_tokens_workspace_bytes(int64_t T, int64_t topk, int64_t E, int64_t I);
+
 /* Message for the last non-OK status returned on this thread ("" if none). */
 const char* dg_last_error(void);
 
