@@ -138,7 +138,7 @@ def load_library(path: Optional[str] = None):
         getattr(lib, name).restype = I
     lib.dg_fp8_tree_attention_workspace_bytes.argtypes = [I64] * 7
     lib.dg_fp8_tree_attention_workspace_bytes.restype = I64
-    lib.dg_fp8_moe_few_tokens_workspace_bytes.argtypes = [I64] * 4
+    lib.dg_fp8_moe_few_tokens_workspace_bytes.argtypes = [I64] * 5
     lib.dg_fp8_moe_few_tokens_workspace_bytes.restype = I64
     if path is None:
         _lib = lib
@@ -774,17 +774,17 @@ def fp8_tree_attention(q: torch.Tensor, cache, page_table: torch.Tensor, context
     return o, lse
 
 
-def get_fp8_moe_few_tokens_workspace_bytes(T: int, topk: int, E: int, I: int) -> int:
+def get_fp8_moe_few_tokens_workspace_bytes(T: int, topk: int, E: int, H: int, I: int) -> int:
     """Workspace bytes a few-token mixture-of-experts call of these sizes needs."""
-    return int(load_library().dg_fp8_moe_few_tokens_workspace_bytes(T, topk, E, I))
+    return int(load_library().dg_fp8_moe_few_tokens_workspace_bytes(T, topk, E, H, I))
 
 
 def make_fp8_moe_few_tokens_workspace(x: torch.Tensor, w2: Tuple[torch.Tensor, torch.Tensor],
                                       topk_ids: torch.Tensor) -> torch.Tensor:
     """A workspace for fp8_moe_few_tokens calls with arguments of these shapes.
     Stream-ordered calls may share it."""
-    E, _, I = w2[0].shape
-    need = get_fp8_moe_few_tokens_workspace_bytes(topk_ids.shape[0], topk_ids.shape[1], E, I)
+    E, H, I = w2[0].shape
+    need = get_fp8_moe_few_tokens_workspace_bytes(topk_ids.shape[0], topk_ids.shape[1], E, H, I)
     return torch.empty(need, dtype=torch.uint8, device=x.device)
 
 
@@ -826,7 +826,7 @@ def fp8_moe_few_tokens(x: torch.Tensor, w1: Tuple[torch.Tensor, torch.Tensor],
             raise TypeError(f"out must be bfloat16 or float32, got {out.dtype}")
         if out.shape != x.shape:
             raise ValueError(f"out {tuple(out.shape)} must be {tuple(x.shape)}")
-    need = get_fp8_moe_few_tokens_workspace_bytes(T, ids.shape[1], E, I)
+    need = get_fp8_moe_few_tokens_workspace_bytes(T, ids.shape[1], E, H, I)
     workspace, ws, ws_bytes = _workspace(workspace, need, x.device)
     _same_device(x, W1, S1, W2, S2, ids, weights, out, workspace)
     with torch.cuda.device(x.device):

@@ -32,10 +32,11 @@ FLAGS = [
 
 
 # Sources compiled on their own with extra flags, then linked in.  The MQA
-# kernel consumes every MFMA result on the VALU at once, so it asks for the
-# MFMA form that writes VGPRs (no accumulator-register reads); the GEMM
-# kernels keep the default.
-SEPARATE = {"mqa_kernel.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+# kernel and the few-token kernels consume every MFMA result on the VALU at
+# once, so they ask for the MFMA form that writes VGPRs (no accumulator-register
+# reads); the GEMM kernels keep the default.
+_VGPR_MFMA = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+SEPARATE = {src: _VGPR_MFMA for src in ("mqa_kernel.hip", "tree_attn_kernel.hip", "moe_few_kernel.hip")}
 OBJ_DIR = os.path.join(HERE, "_build")
 
 

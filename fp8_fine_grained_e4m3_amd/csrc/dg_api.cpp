@@ -818,17 +818,19 @@ dg_status dg_fp8_tree_attention(const void* q, int64_t q_stride, const uint8_t* 
     return ok();
 }
 
-static const char* moe_few_sizes_wrong(int64_t T, int64_t topk, int64_t E, int64_t I) {
+static const char* moe_few_sizes_wrong(int64_t T, int64_t topk, int64_t E, int64_t H, int64_t I) {
     if (T < 0 || T > dg::kMoeMaxTokens) return "T must be from 0 to 256";
     if (topk < 1 || topk > dg::kMoeMaxTopk) return "topk must be from 1 to 16";
     if (E < 1 || E > dg::kMoeMaxExperts) return "E must be from 1 to 1024";
+    if (H < 128 || H % 128 != 0 || H > (1 << 17)) return "H must be a multiple of 128 up to 2^17";
     if (I < 128 || I % 128 != 0 || I > (1 << 17)) return "I must be a multiple of 128 up to 2^17";
     return "";
 }
 
-int64_t dg_fp8_moe_few_tokens_workspace_bytes(int64_t T, int64_t topk, int64_t E, int64_t I) {
-    if (*moe_few_sizes_wrong(T, topk, E, I) || T == 0) return 0;
-    return dg::moe_few_workspace_bytes(T, topk, E, I);
+int64_t dg_fp8_moe_few_tokens_workspace_bytes(int64_t T, int64_t topk, int64_t E, int64_t H,
+                                              int64_t I) {
+    if (*moe_few_sizes_wrong(T, topk, E, H, I) || T == 0) return 0;
+    return dg::moe_few_workspace_bytes(T, topk, E, H, I);
 }
 
 dg_status dg_fp8_moe_few_tokens(const void* x, const uint8_t* w1, const float* s1,
@@ -836,11 +838,9 @@ dg_status dg_fp8_moe_few_tokens(const void* x, const uint8_t* w1, const float* s
                                 const float* topk_weights, void* y, dg_dtype y_dtype, int64_t T,
                                 int64_t topk, int64_t E, int64_t H, int64_t I, void* workspace,
                                 int64_t workspace_bytes, void* stream) {
-    const char* wrong = moe_few_sizes_wrong(T, topk, E, I);
-    REQUIRE(!*wrong, "%s (T=%lld topk=%lld E=%lld I=%lld)", wrong, (long long)T, (long long)topk,
-            (long long)E, (long long)I);
-    REQUIRE(H >= 128 && H % 128 == 0 && H <= (1 << 17), "H=%lld must be a multiple of 128 up to 2^17",
-            (long long)H);
+    const char* wrong = moe_few_sizes_wrong(T, topk, E, H, I);
+    REQUIRE(!*wrong, "%s (T=%lld topk=%lld E=%lld H=%lld I=%lld)", wrong, (long long)T, (long long)topk,
+            (long long)E, (long long)H, (long long)I);
     REQUIRE(y_dtype == DG_BF16 || y_dtype == DG_F32, "y_dtype must be DG_BF16 or DG_F32");
     if (T == 0) return ok();
     REQUIRE_PTR(x, 16);
@@ -851,7 +851,7 @@ dg_status dg_fp8_moe_few_tokens(const void* x, const uint8_t* w1, const float* s
     REQUIRE_PTR(topk_ids, 16);
     REQUIRE_PTR(topk_weights, 16);
     REQUIRE_PTR(y, 16);
-    const int64_t need = dg::moe_few_workspace_bytes(T, topk, E, I);
+    const int64_t need = dg::moe_few_workspace_bytes(T, topk, E, H, I);
     REQUIRE(workspace != nullptr, "workspace is NULL: %lld bytes are needed "
             "(dg_fp8_moe_few_tokens_workspace_bytes)", (long long)need);
     REQUIRE_PTR(workspace, 16);

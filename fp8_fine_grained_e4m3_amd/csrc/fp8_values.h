@@ -46,4 +46,12 @@ __device__ __forceinline__ f32x4_t mfma_bf16(bf16x8_t rows, bf16x8_t cols, f32x4
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(rows, cols, acc, 0, 0, 0);
 }
 
+// Between a wave's LDS writes and reads of the same place by its other lanes:
+// the hardware keeps their order, this keeps the compiler from changing it.
+__device__ __forceinline__ void wave_lds_order() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 }  // namespace dg

@@ -35,13 +35,15 @@ namespace dg {
 namespace {
 
 constexpr int kBlk = 128;
-constexpr int kUpWaves = 4, kDownWaves = 8;
+constexpr int kUpWaves = 4, kDownWaves = 4;
+constexpr int kMaxShares = 8;           // XCDs
 constexpr int kTile = 16;               // rows and tokens of a matrix tile
 constexpr int kGroup = 64;              // tokens of a pass
 
-// Workspace: per reached expert its number, its token count and its list.
+// Workspace, for each group of kGroup tokens: the reached experts with the
+// tokens that they have there, `count` entries from `first` on, in token order.
 struct Reached {
-    int32_t expert, count;
+    int32_t expert, first, count;
 };
 struct Entry {
     int32_t pair;                       // t * topk + j: the row of h
@@ -59,128 +61,190 @@ struct MoeArgs {
     void* y;
     uint16_t* h;                        // [parts][T * topk][I]
     int32_t* reached_count;
-    Reached* reached;                   // [min(E, T * topk)]
-    Entry* entries;                     // [min(E, T * topk)][T]
-    int T, topk, E, H, I;
+    Reached* reached;                   // [groups][slots]
+    Entry* entries;                     // [T * topk]: a group's from group * kGroup * topk on
+    float* parts;                       // the second kernel's shares of y
+    int32_t* arrived;                   // [row tiles][groups]: shares done, zeroed by the first kernel
+    int T, topk, E, H, I, slots;        // slots: min(E, T * topk)
+    int shares, counters;
 };
 
-// The MFMA fragments of a 128-byte K block of a weight row: lane l loads bytes
-// [64 j + 16 g, + 16) of row l & 15, j = 0, 1; fragment 2 j + half takes eight
-// of them, so K value (j, half, g, i) is 64 j + 16 g + 8 half + i.
-struct WBlock {
-    u32x4_t w[2];
+// A half block, 64 K values, of NW tiles of 16 weight rows and of MT tiles of
+// 16 columns in a lane's registers.  Of a weight row l & 15 the lane holds bytes
+// [16 g, + 16), g = l >> 4, and fragment c takes eight of them, so its K value
+// (g, i) is 16 g + 8 c + i.  Columns are 128 bytes a half block: lane l fetches
+// 16 of them, number l & 7, of columns l >> 3 and 8 + (l >> 3), whole cache lines
+// an instruction, and the wave passes them through its own piece of LDS, chunk
+// c of column k at place c ^ (k & 7), to get its fragments.  (Fetching the
+// fragments themselves touches a line a lane; the L1 looks up about one line a
+// clock, and that held the layer at 3.5 TB/s.)
+template <int NW, int MT>
+struct Half {
+    u32x4_t w[NW];
+    u32x4_t x[MT][2];
 };
 
-__device__ __forceinline__ WBlock load_w(const uint8_t* p) {      // p: row + K block + 16 g
-    WBlock b;
-    b.w[0] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p));
-    b.w[1] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p + 64));
-    return b;
+__device__ __forceinline__ bf16x8_t w_frag(const u32x4_t& w, int c) {
+    return c ? e4m3x8_to_bf16x8(w.z, w.w) : e4m3x8_to_bf16x8(w.x, w.y);
 }
 
-__device__ __forceinline__ bf16x8_t w_frag(const WBlock& b, int c) {
-    const u32x4_t& w = b.w[c / 2];
-    return c % 2 ? e4m3x8_to_bf16x8(w.z, w.w) : e4m3x8_to_bf16x8(w.x, w.y);
-}
-
-struct XBlock {
-    u32x4_t x[4];
-};
-
-__device__ __forceinline__ XBlock load_x(const uint16_t* p, bool live) {   // p: row + K block + 16 g
-    XBlock b;
+// acc += scale * (weight block . column block) over the n 128-K blocks kb0,
+// kb0 + step, ...  w, s and cols are uniform; a lane's place in a weight tile is
+// w_off bytes on, its two in column tile t col[t] bytes.  DEPTH half blocks of weights and columns are in flight.
+// Loads retire in order, so both are fetched equally far ahead; none of the
+// main loop's loads is conditional, since a load that some path skips makes the
+// compiler wait for the ones behind it; and the loads stay where they are
+// written, since the scheduler gathers them at the loop's end otherwise.
+template <int NW, int NS, int MT, int DEPTH>
+__device__ __forceinline__ void products(const uint8_t* (&w)[NW], uint32_t w_off, const float* (&s)[NS],
+                                         const uint16_t* cols, const uint32_t (&col)[MT][2], u32x4_t* stage, int kb0,
+                                         int n, int step, int lane, f32x4_t (&acc)[NW][MT]) {
+    static_assert(DEPTH % 2 == 0, "a slot is always the same half");
+    const int put = lane ^ (lane >> 3);                                        // column l >> 3, chunk l & 7
+    const int get = (lane & 15) * 8 + ((2 * (lane >> 4)) ^ (lane & 7));        // column l & 15, chunk 2 g
+    for (int j0 = 0; j0 < n; j0 += 64) {
+        const int blocks = min(64, n - j0), halves = 2 * blocks;
+        float sv[NS];                              // lane j: the scale of the jth block
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        b.x[c] = u32x4_t{0, 0, 0, 0};
-        if (live) b.x[c] = *reinterpret_cast<const u32x4_t*>(p + 64 * (c / 2) + 8 * (c % 2));
-    }
-    return b;
-}
-
-// The K blocks of a wave, gate and up rows by MT token tiles.
-template <int MT>
-__device__ __forceinline__ void up_products(const MoeArgs& a, const uint8_t* (&w)[2], const float* (&s)[2],
-                                            const uint16_t* (&xr)[MT], const bool (&live)[MT], int wave,
-                                            f32x4_t (&acc)[2][MT]) {
-    const int KB = a.H / kBlk;
-    for (int kb = wave; kb < KB; kb += kUpWaves) {
-        WBlock wb[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) wb[r] = load_w(w[r] + (int64_t)kb * kBlk);
-        XBlock xb[MT];
-#pragma unroll
-        for (int t = 0; t < MT; ++t) xb[t] = load_x(xr[t] + kb * kBlk, live[t]);
-        f32x4_t p[2][MT];
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int t = 0; t < MT; ++t) p[r][t] = f32x4_t{0, 0, 0, 0};
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const bf16x8_t f = w_frag(wb[r], c);
-#pragma unroll
-                for (int t = 0; t < MT; ++t) p[r][t] = mfma_bf16(f, __builtin_bit_cast(bf16x8_t, xb[t].x[c]), p[r][t]);
-            }
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const float sc = s[r][kb];
+        for (int r = 0; r < NS; ++r) sv[r] = s[r][kb0 + (int64_t)(j0 + min(lane, blocks - 1)) * step];
+        Half<NW, MT> ring[DEPTH];
+        f32x4_t p[NW][MT];
+        auto load = [&](Half<NW, MT>& d, int i) {
+            const int64_t k = (kb0 + (int64_t)(j0 + i / 2) * step) * kBlk + (i & 1) * 64;
 #pragma unroll
             for (int t = 0; t < MT; ++t)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[r][t][i] = __builtin_fmaf(p[r][t][i], sc, acc[r][t][i]);
+                for (int c = 0; c < 2; ++c)
+                    d.x[t][c] = *reinterpret_cast<const u32x4_t*>(reinterpret_cast<const char*>(cols + k) + col[t][c]);
+#pragma unroll
+            for (int r = 0; r < NW; ++r) d.w[r] = *reinterpret_cast<const u32x4_t*>(w[r] + k + w_off);
+        };
+        auto use = [&](const Half<NW, MT>& d, int i, bool second) {
+            if (!second)
+#pragma unroll
+                for (int r = 0; r < NW; ++r)
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) p[r][t] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) stage[t * 128 + c * 64 + put] = d.x[t][c];
+            wave_lds_order();
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                bf16x8_t x[MT];
+#pragma unroll
+                for (int t = 0; t < MT; ++t) x[t] = __builtin_bit_cast(bf16x8_t, stage[t * 128 + (get ^ c)]);
+#pragma unroll
+                for (int r = 0; r < NW; ++r) {
+                    const bf16x8_t f = w_frag(d.w[r], c);
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) p[r][t] = mfma_bf16(f, x[t], p[r][t]);
+                }
+            }
+            wave_lds_order();
+            if (second)
+#pragma unroll
+                for (int r = 0; r < NW; ++r) {
+                    const float sc = __uint_as_float(
+                        (uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(sv[r / (NW / NS)]), i / 2));
+#pragma unroll
+                    for (int t = 0; t < MT; ++t)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) acc[r][t][k] = __builtin_fmaf(p[r][t][k], sc, acc[r][t][k]);
+                }
+        };
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) {
+            load(ring[d], min(d, halves - 1));
+            __builtin_amdgcn_sched_barrier(0);
         }
+        int i = 0;
+        for (; i + 2 * DEPTH <= halves; i += DEPTH)
+#pragma unroll
+            for (int d = 0; d < DEPTH; ++d) {
+                use(ring[d], i + d, d & 1);
+                __builtin_amdgcn_sched_barrier(0);
+                load(ring[d], i + d + DEPTH);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        // the last DEPTH to 2 DEPTH - 1 halves (or all, where there are fewer)
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d)
+            if (i + d < halves) {
+                use(ring[d], i + d, d & 1);
+                if (i + d + DEPTH < halves) load(ring[d], i + d + DEPTH);
+            }
+        i += DEPTH;
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d)
+            if (i + d < halves) use(ring[d], i + d, d & 1);
     }
 }
 
-template <int PARTS, int MT>
+// Tiles of weight rows a workgroup takes for up to MOST tiles of columns: with
+// more columns to fetch for a weight, more weights for a column, while the
+// registers hold them.
+template <int MOST>
+constexpr int kRowTiles = MOST == 2 ? 2 : 1;
+// Half blocks in flight, likewise.
+template <int NW, int MT>
+constexpr int kDepth = NW + 2 * MT <= 6 ? 4 : 2;
+
+// 16 * RT gate rows and the up rows beside them for the tokens list[first ...]
+// of an expert, MT tiles of them at most.
+template <int PARTS, int RT, int MT>
 __device__ __forceinline__ void up_pass(const MoeArgs& a, int e, int i0, int first, int count,
-                                        const Entry* list, float* sm, int wave, int lane) {
+                                        const int* list, float* sm, int wave, int lane) {
     const int r16 = lane & 15, g = lane >> 4;
-    const uint8_t* w[2];
+    const uint8_t* w[2 * RT];             // gate tiles, then up tiles
     const float* s[2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int row = i0 + r * a.I;
-        w[r] = a.w1 + ((int64_t)e * 2 * a.I + row + r16) * a.H + 16 * g;
-        s[r] = a.s1 + ((int64_t)e * (2 * a.I / kBlk) + row / kBlk) * (a.H / kBlk);
+    for (int r = 0; r < 2 * RT; ++r) {
+        const int row = i0 + (r % RT) * kTile + (r / RT) * a.I;
+        w[r] = a.w1 + ((int64_t)e * 2 * a.I + row) * a.H;
+        s[r / RT] = a.s1 + ((int64_t)e * (2 * a.I / kBlk) + row / kBlk) * (a.H / kBlk);
     }
-    const uint16_t* xr[MT];
-    bool live[MT];
+    // columns past the last token repeat the first one; their sums are not used
+    uint32_t xr[MT][2];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-        const int at = first + 16 * t + r16;
-        live[t] = at < count;
-        const int token = live[t] ? list[at].pair / a.topk : 0;
-        xr[t] = a.x + (int64_t)token * a.H + 16 * g;
-    }
-    f32x4_t acc[2][MT];
+    for (int t = 0; t < MT; ++t)
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+        for (int c = 0; c < 2; ++c) {
+            const int at = first + 16 * t + 8 * c + (lane >> 3);
+            xr[t][c] = 2u * ((uint32_t)(list[at < count ? at : first] / a.topk) * a.H + 8 * (lane & 7));
+        }
+    f32x4_t acc[2 * RT][MT];
+#pragma unroll
+    for (int r = 0; r < 2 * RT; ++r)
 #pragma unroll
         for (int t = 0; t < MT; ++t) acc[r][t] = f32x4_t{0, 0, 0, 0};
-    up_products<MT>(a, w, s, xr, live, wave, acc);
+    const int KB = a.H / kBlk;
+    u32x4_t* stage = reinterpret_cast<u32x4_t*>(sm) + wave * MT * 128;    // the sums come after
+    products<2 * RT, 2, MT, kDepth<2 * RT, MT>>(w, r16 * a.H + 16 * g, s, a.x, xr, stage, wave,
+                                       (KB - wave + kUpWaves - 1) / kUpWaves, kUpWaves, lane, acc);
 
-    // [wave][gate, up][token][16 rows]
+    __syncthreads();
+    // [wave][gate tiles, up tiles][token][16 rows]
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+    for (int r = 0; r < 2 * RT; ++r)
 #pragma unroll
         for (int t = 0; t < MT; ++t)
-            *reinterpret_cast<f32x4_t*>(sm + (((wave * 2 + r) * MT + t) * 16 + r16) * 16 + 4 * g) = acc[r][t];
+            *reinterpret_cast<f32x4_t*>(sm + (((wave * 2 * RT + r) * MT + t) * 16 + r16) * 16 + 4 * g) = acc[r][t];
     __syncthreads();
-    for (int i = threadIdx.x; i < MT * 256; i += kUpWaves * 64) {
-        const int tok = i / 16, row = i % 16;
+    for (int i = threadIdx.x; i < RT * MT * 256; i += kUpWaves * 64) {
+        const int tok = i / (16 * RT), row = i % (16 * RT);
         if (first + tok < count) {
             float v[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 v[r] = 0.0f;
 #pragma unroll
-                for (int k = 0; k < kUpWaves; ++k) v[r] += sm[((k * 2 + r) * MT * 16 + tok) * 16 + row];
+                for (int k = 0; k < kUpWaves; ++k)
+                    v[r] += sm[((k * 2 * RT + r * RT + row / 16) * MT * 16 + tok) * 16 + row % 16];
             }
             float rest = v[0] / (1.0f + __expf(-v[0])) * v[1];
-            uint16_t* dst = a.h + (int64_t)list[first + tok].pair * a.I + i0 + row;
+            uint16_t* dst = a.h + (int64_t)list[first + tok] * a.I + i0 + row;
 #pragma unroll
             for (int p = 0; p < PARTS; ++p) {
                 uint32_t bits = __float_as_uint(rest) & 0xFFFF0000u;
@@ -194,23 +258,33 @@ __device__ __forceinline__ void up_pass(const MoeArgs& a, int e, int i0, int fir
     __syncthreads();
 }
 
-template <int PARTS>
-__global__ __launch_bounds__(kUpWaves * 64) void moe_up_kernel(MoeArgs a) {
+template <int PARTS, int MOST>
+__global__ __launch_bounds__(kUpWaves * 64, 2) void moe_up_kernel(MoeArgs a) {
+    constexpr int RT = kRowTiles<MOST>;
     __shared__ uint32_t bitmap[kMoeMaxExperts / 32];
-    __shared__ Entry list[kMoeMaxTokens];
-    __shared__ float sm[kUpWaves * 2 * 4 * 256];
+    __shared__ int list[kMoeMaxTokens];               // the rows of h of its tokens
+    __shared__ __attribute__((aligned(16))) float sm[kUpWaves * 2 * RT * MOST * 256];   // >= the waves' stages
     __shared__ int found[2];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int tiles = a.I / kTile;
+    const int tiles = a.I / (kTile * RT);
     const int tile = blockIdx.x % tiles, nth = blockIdx.x / tiles;
     const int pairs = a.T * a.topk;
 
+    for (int64_t i = (int64_t)blockIdx.x * (kUpWaves * 64) + threadIdx.x; i < a.counters;
+         i += (int64_t)gridDim.x * (kUpWaves * 64))
+        a.arrived[i] = 0;
+
     // the nth of the experts that are reached
+    int* ids = reinterpret_cast<int*>(sm);            // until the sums need it
+    static_assert(kGroup == 64, "a wave has a group's tokens in its lanes");
+    static_assert(MOST == 1 || sizeof(sm) >= kMoeMaxTokens * kMoeMaxTopk * 4, "the ids fit");
+    static_assert(sizeof(sm) >= 16 * kMoeMaxTopk * 4, "those of 16 tokens fit");
     if (threadIdx.x < kMoeMaxExperts / 32) bitmap[threadIdx.x] = 0;
     __syncthreads();
     for (int p = threadIdx.x; p < pairs; p += kUpWaves * 64) {
         const int id = a.ids[p];
+        ids[p] = id;
         if (id >= 0 && id < a.E) atomicOr(&bitmap[id >> 5], 1u << (id & 31));
     }
     __syncthreads();
@@ -219,211 +293,392 @@ __global__ __launch_bounds__(kUpWaves * 64) void moe_up_kernel(MoeArgs a) {
         const int c = __builtin_popcount(word);
         int before = c;                               // inclusive prefix over the words
 #pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
+        for (int o = 1; o < kMoeMaxExperts / 32; o <<= 1) {
             const int v = __shfl_up(before, o);
             if (lane >= o) before += v;
         }
-        const int total = __builtin_amdgcn_readlane(before, 63);
+        const int total = __builtin_amdgcn_readlane(before, kMoeMaxExperts / 32 - 1);
         before -= c;
-        if (lane == 0) found[0] = -1;
-        if (nth >= before && nth < before + c) {
-            uint32_t w = word;
-            for (int i = before; i < nth; ++i) w &= w - 1;
-            found[0] = lane * 32 + __builtin_ctz(w);
+        const uint64_t holds = __ballot(nth >= before && nth < before + c);
+        int e = -1, count = 0;
+        if (holds != 0) {                             // uniform
+            const int at = __builtin_ctzll(holds);
+            uint32_t w = __builtin_amdgcn_readlane(word, at);
+            for (int i = __builtin_amdgcn_readlane(before, at); i < nth; ++i) w &= w - 1;
+            e = at * 32 + __builtin_ctz(w);
+            // its tokens: a token's first slot with it carries the weights of all of them
+            for (int t0 = 0; t0 < a.T; t0 += kGroup) {
+                const int t = min(t0 + lane, a.T - 1);
+                int first = -1, below = 0;
+                for (int j = a.topk - 1; j >= 0; --j) {
+                    const int id = ids[t * a.topk + j];
+                    if (id == e) first = t * a.topk + j;
+                    below += id >= 0 && id < e;
+                }
+                if (t0 + lane >= a.T) first = -1, below = 0;
+                const uint64_t have = __ballot(first >= 0);
+                const int n = __builtin_popcountll(have), i = __builtin_popcountll(have & ((1ull << lane) - 1));
+                if (first >= 0) list[count + i] = first;
+                if (tile == 0) {                      // for the second kernel
+                    // the group's slots of lower experts: room for all of their entries
+#pragma unroll
+                    for (int o = 32; o >= 1; o >>= 1) below += __shfl_xor(below, o);
+                    if (first >= 0) {
+                        float weight = 0.0f;
+                        for (int j = 0; j < a.topk; ++j)
+                            if (ids[t * a.topk + j] == e) weight += a.weights[t * a.topk + j];
+                        a.entries[t0 * a.topk + below + i] = Entry{first, weight};
+                    }
+                    if (lane == 0) a.reached[t0 / kGroup * a.slots + nth] = Reached{e, below, n};
+                }
+                count += n;
+            }
         }
-        if (blockIdx.x == 0 && lane == 0) *a.reached_count = total;
+        if (lane == 0) {
+            found[0] = e;
+            found[1] = count;
+            if (blockIdx.x == 0) *a.reached_count = total;
+        }
     }
     __syncthreads();
     const int e = found[0];
     if (e < 0) return;                                // uniform
-
-    // its tokens: a token's first slot with it carries the weights of all of them
-    if (wave == 0) {
-        int count = 0;
-        for (int t0 = 0; t0 < a.T; t0 += 64) {
-            const int t = t0 + lane;
-            int first = -1;
-            float weight = 0.0f;
-            if (t < a.T)
-                for (int j = 0; j < a.topk; ++j)
-                    if (a.ids[t * a.topk + j] == e) {
-                        if (first < 0) first = t * a.topk + j;
-                        weight += a.weights[t * a.topk + j];
-                    }
-            const uint64_t have = __ballot(first >= 0);
-            if (first >= 0) {
-                const int at = count + __builtin_popcountll(have & ((1ull << lane) - 1));
-                list[at] = Entry{first, weight};
-                if (tile == 0) a.entries[(int64_t)nth * a.T + at] = Entry{first, weight};
-            }
-            count += __builtin_popcountll(have);
-        }
-        if (lane == 0) {
-            found[1] = count;
-            if (tile == 0) a.reached[nth] = Reached{e, count};
-        }
-    }
-    __syncthreads();
-    const int count = found[1];
-    for (int first = 0; first < count; first += kGroup) {
+    const int count = found[1], i0 = tile * kTile * RT;
+    for (int first = 0; first < count; first += 16 * MOST) {
         const int left = count - first;
-        if (left <= 16) up_pass<PARTS, 1>(a, e, tile * kTile, first, count, list, sm, wave, lane);
-        else if (left <= 32) up_pass<PARTS, 2>(a, e, tile * kTile, first, count, list, sm, wave, lane);
-        else up_pass<PARTS, 4>(a, e, tile * kTile, first, count, list, sm, wave, lane);
+        if (MOST == 1 || left <= 16)
+            up_pass<PARTS, RT, 1>(a, e, i0, first, count, list, sm, wave, lane);
+        else if (MOST == 2 || left <= 32)
+            up_pass<PARTS, RT, MOST == 1 ? 1 : 2>(a, e, i0, first, count, list, sm, wave, lane);
+        else
+            up_pass<PARTS, RT, MOST>(a, e, i0, first, count, list, sm, wave, lane);
     }
 }
 
-// One expert's K blocks [kb0, kb1) for 16 rows of y and MT tiles of its tokens
-// from `first` on; the weighted product is added to the wave's slab.
-template <int PARTS, int MT>
-__device__ __forceinline__ void down_pass(const MoeArgs& a, int e, int n0, int kb0, int kb1, int first, int last,
-                                          const Entry* list, int token0, float* slab, int lane) {
-    const int r16 = lane & 15, g = lane >> 4;
-    const uint8_t* w = a.w2 + ((int64_t)e * a.H + n0 + r16) * a.I + 16 * g;
-    const float* s = a.s2 + ((int64_t)e * (a.H / kBlk) + n0 / kBlk) * (a.I / kBlk);
-    const int64_t part = (int64_t)a.T * a.topk * a.I;
-    const uint16_t* hr[MT];
-    bool live[MT];
-    int token[MT];
-    float weight[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) {
-        const int at = first + 16 * t + r16;
-        live[t] = at < last;
-        Entry en{0, 0.0f};
-        if (live[t]) en = list[at];
-        hr[t] = a.h + (int64_t)en.pair * a.I + 16 * g;
-        token[t] = en.pair / a.topk - token0;
-        weight[t] = en.weight;
-    }
-    f32x4_t acc[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) acc[t] = f32x4_t{0, 0, 0, 0};
-    for (int kb = kb0; kb < kb1; ++kb) {
-        const WBlock wb = load_w(w + (int64_t)kb * kBlk);
-        XBlock hb[PARTS][MT];
-#pragma unroll
-        for (int p = 0; p < PARTS; ++p)
-#pragma unroll
-            for (int t = 0; t < MT; ++t) hb[p][t] = load_x(hr[t] + p * part + kb * kBlk, live[t]);
-        f32x4_t q[MT];
-#pragma unroll
-        for (int t = 0; t < MT; ++t) q[t] = f32x4_t{0, 0, 0, 0};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const bf16x8_t f = w_frag(wb, c);
-#pragma unroll
-            for (int p = PARTS - 1; p >= 0; --p)
-#pragma unroll
-                for (int t = 0; t < MT; ++t) q[t] = mfma_bf16(f, __builtin_bit_cast(bf16x8_t, hb[p][t].x[c]), q[t]);
-        }
-        const float sc = s[kb];
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[t][i] = __builtin_fmaf(q[t][i], sc, acc[t][i]);
-    }
-    // a token is in an expert's list once: no two lanes of a tile meet
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-        if (live[t]) {
-            f32x4_t* at = reinterpret_cast<f32x4_t*>(slab + token[t] * kTile + 4 * g);
-            *at += acc[t] * weight[t];
-        }
-}
+// Tokens whose parts fit MOST column tiles, and the tokens of a workgroup.
+template <int PARTS, int MOST>
+constexpr int kPass = 16 * MOST / PARTS;
+template <int MOST>
+constexpr int kDownTokens = MOST == 1 ? 16 : kGroup;
 
-template <int PARTS>
+// 16 * RT rows of y for the workgroup's tokens.  The work is a list of passes,
+// an expert and up to kPass of its tokens each, of I / 128 K blocks; the waves
+// take equal runs of the list's blocks.  A pass's columns are its tokens' first
+// parts, then their second ones, ...  A wave's loads run DEPTH half blocks ahead
+// of its products and over the ends of passes, so HBM's latency is met once.
+template <int PARTS, int MOST>
 __global__ __launch_bounds__(kDownWaves * 64) void moe_down_kernel(MoeArgs a) {
-    __shared__ float slabs[kDownWaves][kGroup * kTile];
-    const int lane = threadIdx.x & 63;
+    constexpr int RT = kRowTiles<MOST>, ROWS = RT * kTile, MT = MOST, DEPTH = kDepth<RT, MT>;
+    constexpr int TOKENS = kDownTokens<MOST>, PASS = kPass<PARTS, MOST>;
+    struct Pass {
+        int expert;
+        int first, tokens;                             // in `entries`
+    };
+    __shared__ __attribute__((aligned(16))) float slabs[kDownWaves][TOKENS * ROWS];
+    __shared__ u32x4_t stages[kDownWaves][MT * 128];
+    __shared__ Entry entries[TOKENS * kMoeMaxTopk];
+    __shared__ Pass passes[TOKENS * kMoeMaxTopk];
+    __shared__ int totals[kDownWaves];
+    const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n0 = blockIdx.x * kTile, token0 = blockIdx.y * kGroup;
-    const int tokens = min(a.T - token0, kGroup);
+    const int z = blockIdx.x % a.shares, tile = blockIdx.x / a.shares;
+    const int n0 = tile * ROWS, token0 = blockIdx.y * TOKENS;
+    const int tokens = min(a.T - token0, TOKENS);
     float* slab = slabs[wave];
-    for (int i = lane; i < kGroup * kTile; i += 64) slab[i] = 0.0f;
+    for (int i = lane; i < TOKENS * ROWS; i += 64) slab[i] = 0.0f;
+
+    // the list of passes: a thread an expert, its place by a prefix sum
+    for (int i = threadIdx.x; i < tokens * a.topk; i += kDownWaves * 64) entries[i] = a.entries[token0 * a.topk + i];
+    int pass_count = 0;
+    const int reached = *a.reached_count;
+    for (int base = 0; base < reached; base += kDownWaves * 64) {
+        const int nth = base + (int)threadIdx.x;
+        Reached r{0, 0, 0};
+        if (nth < reached) r = a.reached[blockIdx.y * a.slots + nth];
+        const int n = (r.count + PASS - 1) / PASS;
+        int before = n;                                // inclusive prefix in the wave
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int v = __shfl_up(before, o);
+            if (lane >= o) before += v;
+        }
+        if (lane == 63) totals[wave] = before;
+        __syncthreads();
+        int at = pass_count + before - n;
+#pragma unroll
+        for (int w = 0; w < kDownWaves; ++w) {
+            if (w < wave) at += totals[w];
+            pass_count += totals[w];
+        }
+        for (int i = 0; i < n; ++i) passes[at + i] = Pass{r.expert, r.first + i * PASS, min(PASS, r.count - i * PASS)};
+        __syncthreads();
+    }
 
     const int KB = a.I / kBlk;
-    const int64_t blocks = (int64_t)*a.reached_count * KB;
-    const int64_t u0 = blocks * wave / kDownWaves, u1 = blocks * (wave + 1) / kDownWaves;
-    for (int64_t u = u0; u < u1;) {
-        const int nth = (int)(u / KB), kb0 = (int)(u - (int64_t)nth * KB);
-        const int kb1 = (int)min((int64_t)KB, kb0 + (u1 - u));
-        const int e = a.reached[nth].expert, count = a.reached[nth].count;
-        const Entry* list = a.entries + (int64_t)nth * a.T;
-        // the list is in order of tokens: this workgroup's are a run of it
-        int first = 0, last = count;
-        if (gridDim.y > 1) {
-            int before = 0, within = 0;
-            for (int i = lane; i < count; i += 64) {
-                const int t = list[i].pair / a.topk;
-                before += t < token0;
-                within += t < token0 + kGroup;
-            }
+    const int64_t blocks = (int64_t)pass_count * KB;
+    const int share = z * kDownWaves + wave, all = a.shares * kDownWaves;
+    const int64_t u0 = blocks * share / all;
+    const int halves = 2 * (int)(blocks * (share + 1) / all - u0);
+    const uint32_t w_off = r16 * a.I + 16 * g;
+    u32x4_t* stage = stages[wave];
+    const int put = lane ^ (lane >> 3), get = (lane & 15) * 8 + ((2 * (lane >> 4)) ^ (lane & 7));
+    if (halves > 0) {
+        // the loads' place
+        int lp = (int)(u0 / KB), lk = (int)(u0 - (int64_t)lp * KB);
+        const uint8_t* w;
+        const float* s;
+        uint32_t col[MT][2];
+        auto aim = [&]() {
+            const int e = __builtin_amdgcn_readfirstlane(passes[lp].expert);
+            const int first = passes[lp].first, n = passes[lp].tokens;
+            w = a.w2 + ((int64_t)e * a.H + n0) * a.I;
+            s = a.s2 + ((int64_t)e * (a.H / kBlk) + n0 / kBlk) * KB;
 #pragma unroll
-            for (int o = 32; o >= 1; o >>= 1) {
-                before += __shfl_xor(before, o);
-                within += __shfl_xor(within, o);
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    // columns past the last repeat the first one; their sums are not used
+                    const int c = 16 * t + 8 * i + (lane >> 3), p = c / n;
+                    const int pair = entries[first + (p < PARTS ? c - p * n : 0)].pair;
+                    col[t][i] = 2u * (((uint32_t)(p < PARTS ? p : 0) * a.T * a.topk + pair) * (uint32_t)a.I +
+                                      8 * (lane & 7));
+                }
+        };
+        Half<RT, MT> ring[DEPTH];
+        float scale[DEPTH / 2];
+        auto load = [&](int d) {
+            const int k = lk * kBlk + (d & 1) * 64;
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    ring[d].x[t][c] = *reinterpret_cast<const u32x4_t*>(reinterpret_cast<const char*>(a.h + k) + col[t][c]);
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+                ring[d].w[r] = *reinterpret_cast<const u32x4_t*>(w + (int64_t)r * kTile * a.I + k + w_off);
+            if (d & 1) {
+                scale[d / 2] = s[lk];
+                // past the last block the last one again
+                if (lk + 1 < KB) ++lk;
+                else if (lp + 1 < pass_count) {
+                    ++lp;
+                    lk = 0;
+                    aim();
+                }
             }
-            first = __builtin_amdgcn_readfirstlane(before);
-            last = __builtin_amdgcn_readfirstlane(within);
+        };
+        // the products' place
+        int up = lp, uk = lk;
+        f32x4_t acc[RT][MT], p[RT][MT];
+        auto clear = [&](f32x4_t (&v)[RT][MT]) {
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int t = 0; t < MT; ++t) v[r][t] = f32x4_t{0, 0, 0, 0};
+        };
+        // the weighted sums to the slab; a token is in an expert's list once, so no
+        // two lanes of a part meet
+        auto flush = [&]() {
+            const int first = passes[up].first, n = passes[up].tokens;
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                const int c = 16 * t + r16, part = c / n;
+                const Entry en = entries[first + (part < PARTS ? c - part * n : 0)];
+                float* at = slab + (en.pair / a.topk - token0) * ROWS + 4 * g;
+#pragma unroll
+                for (int q = 0; q < PARTS; ++q) {
+                    if (part == q)
+#pragma unroll
+                        for (int r = 0; r < RT; ++r)
+                            *reinterpret_cast<f32x4_t*>(at + r * kTile) += acc[r][t] * en.weight;
+                    wave_lds_order();
+                }
+            }
+        };
+        aim();
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) {
+            load(d);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        // three parts of four tiles would not fit the registers
-        for (constexpr int MOST = PARTS == 3 ? 2 : 4; first < last; first += 16 * MOST) {
-            const int n = last - first;
-            if (MOST == 4 && n > 32) down_pass<PARTS, MOST>(a, e, n0, kb0, kb1, first, last, list, token0, slab, lane);
-            else if (n > 16) down_pass<PARTS, 2>(a, e, n0, kb0, kb1, first, last, list, token0, slab, lane);
-            else down_pass<PARTS, 1>(a, e, n0, kb0, kb1, first, last, list, token0, slab, lane);
-        }
-        u += kb1 - kb0;
+        clear(acc);
+        for (int i = 0; i < halves; i += DEPTH)
+#pragma unroll
+            for (int d = 0; d < DEPTH; ++d) {
+                if (i + d < halves) {
+                    if (d % 2 == 0) clear(p);
+#pragma unroll
+                    for (int t = 0; t < MT; ++t)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) stage[t * 128 + c * 64 + put] = ring[d].x[t][c];
+                    wave_lds_order();
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        bf16x8_t x[MT];
+#pragma unroll
+                        for (int t = 0; t < MT; ++t) x[t] = __builtin_bit_cast(bf16x8_t, stage[t * 128 + (get ^ c)]);
+#pragma unroll
+                        for (int r = 0; r < RT; ++r) {
+                            const bf16x8_t f = w_frag(ring[d].w[r], c);
+#pragma unroll
+                            for (int t = 0; t < MT; ++t) p[r][t] = mfma_bf16(f, x[t], p[r][t]);
+                        }
+                    }
+                    wave_lds_order();
+                    if (d % 2 == 1) {
+                        const float sc = scale[d / 2];
+#pragma unroll
+                        for (int r = 0; r < RT; ++r)
+#pragma unroll
+                            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) acc[r][t][k] = __builtin_fmaf(p[r][t][k], sc, acc[r][t][k]);
+                        ++uk;
+                        if (uk == KB || i + d + 1 == halves) {
+                            flush();
+                            clear(acc);
+                            uk = 0;
+                            ++up;
+                        }
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                load(d);
+                __builtin_amdgcn_sched_barrier(0);
+            }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < tokens * kTile; i += kDownWaves * 64) {
-        float v = 0.0f;
+    // two values a thread: the waves' slabs in order, then the shares in order
+    auto put_y = [&](int i, float v0, float v1) {
+        const int64_t at = (int64_t)(token0 + 2 * i / ROWS) * a.H + n0 + 2 * i % ROWS;
+        if constexpr (PARTS == 3) *reinterpret_cast<f32x2_t*>(static_cast<float*>(a.y) + at) = f32x2_t{v0, v1};
+        else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.y) + at) = f32x2_to_bf16x2(v0, v1);
+    };
+    // [tile][group][share][token][rows]
+    const int64_t home = ((int64_t)tile * gridDim.y + blockIdx.y) * a.shares;
+    uint64_t* parts = reinterpret_cast<uint64_t*>(a.parts + home * (TOKENS * ROWS));
+    for (int i = threadIdx.x; i < tokens * ROWS / 2; i += kDownWaves * 64) {
+        f32x2_t v = {0.0f, 0.0f};
 #pragma unroll
-        for (int k = 0; k < kDownWaves; ++k) v += slabs[k][i];
-        const int64_t at = (int64_t)(token0 + i / kTile) * a.H + n0 + i % kTile;
-        if constexpr (PARTS == 3) static_cast<float*>(a.y)[at] = v;
-        else static_cast<__bf16*>(a.y)[at] = (__bf16)v;
+        for (int k = 0; k < kDownWaves; ++k) v += *reinterpret_cast<const f32x2_t*>(slabs[k] + 2 * i);
+        if (a.shares == 1) put_y(i, v.x, v.y);
+        else
+            __hip_atomic_store(parts + z * (TOKENS * ROWS / 2) + i, __builtin_bit_cast(uint64_t, v), __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
+    }
+    if (a.shares == 1) return;
+    // The share that arrives last adds them up.  Its count is taken after every
+    // wave's device-coherent stores have completed, and the parts are read with
+    // device-coherent loads after it (the GEMMs' split-K order).
+    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+    int* arrived = a.arrived + tile * gridDim.y + blockIdx.y;
+    if (threadIdx.x == 0)
+        totals[0] = __hip_atomic_fetch_add(arrived, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (totals[0] != a.shares - 1) return;
+    for (int i = threadIdx.x; i < tokens * ROWS / 2; i += kDownWaves * 64) {
+        uint64_t part[kMaxShares];
+#pragma unroll
+        for (int k = 0; k < kMaxShares; ++k)
+            part[k] = __hip_atomic_load(parts + min(k, a.shares - 1) * (TOKENS * ROWS / 2) + i, __ATOMIC_RELAXED,
+                                        __HIP_MEMORY_SCOPE_AGENT);
+        f32x2_t v = {0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < kMaxShares; ++k)
+            if (k < a.shares) v += __builtin_bit_cast(f32x2_t, part[k]);
+        put_y(i, v.x, v.y);
     }
 }
 
-template <int PARTS>
-hipError_t launch(const MoeArgs& a, int slots, hipStream_t stream) {
-    hipLaunchKernelGGL((moe_up_kernel<PARTS>), dim3((unsigned)((int64_t)slots * (a.I / kTile))),
-                       dim3(kUpWaves * 64), 0, stream, a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((moe_down_kernel<PARTS>),
-                       dim3((unsigned)(a.H / kTile), (unsigned)((a.T + kGroup - 1) / kGroup)),
+template <int PARTS, int MOST>
+hipError_t launch_up(const MoeArgs& a, hipStream_t stream) {
+    hipLaunchKernelGGL((moe_up_kernel<PARTS, MOST>),
+                       dim3((unsigned)((int64_t)a.slots * (a.I / (kRowTiles<MOST> * kTile)))), dim3(kUpWaves * 64), 0,
+                       stream, a);
+    return hipGetLastError();
+}
+
+template <int PARTS, int MOST>
+hipError_t launch_down(const MoeArgs& a, hipStream_t stream) {
+    constexpr int TOKENS = kDownTokens<MOST>;
+    hipLaunchKernelGGL((moe_down_kernel<PARTS, MOST>),
+                       dim3((unsigned)(a.H / (kRowTiles<MOST> * kTile) * a.shares), (unsigned)((a.T + TOKENS - 1) / TOKENS)),
                        dim3(kDownWaves * 64), 0, stream, a);
     return hipGetLastError();
 }
 
+// Column tiles of a pass: one where no expert can have more, two where an
+// expert has 12 columns or fewer on average (most of them then fit one), four
+// else.  A pass more reads the weights again, from the caches.
+int up_tiles(int64_t T, int64_t topk, int64_t E) {
+    return T <= 16 ? 1 : T <= 32 || T * topk <= 12 * E ? 2 : 4;
+}
+
+int down_tiles(int64_t T, int64_t topk, int64_t E, int parts) {
+    return T * parts <= 16 ? 1 : T * parts <= 32 || T * topk * parts <= 24 * E ? 2 : 4;
+}
+
+// Workgroups that share a tile's passes: eight, one an XCD, whose second-level
+// cache then meets an eighth of the hidden values, while a wave has two blocks.
+int down_shares(int64_t T, int64_t topk, int64_t E, int64_t I) {
+    const int64_t blocks = std::min(E, T * topk) * (I / kBlk);
+    return (int)std::max<int64_t>(1, std::min<int64_t>(kMaxShares, blocks / (2 * kDownWaves)));
+}
+
 constexpr int64_t align16(int64_t n) { return (n + 15) / 16 * 16; }
+
+// The workspace's pieces, laid out at `base` (sizes alone where it is NULL).
+int64_t lay_out(MoeArgs& a, int parts, char* base) {
+    const int64_t T = a.T, groups = (T + kGroup - 1) / kGroup, pairs = T * a.topk;
+    a.slots = std::min(a.E, a.T * a.topk);
+    a.shares = down_shares(T, a.topk, a.E, a.I);
+    const int most = down_tiles(T, a.topk, a.E, parts), rows = kTile * (most == 2 ? 2 : 1);
+    a.counters = (int)(a.H / rows * groups);
+    int64_t n = 0;
+    auto piece = [&](int64_t bytes) {
+        char* at = base + n;
+        n += align16(bytes);
+        return at;
+    };
+    a.reached_count = reinterpret_cast<int32_t*>(piece(4));
+    a.reached = reinterpret_cast<Reached*>(piece(groups * a.slots * (int64_t)sizeof(Reached)));
+    a.entries = reinterpret_cast<Entry*>(piece(pairs * (int64_t)sizeof(Entry)));
+    a.arrived = reinterpret_cast<int32_t*>(piece(4ll * a.counters));
+    a.h = reinterpret_cast<uint16_t*>(piece(parts * pairs * a.I * 2));
+    a.parts = reinterpret_cast<float*>(
+        piece(a.shares == 1 ? 0 : 4ll * a.shares * groups * (most == 1 ? 16 : kGroup) * a.H));
+    return n;
+}
+
+template <int PARTS>
+hipError_t launch(const MoeArgs& a, hipStream_t stream) {
+    hipError_t e;
+    const int up = up_tiles(a.T, a.topk, a.E);
+    if (up == 1) e = launch_up<PARTS, 1>(a, stream);
+    else if (up == 2) e = launch_up<PARTS, 2>(a, stream);
+    else e = launch_up<PARTS, 4>(a, stream);
+    if (e != hipSuccess) return e;
+    const int down = down_tiles(a.T, a.topk, a.E, PARTS);
+    if (down == 1) return launch_down<PARTS, 1>(a, stream);
+    if (down == 2) return launch_down<PARTS, 2>(a, stream);
+    return launch_down<PARTS, 4>(a, stream);
+}
 
 }  // namespace
 
-int64_t moe_few_workspace_bytes(int64_t T, int64_t topk, int64_t E, int64_t I) {
-    const int64_t slots = std::min(E, T * topk);
-    return 16 + align16(slots * (int64_t)sizeof(Reached)) + align16(slots * T * (int64_t)sizeof(Entry)) +
-           3 * T * topk * I * 2;
+int64_t moe_few_workspace_bytes(int64_t T, int64_t topk, int64_t E, int64_t H, int64_t I) {
+    MoeArgs a{};
+    a.T = (int)T; a.topk = (int)topk; a.E = (int)E; a.H = (int)H; a.I = (int)I;
+    return std::max(lay_out(a, 2, nullptr), lay_out(a, 3, nullptr));
 }
 
 hipError_t launch_moe_few(const MoeFewProblem& p, hipStream_t stream) {
-    MoeArgs a;
+    MoeArgs a{};
     a.x = p.x; a.w1 = p.w1; a.s1 = p.s1; a.w2 = p.w2; a.s2 = p.s2;
     a.ids = p.ids; a.weights = p.weights; a.y = p.y;
     a.T = (int)p.T; a.topk = (int)p.topk; a.E = (int)p.E; a.H = (int)p.H; a.I = (int)p.I;
-    const int slots = std::min(a.E, a.T * a.topk);
-    char* at = static_cast<char*>(p.workspace);
-    a.reached_count = reinterpret_cast<int32_t*>(at);
-    at += 16;
-    a.reached = reinterpret_cast<Reached*>(at);
-    at += align16(slots * (int64_t)sizeof(Reached));
-    a.entries = reinterpret_cast<Entry*>(at);
-    at += align16((int64_t)slots * a.T * (int64_t)sizeof(Entry));
-    a.h = reinterpret_cast<uint16_t*>(at);
-    return p.out_f32 ? launch<3>(a, slots, stream) : launch<2>(a, slots, stream);
+    lay_out(a, p.out_f32 ? 3 : 2, static_cast<char*>(p.workspace));
+    return p.out_f32 ? launch<3>(a, stream) : launch<2>(a, stream);
 }
 
 }  // namespace dg

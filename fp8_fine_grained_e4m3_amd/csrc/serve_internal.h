@@ -68,7 +68,7 @@ struct MoeFewProblem {
     int64_t T, topk, E, H, I;
     void* workspace;
 };
-int64_t moe_few_workspace_bytes(int64_t T, int64_t topk, int64_t E, int64_t I);
+int64_t moe_few_workspace_bytes(int64_t T, int64_t topk, int64_t E, int64_t H, int64_t I);
 hipError_t launch_moe_few(const MoeFewProblem& p, hipStream_t stream);
 
 }  // namespace dg

@@ -543,7 +543,7 @@ int64_t dg_fp8_tree_attention_workspace_bytes(int64_t B, int64_t N, int64_t Hq, 
  *   y            [T, H]       DG_BF16 (rounded once) or DG_F32
  * Rules: T <= 256, 1 <= topk <= 16, 1 <= E <= 1024, H and I multiples of 128 up
  * to 2^17.
- * workspace: dg_fp8_moe_few_tokens_workspace_bytes(T, topk, E, I), never
+ * workspace: dg_fp8_moe_few_tokens_workspace_bytes(T, topk, E, H, I), never
  * initialised, not shared by calls that may overlap.  Two kernel launches.
  */
 dg_status dg_fp8_moe_few_tokens(const void* x, const uint8_t* w1, const float* s1,
@@ -552,7 +552,8 @@ dg_status dg_fp8_moe_few_tokens(const void* x, const uint8_t* w1, const float* s
                                 int64_t T, int64_t topk, int64_t E, int64_t H, int64_t I,
                                 void* workspace, int64_t workspace_bytes, void* stream);
 /* A function of the sizes alone (no HIP call); 0 for sizes that are rejected. */
-int64_t dg_fp8_moe_few_tokens_workspace_bytes(int64_t T, int64_t topk, int64_t E, int64_t I);
+int64_t dg_fp8_moe_few_tokens_workspace_bytes(int64_t T, int64_t topk, int64_t E, int64_t H,
+                                              int64_t I);
 
 /* Message for the last non-OK status returned on this thread ("" if none). */
 const char* dg_last_error(void);
