@@ -30,6 +30,7 @@
 #include "serve_internal.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace dg {
 namespace {
@@ -69,116 +70,173 @@ struct MoeArgs {
     int shares, counters;
 };
 
-// A half block, 64 K values, of NW tiles of 16 weight rows and of MT tiles of
-// 16 columns in a lane's registers.  Of a weight row l & 15 the lane holds bytes
-// [16 g, + 16), g = l >> 4, and fragment c takes eight of them, so its K value
-// (g, i) is 16 g + 8 c + i.  Columns are 128 bytes a half block: lane l fetches
-// 16 of them, number l & 7, of columns l >> 3 and 8 + (l >> 3), whole cache lines
-// an instruction, and the wave passes them through its own piece of LDS, chunk
-// c of column k at place c ^ (k & 7), to get its fragments.  (Fetching the
-// fragments themselves touches a line a lane; the L1 looks up about one line a
-// clock, and that held the layer at 3.5 TB/s.)
+// A 128-K block of NW tiles of 16 weight rows and of MT tiles of 16 columns on
+// its way from memory to the matrix unit.  A weight row's block is one cache
+// line, a column's two (a half of 64 K values each).  Lane l fetches 16 bytes,
+// number l & 7, of lines l >> 3 and 8 + (l >> 3) of a tile, so an instruction
+// asks for 8 whole lines; the wave passes them through its own piece of LDS,
+// chunk c of line k at place c ^ (k & 7), to get the matrix operands.  (Fetching
+// operands straight from memory, 16 rows of 64 bytes an instruction, asks the
+// L1 for a line a lane, of which it looks up about one a clock, and fetches a
+// line's halves apart: 4.9 TB/s in a plain read, against 6.2.)
+// Operand lane l: bytes [16 g, + 16) of half h of row l & 15, g = l >> 4; fragment
+// c takes eight of them, so its K value (g, i) is 64 h + 16 g + 8 c + i.
 template <int NW, int MT>
-struct Half {
-    u32x4_t w[NW];
-    u32x4_t x[MT][2];
+struct Block {
+    static constexpr int STAGE = (NW + MT) * 128;      // 16-byte chunks of LDS a wave
+    u32x4_t w[NW][2];
+    u32x4_t x[2][MT][2];
+
+    // at(r, i): the lane's place in lines i of weight tile r
+    template <typename F>
+    __device__ __forceinline__ void load_w(F at) {
+#pragma unroll
+        for (int r = 0; r < NW; ++r)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) w[r][i] = *reinterpret_cast<const u32x4_t*>(at(r, i));
+    }
+
+    // at(t, i): the lane's place in columns i of tile t, first half
+    template <typename F>
+    __device__ __forceinline__ void load_x(F at) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) x[h][t][i] = *reinterpret_cast<const u32x4_t*>(at(t, i) + 128 * h);
+    }
+
+    // p = weights . columns; next_w and next_x fetch the next block into this one
+    // as soon as its registers are free.
+    template <typename F, typename G>
+    __device__ __forceinline__ void multiply(u32x4_t* stage, int lane, f32x4_t (&p)[NW][MT], F next_w, G next_x) {
+        u32x4_t* xs = stage + NW * 128;
+        const int put = lane ^ (lane >> 3);                                  // line l >> 3, chunk l & 7
+        const int row = (lane & 15) * 8, g = lane >> 4, turn = lane & 7;     // line l & 15
+#pragma unroll
+        for (int r = 0; r < NW; ++r)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) stage[r * 128 + i * 64 + put] = w[r][i];
+        __builtin_amdgcn_sched_barrier(0);
+        next_w();
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int r = 0; r < NW; ++r)
+#pragma unroll
+            for (int t = 0; t < MT; ++t) p[r][t] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) xs[t * 128 + i * 64 + put] = x[h][t][i];
+            if (h == 1) {
+                __builtin_amdgcn_sched_barrier(0);
+                next_x();
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            wave_lds_order();
+            u32x4_t v[NW];
+#pragma unroll
+            for (int r = 0; r < NW; ++r) v[r] = stage[r * 128 + row + ((4 * h + g) ^ turn)];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                bf16x8_t f[MT];
+#pragma unroll
+                for (int t = 0; t < MT; ++t) f[t] = __builtin_bit_cast(bf16x8_t, xs[t * 128 + row + ((2 * g + c) ^ turn)]);
+#pragma unroll
+                for (int r = 0; r < NW; ++r) {
+                    const bf16x8_t a = c ? e4m3x8_to_bf16x8(v[r].z, v[r].w) : e4m3x8_to_bf16x8(v[r].x, v[r].y);
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) p[r][t] = mfma_bf16(a, f[t], p[r][t]);
+                }
+            }
+            wave_lds_order();
+        }
+    }
 };
 
-__device__ __forceinline__ bf16x8_t w_frag(const u32x4_t& w, int c) {
-    return c ? e4m3x8_to_bf16x8(w.z, w.w) : e4m3x8_to_bf16x8(w.x, w.y);
+template <int NW, int MT>
+__device__ __forceinline__ void clear(f32x4_t (&v)[NW][MT]) {
+#pragma unroll
+    for (int r = 0; r < NW; ++r)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) v[r][t] = f32x4_t{0, 0, 0, 0};
+}
+
+// acc += scale * p
+template <int MT>
+__device__ __forceinline__ void promote(const f32x4_t (&p)[MT], float scale, f32x4_t (&acc)[MT]) {
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[t][k] = __builtin_fmaf(p[t][k], scale, acc[t][k]);
+}
+
+// Blocks in flight.  Loads retire in order, so weights and columns are fetched
+// equally far ahead; none of the main loops' loads is conditional, since a load
+// that some path skips makes the compiler wait for the ones behind it; and they
+// stay where they are written, since the scheduler gathers them at the loop's
+// end otherwise.
+constexpr int kDepth = 1;
+
+// Runs step(slot, block, whether to fetch block + kDepth into the slot) for
+// blocks 0 ... count - 1.
+template <typename F>
+__device__ __forceinline__ void in_flight(int count, F step) {
+    int i = 0;
+    for (; i + 2 * kDepth <= count; i += kDepth)
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d) step(d, i + d, std::true_type{});
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+        if (i + d + kDepth < count) step(d, i + d, std::true_type{});
+        else if (i + d < count) step(d, i + d, std::false_type{});
+    }
+    i += kDepth;
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d)
+        if (i + d < count) step(d, i + d, std::false_type{});
 }
 
 // acc += scale * (weight block . column block) over the n 128-K blocks kb0,
-// kb0 + step, ...  w, s and cols are uniform; a lane's place in a weight tile is
-// w_off bytes on, its two in column tile t col[t] bytes.  DEPTH half blocks of weights and columns are in flight.
-// Loads retire in order, so both are fetched equally far ahead; none of the
-// main loop's loads is conditional, since a load that some path skips makes the
-// compiler wait for the ones behind it; and the loads stay where they are
-// written, since the scheduler gathers them at the loop's end otherwise.
-template <int NW, int NS, int MT, int DEPTH>
-__device__ __forceinline__ void products(const uint8_t* (&w)[NW], uint32_t w_off, const float* (&s)[NS],
-                                         const uint16_t* cols, const uint32_t (&col)[MT][2], u32x4_t* stage, int kb0,
-                                         int n, int step, int lane, f32x4_t (&acc)[NW][MT]) {
-    static_assert(DEPTH % 2 == 0, "a slot is always the same half");
-    const int put = lane ^ (lane >> 3);                                        // column l >> 3, chunk l & 7
-    const int get = (lane & 15) * 8 + ((2 * (lane >> 4)) ^ (lane & 7));        // column l & 15, chunk 2 g
+// kb0 + step, ...  w, s and cols are uniform; a lane's places in a weight tile are
+// w_off and w_off + w_next bytes on, its two in column tile t col[t] bytes.
+template <int NW, int NS, int MT>
+__device__ __forceinline__ void products(const uint8_t* (&w)[NW], uint32_t w_off, uint32_t w_next,
+                                         const float* (&s)[NS], const uint16_t* cols, const uint32_t (&col)[MT][2],
+                                         u32x4_t* stage, int kb0, int n, int step, int lane, f32x4_t (&acc)[NW][MT]) {
     for (int j0 = 0; j0 < n; j0 += 64) {
-        const int blocks = min(64, n - j0), halves = 2 * blocks;
+        const int blocks = min(64, n - j0);
         float sv[NS];                              // lane j: the scale of the jth block
 #pragma unroll
         for (int r = 0; r < NS; ++r) sv[r] = s[r][kb0 + (int64_t)(j0 + min(lane, blocks - 1)) * step];
-        Half<NW, MT> ring[DEPTH];
-        f32x4_t p[NW][MT];
-        auto load = [&](Half<NW, MT>& d, int i) {
-            const int64_t k = (kb0 + (int64_t)(j0 + i / 2) * step) * kBlk + (i & 1) * 64;
-#pragma unroll
-            for (int t = 0; t < MT; ++t)
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    d.x[t][c] = *reinterpret_cast<const u32x4_t*>(reinterpret_cast<const char*>(cols + k) + col[t][c]);
-#pragma unroll
-            for (int r = 0; r < NW; ++r) d.w[r] = *reinterpret_cast<const u32x4_t*>(w[r] + k + w_off);
+        Block<NW, MT> ring[kDepth];
+        auto load_w = [&](int d, int j) {
+            const int64_t k = (kb0 + (int64_t)(j0 + j) * step) * kBlk;
+            ring[d].load_w([&](int r, int i) { return w[r] + k + (w_off + i * w_next); });
         };
-        auto use = [&](const Half<NW, MT>& d, int i, bool second) {
-            if (!second)
-#pragma unroll
-                for (int r = 0; r < NW; ++r)
-#pragma unroll
-                    for (int t = 0; t < MT; ++t) p[r][t] = f32x4_t{0, 0, 0, 0};
-#pragma unroll
-            for (int t = 0; t < MT; ++t)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) stage[t * 128 + c * 64 + put] = d.x[t][c];
-            wave_lds_order();
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                bf16x8_t x[MT];
-#pragma unroll
-                for (int t = 0; t < MT; ++t) x[t] = __builtin_bit_cast(bf16x8_t, stage[t * 128 + (get ^ c)]);
-#pragma unroll
-                for (int r = 0; r < NW; ++r) {
-                    const bf16x8_t f = w_frag(d.w[r], c);
-#pragma unroll
-                    for (int t = 0; t < MT; ++t) p[r][t] = mfma_bf16(f, x[t], p[r][t]);
-                }
-            }
-            wave_lds_order();
-            if (second)
-#pragma unroll
-                for (int r = 0; r < NW; ++r) {
-                    const float sc = __uint_as_float(
-                        (uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(sv[r / (NW / NS)]), i / 2));
-#pragma unroll
-                    for (int t = 0; t < MT; ++t)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) acc[r][t][k] = __builtin_fmaf(p[r][t][k], sc, acc[r][t][k]);
-                }
+        auto load_x = [&](int d, int j) {
+            const int64_t k = (kb0 + (int64_t)(j0 + j) * step) * kBlk;
+            ring[d].load_x([&](int t, int i) { return reinterpret_cast<const char*>(cols + k) + col[t][i]; });
         };
 #pragma unroll
-        for (int d = 0; d < DEPTH; ++d) {
-            load(ring[d], min(d, halves - 1));
+        for (int d = 0; d < kDepth; ++d) {
+            load_w(d, min(d, blocks - 1));
+            load_x(d, min(d, blocks - 1));
             __builtin_amdgcn_sched_barrier(0);
         }
-        int i = 0;
-        for (; i + 2 * DEPTH <= halves; i += DEPTH)
+        in_flight(blocks, [&](int d, int j, auto more) {
+            f32x4_t p[NW][MT];
+            ring[d].multiply(stage, lane, p, [&]() { if constexpr (more) load_w(d, j + kDepth); },
+                             [&]() { if constexpr (more) load_x(d, j + kDepth); });
 #pragma unroll
-            for (int d = 0; d < DEPTH; ++d) {
-                use(ring[d], i + d, d & 1);
-                __builtin_amdgcn_sched_barrier(0);
-                load(ring[d], i + d + DEPTH);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-        // the last DEPTH to 2 DEPTH - 1 halves (or all, where there are fewer)
-#pragma unroll
-        for (int d = 0; d < DEPTH; ++d)
-            if (i + d < halves) {
-                use(ring[d], i + d, d & 1);
-                if (i + d + DEPTH < halves) load(ring[d], i + d + DEPTH);
-            }
-        i += DEPTH;
-#pragma unroll
-        for (int d = 0; d < DEPTH; ++d)
-            if (i + d < halves) use(ring[d], i + d, d & 1);
+            for (int r = 0; r < NW; ++r)
+                promote(p[r], __uint_as_float((uint32_t)__builtin_amdgcn_readlane(
+                                  (int)__float_as_uint(sv[r / (NW / NS)]), j)), acc[r]);
+            __builtin_amdgcn_sched_barrier(0);
+        });
     }
 }
 
@@ -187,10 +245,6 @@ __device__ __forceinline__ void products(const uint8_t* (&w)[NW], uint32_t w_off
 // registers hold them.
 template <int MOST>
 constexpr int kRowTiles = MOST == 2 ? 2 : 1;
-// Half blocks in flight, likewise.
-template <int NW, int MT>
-constexpr int kDepth = NW + 2 * MT <= 6 ? 4 : 2;
-
 // 16 * RT gate rows and the up rows beside them for the tokens list[first ...]
 // of an expert, MT tiles of them at most.
 template <int PARTS, int RT, int MT>
@@ -215,13 +269,10 @@ __device__ __forceinline__ void up_pass(const MoeArgs& a, int e, int i0, int fir
             xr[t][c] = 2u * ((uint32_t)(list[at < count ? at : first] / a.topk) * a.H + 8 * (lane & 7));
         }
     f32x4_t acc[2 * RT][MT];
-#pragma unroll
-    for (int r = 0; r < 2 * RT; ++r)
-#pragma unroll
-        for (int t = 0; t < MT; ++t) acc[r][t] = f32x4_t{0, 0, 0, 0};
+    clear(acc);
     const int KB = a.H / kBlk;
-    u32x4_t* stage = reinterpret_cast<u32x4_t*>(sm) + wave * MT * 128;    // the sums come after
-    products<2 * RT, 2, MT, kDepth<2 * RT, MT>>(w, r16 * a.H + 16 * g, s, a.x, xr, stage, wave,
+    u32x4_t* stage = reinterpret_cast<u32x4_t*>(sm) + wave * Block<2 * RT, MT>::STAGE;    // the sums come after
+    products<2 * RT, 2, MT>(w, (lane >> 3) * a.H + 16 * (lane & 7), 8 * a.H, s, a.x, xr, stage, wave,
                                        (KB - wave + kUpWaves - 1) / kUpWaves, kUpWaves, lane, acc);
 
     __syncthreads();
@@ -263,7 +314,9 @@ __global__ __launch_bounds__(kUpWaves * 64, 2) void moe_up_kernel(MoeArgs a) {
     constexpr int RT = kRowTiles<MOST>;
     __shared__ uint32_t bitmap[kMoeMaxExperts / 32];
     __shared__ int list[kMoeMaxTokens];               // the rows of h of its tokens
-    __shared__ __attribute__((aligned(16))) float sm[kUpWaves * 2 * RT * MOST * 256];   // >= the waves' stages
+    // the waves' stages, then their sums
+    __shared__ __attribute__((aligned(16))) float sm[kUpWaves * (2 * RT * MOST > 2 * (2 * RT + MOST)
+                                                                      ? 2 * RT * MOST : 2 * (2 * RT + MOST)) * 256];
     __shared__ int found[2];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -364,20 +417,18 @@ constexpr int kDownTokens = MOST == 1 ? 16 : kGroup;
 // 16 * RT rows of y for the workgroup's tokens.  The work is a list of passes,
 // an expert and up to kPass of its tokens each, of I / 128 K blocks; the waves
 // take equal runs of the list's blocks.  A pass's columns are its tokens' first
-// parts, then their second ones, ...  A wave's loads run DEPTH half blocks ahead
-// of its products and over the ends of passes, so HBM's latency is met once.
+// parts, then their second ones, ...  A wave's loads run kDepth blocks ahead of
+// its products and over the ends of passes, so HBM's latency is met once.
 template <int PARTS, int MOST>
 __global__ __launch_bounds__(kDownWaves * 64) void moe_down_kernel(MoeArgs a) {
-    constexpr int RT = kRowTiles<MOST>, ROWS = RT * kTile, MT = MOST, DEPTH = kDepth<RT, MT>;
+    constexpr int RT = kRowTiles<MOST>, ROWS = RT * kTile, MT = MOST;
     constexpr int TOKENS = kDownTokens<MOST>, PASS = kPass<PARTS, MOST>;
-    struct Pass {
-        int expert;
-        int first, tokens;                             // in `entries`
-    };
+    // a pass: expert | first of `entries` << 10 | tokens << 20
+    static_assert(kMoeMaxExperts <= 1024 && kGroup * kMoeMaxTopk <= 1024 && PASS < 2048, "a pass fits a word");
     __shared__ __attribute__((aligned(16))) float slabs[kDownWaves][TOKENS * ROWS];
-    __shared__ u32x4_t stages[kDownWaves][MT * 128];
+    __shared__ u32x4_t stages[kDownWaves][Block<RT, MT>::STAGE];
     __shared__ Entry entries[TOKENS * kMoeMaxTopk];
-    __shared__ Pass passes[TOKENS * kMoeMaxTopk];
+    __shared__ uint32_t passes[TOKENS * kMoeMaxTopk];
     __shared__ int totals[kDownWaves];
     const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -410,7 +461,8 @@ __global__ __launch_bounds__(kDownWaves * 64) void moe_down_kernel(MoeArgs a) {
             if (w < wave) at += totals[w];
             pass_count += totals[w];
         }
-        for (int i = 0; i < n; ++i) passes[at + i] = Pass{r.expert, r.first + i * PASS, min(PASS, r.count - i * PASS)};
+        for (int i = 0; i < n; ++i)
+            passes[at + i] = r.expert | (r.first + i * PASS) << 10 | min(PASS, r.count - i * PASS) << 20;
         __syncthreads();
     }
 
@@ -418,19 +470,18 @@ __global__ __launch_bounds__(kDownWaves * 64) void moe_down_kernel(MoeArgs a) {
     const int64_t blocks = (int64_t)pass_count * KB;
     const int share = z * kDownWaves + wave, all = a.shares * kDownWaves;
     const int64_t u0 = blocks * share / all;
-    const int halves = 2 * (int)(blocks * (share + 1) / all - u0);
-    const uint32_t w_off = r16 * a.I + 16 * g;
+    const int count = (int)(blocks * (share + 1) / all - u0);
+    const uint32_t w_off = (lane >> 3) * a.I + 16 * (lane & 7);
     u32x4_t* stage = stages[wave];
-    const int put = lane ^ (lane >> 3), get = (lane & 15) * 8 + ((2 * (lane >> 4)) ^ (lane & 7));
-    if (halves > 0) {
+    if (count > 0) {
         // the loads' place
         int lp = (int)(u0 / KB), lk = (int)(u0 - (int64_t)lp * KB);
         const uint8_t* w;
         const float* s;
         uint32_t col[MT][2];
         auto aim = [&]() {
-            const int e = __builtin_amdgcn_readfirstlane(passes[lp].expert);
-            const int first = passes[lp].first, n = passes[lp].tokens;
+            const int pass = __builtin_amdgcn_readfirstlane(passes[lp]);
+            const int e = pass & 1023, first = pass >> 10 & 1023, n = pass >> 20;
             w = a.w2 + ((int64_t)e * a.H + n0) * a.I;
             s = a.s2 + ((int64_t)e * (a.H / kBlk) + n0 / kBlk) * KB;
 #pragma unroll
@@ -444,42 +495,33 @@ __global__ __launch_bounds__(kDownWaves * 64) void moe_down_kernel(MoeArgs a) {
                                       8 * (lane & 7));
                 }
         };
-        Half<RT, MT> ring[DEPTH];
-        float scale[DEPTH / 2];
-        auto load = [&](int d) {
-            const int k = lk * kBlk + (d & 1) * 64;
-#pragma unroll
-            for (int t = 0; t < MT; ++t)
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    ring[d].x[t][c] = *reinterpret_cast<const u32x4_t*>(reinterpret_cast<const char*>(a.h + k) + col[t][c]);
-#pragma unroll
-            for (int r = 0; r < RT; ++r)
-                ring[d].w[r] = *reinterpret_cast<const u32x4_t*>(w + (int64_t)r * kTile * a.I + k + w_off);
-            if (d & 1) {
-                scale[d / 2] = s[lk];
-                // past the last block the last one again
-                if (lk + 1 < KB) ++lk;
-                else if (lp + 1 < pass_count) {
-                    ++lp;
-                    lk = 0;
-                    aim();
-                }
+        Block<RT, MT> ring[kDepth];
+        float scale[kDepth];
+        auto load_w = [&](int d) {
+            ring[d].load_w([&](int r, int i) {
+                return w + ((int64_t)(r * kTile + 8 * i) * a.I + lk * kBlk) + w_off;
+            });
+        };
+        auto load_x = [&](int d) {
+            ring[d].load_x([&](int t, int i) { return reinterpret_cast<const char*>(a.h + lk * kBlk) + col[t][i]; });
+            scale[d] = s[lk];
+        };
+        auto advance = [&]() {
+            if (lk + 1 < KB) ++lk;
+            else if (lp + 1 < pass_count) {            // else there is nothing more to fetch
+                ++lp;
+                lk = 0;
+                aim();
             }
         };
         // the products' place
         int up = lp, uk = lk;
-        f32x4_t acc[RT][MT], p[RT][MT];
-        auto clear = [&](f32x4_t (&v)[RT][MT]) {
-#pragma unroll
-            for (int r = 0; r < RT; ++r)
-#pragma unroll
-                for (int t = 0; t < MT; ++t) v[r][t] = f32x4_t{0, 0, 0, 0};
-        };
+        f32x4_t acc[RT][MT];
         // the weighted sums to the slab; a token is in an expert's list once, so no
         // two lanes of a part meet
         auto flush = [&]() {
-            const int first = passes[up].first, n = passes[up].tokens;
+            const int pass = __builtin_amdgcn_readfirstlane(passes[up]);
+            const int first = pass >> 10 & 1023, n = pass >> 20;
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
                 const int c = 16 * t + r16, part = c / n;
@@ -497,55 +539,32 @@ __global__ __launch_bounds__(kDownWaves * 64) void moe_down_kernel(MoeArgs a) {
         };
         aim();
 #pragma unroll
-        for (int d = 0; d < DEPTH; ++d) {
-            load(d);
+        for (int d = 0; d < kDepth; ++d) {
+            load_w(d);
+            load_x(d);
+            advance();
             __builtin_amdgcn_sched_barrier(0);
         }
         clear(acc);
-        for (int i = 0; i < halves; i += DEPTH)
-#pragma unroll
-            for (int d = 0; d < DEPTH; ++d) {
-                if (i + d < halves) {
-                    if (d % 2 == 0) clear(p);
-#pragma unroll
-                    for (int t = 0; t < MT; ++t)
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) stage[t * 128 + c * 64 + put] = ring[d].x[t][c];
-                    wave_lds_order();
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        bf16x8_t x[MT];
-#pragma unroll
-                        for (int t = 0; t < MT; ++t) x[t] = __builtin_bit_cast(bf16x8_t, stage[t * 128 + (get ^ c)]);
-#pragma unroll
-                        for (int r = 0; r < RT; ++r) {
-                            const bf16x8_t f = w_frag(ring[d].w[r], c);
-#pragma unroll
-                            for (int t = 0; t < MT; ++t) p[r][t] = mfma_bf16(f, x[t], p[r][t]);
-                        }
-                    }
-                    wave_lds_order();
-                    if (d % 2 == 1) {
-                        const float sc = scale[d / 2];
-#pragma unroll
-                        for (int r = 0; r < RT; ++r)
-#pragma unroll
-                            for (int t = 0; t < MT; ++t)
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) acc[r][t][k] = __builtin_fmaf(p[r][t][k], sc, acc[r][t][k]);
-                        ++uk;
-                        if (uk == KB || i + d + 1 == halves) {
-                            flush();
-                            clear(acc);
-                            uk = 0;
-                            ++up;
-                        }
-                    }
+        in_flight(count, [&](int d, int i, auto more) {
+            f32x4_t p[RT][MT];
+            const float sc = scale[d];
+            ring[d].multiply(stage, lane, p, [&]() { if constexpr (more) load_w(d); }, [&]() {
+                if constexpr (more) {
+                    load_x(d);
+                    advance();
                 }
-                __builtin_amdgcn_sched_barrier(0);
-                load(d);
-                __builtin_amdgcn_sched_barrier(0);
+            });
+#pragma unroll
+            for (int r = 0; r < RT; ++r) promote(p[r], sc, acc[r]);
+            if (++uk == KB || i + 1 == count) {
+                flush();
+                clear(acc);
+                uk = 0;
+                ++up;
             }
+            __builtin_amdgcn_sched_barrier(0);
+        });
     }
     __syncthreads();
     // two values a thread: the waves' slabs in order, then the shares in order
