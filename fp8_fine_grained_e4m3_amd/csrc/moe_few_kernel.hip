@@ -179,31 +179,41 @@ __device__ __forceinline__ void promote(const f32x4_t (&p)[MT], float scale, f32
 // that some path skips makes the compiler wait for the ones behind it; and they
 // stay where they are written, since the scheduler gathers them at the loop's
 // end otherwise.
-constexpr int kDepth = 1;
+// One is in the stage and one on its way; two more on their way gain 6% of the
+// whole layer where a workgroup's registers are few (one column tile), nothing
+// or less elsewhere.
+template <int MT>
+constexpr int kUpDepth = MT == 1 ? 2 : 1;
+constexpr int kDownDepth = 1;
 
-// Runs step(slot, block, whether to fetch block + kDepth into the slot) for
+// Runs step(slot, block, whether to fetch block + DEPTH into the slot) for
 // blocks 0 ... count - 1.
-template <typename F>
+template <int DEPTH, typename F>
 __device__ __forceinline__ void in_flight(int count, F step) {
     int i = 0;
-    for (; i + 2 * kDepth <= count; i += kDepth)
+    if constexpr (DEPTH == 1) {
+        for (; i + 1 < count; ++i) step(0, i, std::true_type{});
+        if (i < count) step(0, i, std::false_type{});
+        return;
+    }
+    for (; i + 2 * DEPTH <= count; i += DEPTH)
 #pragma unroll
-        for (int d = 0; d < kDepth; ++d) step(d, i + d, std::true_type{});
+        for (int d = 0; d < DEPTH; ++d) step(d, i + d, std::true_type{});
 #pragma unroll
-    for (int d = 0; d < kDepth; ++d) {
-        if (i + d + kDepth < count) step(d, i + d, std::true_type{});
+    for (int d = 0; d < DEPTH; ++d) {
+        if (i + d + DEPTH < count) step(d, i + d, std::true_type{});
         else if (i + d < count) step(d, i + d, std::false_type{});
     }
-    i += kDepth;
+    i += DEPTH;
 #pragma unroll
-    for (int d = 0; d < kDepth; ++d)
+    for (int d = 0; d < DEPTH; ++d)
         if (i + d < count) step(d, i + d, std::false_type{});
 }
 
 // acc += scale * (weight block . column block) over the n 128-K blocks kb0,
 // kb0 + step, ...  w, s and cols are uniform; a lane's places in a weight tile are
 // w_off and w_off + w_next bytes on, its two in column tile t col[t] bytes.
-template <int NW, int NS, int MT>
+template <int NW, int NS, int MT, int DEPTH>
 __device__ __forceinline__ void products(const uint8_t* (&w)[NW], uint32_t w_off, uint32_t w_next,
                                          const float* (&s)[NS], const uint16_t* cols, const uint32_t (&col)[MT][2],
                                          u32x4_t* stage, int kb0, int n, int step, int lane, f32x4_t (&acc)[NW][MT]) {
@@ -212,7 +222,7 @@ __device__ __forceinline__ void products(const uint8_t* (&w)[NW], uint32_t w_off
         float sv[NS];                              // lane j: the scale of the jth block
 #pragma unroll
         for (int r = 0; r < NS; ++r) sv[r] = s[r][kb0 + (int64_t)(j0 + min(lane, blocks - 1)) * step];
-        Block<NW, MT> ring[kDepth];
+        Block<NW, MT> ring[DEPTH];
         auto load_w = [&](int d, int j) {
             const int64_t k = (kb0 + (int64_t)(j0 + j) * step) * kBlk;
             ring[d].load_w([&](int r, int i) { return w[r] + k + (w_off + i * w_next); });
@@ -222,15 +232,15 @@ __device__ __forceinline__ void products(const uint8_t* (&w)[NW], uint32_t w_off
             ring[d].load_x([&](int t, int i) { return reinterpret_cast<const char*>(cols + k) + col[t][i]; });
         };
 #pragma unroll
-        for (int d = 0; d < kDepth; ++d) {
+        for (int d = 0; d < DEPTH; ++d) {
             load_w(d, min(d, blocks - 1));
             load_x(d, min(d, blocks - 1));
             __builtin_amdgcn_sched_barrier(0);
         }
-        in_flight(blocks, [&](int d, int j, auto more) {
+        in_flight<DEPTH>(blocks, [&](int d, int j, auto more) {
             f32x4_t p[NW][MT];
-            ring[d].multiply(stage, lane, p, [&]() { if constexpr (more) load_w(d, j + kDepth); },
-                             [&]() { if constexpr (more) load_x(d, j + kDepth); });
+            ring[d].multiply(stage, lane, p, [&]() { if constexpr (more) load_w(d, j + DEPTH); },
+                             [&]() { if constexpr (more) load_x(d, j + DEPTH); });
 #pragma unroll
             for (int r = 0; r < NW; ++r)
                 promote(p[r], __uint_as_float((uint32_t)__builtin_amdgcn_readlane(
@@ -247,7 +257,7 @@ template <int MOST>
 constexpr int kRowTiles = MOST == 2 ? 2 : 1;
 // 16 * RT gate rows and the up rows beside them for the tokens list[first ...]
 // of an expert, MT tiles of them at most.
-template <int PARTS, int RT, int MT>
+template <int PARTS, int RT, int MT, int DEPTH>
 __device__ __forceinline__ void up_pass(const MoeArgs& a, int e, int i0, int first, int count,
                                         const int* list, float* sm, int wave, int lane) {
     const int r16 = lane & 15, g = lane >> 4;
@@ -272,7 +282,7 @@ __device__ __forceinline__ void up_pass(const MoeArgs& a, int e, int i0, int fir
     clear(acc);
     const int KB = a.H / kBlk;
     u32x4_t* stage = reinterpret_cast<u32x4_t*>(sm) + wave * Block<2 * RT, MT>::STAGE;    // the sums come after
-    products<2 * RT, 2, MT>(w, (lane >> 3) * a.H + 16 * (lane & 7), 8 * a.H, s, a.x, xr, stage, wave,
+    products<2 * RT, 2, MT, DEPTH>(w, (lane >> 3) * a.H + 16 * (lane & 7), 8 * a.H, s, a.x, xr, stage, wave,
                                        (KB - wave + kUpWaves - 1) / kUpWaves, kUpWaves, lane, acc);
 
     __syncthreads();
@@ -311,7 +321,7 @@ __device__ __forceinline__ void up_pass(const MoeArgs& a, int e, int i0, int fir
 
 template <int PARTS, int MOST>
 __global__ __launch_bounds__(kUpWaves * 64, 2) void moe_up_kernel(MoeArgs a) {
-    constexpr int RT = kRowTiles<MOST>;
+    constexpr int RT = kRowTiles<MOST>, DEPTH = kUpDepth<MOST>;
     __shared__ uint32_t bitmap[kMoeMaxExperts / 32];
     __shared__ int list[kMoeMaxTokens];               // the rows of h of its tokens
     // the waves' stages, then their sums
@@ -400,11 +410,11 @@ __global__ __launch_bounds__(kUpWaves * 64, 2) void moe_up_kernel(MoeArgs a) {
     for (int first = 0; first < count; first += 16 * MOST) {
         const int left = count - first;
         if (MOST == 1 || left <= 16)
-            up_pass<PARTS, RT, 1>(a, e, i0, first, count, list, sm, wave, lane);
+            up_pass<PARTS, RT, 1, DEPTH>(a, e, i0, first, count, list, sm, wave, lane);
         else if (MOST == 2 || left <= 32)
-            up_pass<PARTS, RT, MOST == 1 ? 1 : 2>(a, e, i0, first, count, list, sm, wave, lane);
+            up_pass<PARTS, RT, MOST == 1 ? 1 : 2, DEPTH>(a, e, i0, first, count, list, sm, wave, lane);
         else
-            up_pass<PARTS, RT, MOST>(a, e, i0, first, count, list, sm, wave, lane);
+            up_pass<PARTS, RT, MOST, DEPTH>(a, e, i0, first, count, list, sm, wave, lane);
     }
 }
 
@@ -417,7 +427,7 @@ constexpr int kDownTokens = MOST == 1 ? 16 : kGroup;
 // 16 * RT rows of y for the workgroup's tokens.  The work is a list of passes,
 // an expert and up to kPass of its tokens each, of I / 128 K blocks; the waves
 // take equal runs of the list's blocks.  A pass's columns are its tokens' first
-// parts, then their second ones, ...  A wave's loads run kDepth blocks ahead of
+// parts, then their second ones, ...  A wave's loads run kDownDepth blocks ahead of
 // its products and over the ends of passes, so HBM's latency is met once.
 template <int PARTS, int MOST>
 __global__ __launch_bounds__(kDownWaves * 64) void moe_down_kernel(MoeArgs a) {
@@ -495,8 +505,8 @@ __global__ __launch_bounds__(kDownWaves * 64) void moe_down_kernel(MoeArgs a) {
                                       8 * (lane & 7));
                 }
         };
-        Block<RT, MT> ring[kDepth];
-        float scale[kDepth];
+        Block<RT, MT> ring[kDownDepth];
+        float scale[kDownDepth];
         auto load_w = [&](int d) {
             ring[d].load_w([&](int r, int i) {
                 return w + ((int64_t)(r * kTile + 8 * i) * a.I + lk * kBlk) + w_off;
@@ -539,14 +549,14 @@ __global__ __launch_bounds__(kDownWaves * 64) void moe_down_kernel(MoeArgs a) {
         };
         aim();
 #pragma unroll
-        for (int d = 0; d < kDepth; ++d) {
+        for (int d = 0; d < kDownDepth; ++d) {
             load_w(d);
             load_x(d);
             advance();
             __builtin_amdgcn_sched_barrier(0);
         }
         clear(acc);
-        in_flight(count, [&](int d, int i, auto more) {
+        in_flight<kDownDepth>(count, [&](int d, int i, auto more) {
             f32x4_t p[RT][MT];
             const float sc = scale[d];
             ring[d].multiply(stage, lane, p, [&]() { if constexpr (more) load_w(d); }, [&]() {
@@ -637,11 +647,12 @@ int down_tiles(int64_t T, int64_t topk, int64_t E, int parts) {
     return T * parts <= 16 ? 1 : T * parts <= 32 || T * topk * parts <= 24 * E ? 2 : 4;
 }
 
-// Workgroups that share a tile's passes: eight, one an XCD, whose second-level
-// cache then meets an eighth of the hidden values, while a wave has two blocks.
-int down_shares(int64_t T, int64_t topk, int64_t E, int64_t I) {
-    const int64_t blocks = std::min(E, T * topk) * (I / kBlk);
-    return (int)std::max<int64_t>(1, std::min<int64_t>(kMaxShares, blocks / (2 * kDownWaves)));
+// Workgroups that share a tile's passes: what makes 512 of them (1024 of those
+// with one row tile), while a wave has two blocks.
+int down_shares(int64_t T, int64_t topk, int64_t E, int64_t H, int64_t I, int row_tiles) {
+    const int64_t blocks = std::min(E, T * topk) * (I / kBlk), tiles = H / (kTile * row_tiles);
+    const int64_t wanted = ((row_tiles == 1 ? 1024 : 512) + tiles - 1) / tiles;
+    return (int)std::max<int64_t>(1, std::min({(int64_t)kMaxShares, wanted, blocks / (2 * kDownWaves)}));
 }
 
 constexpr int64_t align16(int64_t n) { return (n + 15) / 16 * 16; }
@@ -650,9 +661,9 @@ constexpr int64_t align16(int64_t n) { return (n + 15) / 16 * 16; }
 int64_t lay_out(MoeArgs& a, int parts, char* base) {
     const int64_t T = a.T, groups = (T + kGroup - 1) / kGroup, pairs = T * a.topk;
     a.slots = std::min(a.E, a.T * a.topk);
-    a.shares = down_shares(T, a.topk, a.E, a.I);
-    const int most = down_tiles(T, a.topk, a.E, parts), rows = kTile * (most == 2 ? 2 : 1);
-    a.counters = (int)(a.H / rows * groups);
+    const int most = down_tiles(T, a.topk, a.E, parts), row_tiles = most == 2 ? kRowTiles<2> : 1;
+    a.shares = down_shares(T, a.topk, a.E, a.H, a.I, row_tiles);
+    a.counters = (int)(a.H / (kTile * row_tiles) * groups);
     int64_t n = 0;
     auto piece = [&](int64_t bytes) {
         char* at = base + n;
