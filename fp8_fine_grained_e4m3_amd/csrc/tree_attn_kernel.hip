@@ -12,9 +12,8 @@
 //
 // Bound: a few rows per key head leave the cache's bytes as the floor, so the
 // cache goes from HBM straight to registers, no LDS and no barrier on the way:
-// a wave takes 32 keys a step, holds its own running maximum and sum, fetches
-// the next step's keys as soon as this step's are in the product and its
-// values after the second product.
+// a wave takes 32 keys a step, holds its own running maximum and sum, and asks
+// for the next step's keys and values while it computes.
 //  * S^T = K q^T by 16x16x32 bf16 MFMA (e4m3 and the query are exact in bf16):
 //    lane l converts the 16-byte pieces of key l & 15 that it loaded itself;
 //    the query has the same order of D in its fragments.
@@ -24,12 +23,24 @@
 //    of one D value in a lane; a lane loads D / 16 consecutive values of those
 //    8 keys and exchanges halves of words in registers (v_perm), so the cache
 //    keeps its row order.
-//  * P is rounded to bf16 for the second product with the value's scale in it
-//    (one rounding, relative 2^-9, of terms whose sum is rounded to bf16 at
-//    the end); maximum, sum and O are fp32.
-// The keys are split over workgroups where (request, key head) pairs are few;
-// partial O, maximum and sum meet in the workspace and a second kernel joins
-// them in the order of the splits.
+//  * P, times the values' scales, is rounded to fp16 for the second product (e4m3
+//    is exact in fp16 too): 11 bits, against bf16's 8, keep its rounding below
+//    the output's.  fp16 has few exponents, so P vs 2^(14 - x) is what is
+//    rounded, x the exponent of the largest scale that the wave has met: terms
+//    down to 2^-38 of the largest possible one count.  Maximum, sum and O are
+//    fp32.
+// A wave has 16 or 32 rows.  A workgroup's four waves share the steps of up to 32
+// rows and add up in LDS, or take two times 32 rows, or four times, where there
+// are more: then a fetched key serves 128 rows from the caches, and the VALU
+// (widening keys and values, exponentials) is the bound.
+//
+// Requests differ in length, so the steps of all of them, end to end, are cut
+// into equal runs, one a workgroup for each key head: a workgroup goes through
+// the requests that its run touches.  Where a run ends inside a request, its O,
+// maximum and sum go to the workspace, and a second kernel joins a request's
+// parts in order, a thread for four values of a row.  (Joined by the last
+// workgroup to arrive instead, a long request's parts pass through one CU: 344 us
+// for two trees of 16 over 100001 tokens.)
 #include "fp8_values.h"
 #include "serve_internal.h"
 
@@ -39,7 +50,7 @@ namespace dg {
 namespace {
 
 constexpr int kWaves = 4;
-constexpr int kStep = 32;                 // keys a wave's step
+constexpr int kStep = 32;                 // keys of a wave's step
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -56,10 +67,11 @@ struct AttnArgs {
     const uint64_t* mask;
     uint16_t* o;
     float* lse;
-    float* part_o;                        // [B, H, N * G, splits, D]
-    float* part_ml;                       // [B, H, N * G, splits, 2]
+    int2* split;                          // [B, H, row blocks]: first and last run of a request; last < first: one
+    float* parts;                         // [runs * H, row blocks, 2]: O [ROWS, D], then maxima and sums [ROWS, 2]
     float scale;
-    int B, N, H, G, num_pages, page_shift, max_pages, splits, mask_words;
+    int B, N, H, G, num_pages, page_shift, max_pages, mask_words;
+    int runs, row_blocks;
 };
 
 template <int D>
@@ -85,60 +97,118 @@ struct Place {
     bool live[2];                         // the tile has keys and a valid page
 };
 
-__device__ __forceinline__ int request_len(const AttnArgs& a, int b, int& ctx, int& n) {
+// A request's context, tree and the steps of row block rb over them.
+struct Request {
+    int ctx, n, L, steps;
+};
+
+__device__ __forceinline__ Request request_of(const AttnArgs& a, int ctx, int n, int first_row) {
     const int most = a.max_pages << a.page_shift;
-    ctx = min(max(a.ctx[b], 0), most);
-    n = a.tree ? min(max(a.tree[b], 0), a.N) : a.N;
-    return min((int64_t)ctx + n, (int64_t)most);
+    Request r;
+    r.ctx = min(max(ctx, 0), most);
+    r.n = min(max(n, 0), a.N);
+    r.L = min(r.ctx + r.n, most);
+    r.steps = first_row < r.n * a.G ? (r.L + kStep - 1) / kStep : 0;
+    return r;
 }
 
-template <int D, int RT>
-__global__ __launch_bounds__(kWaves * 64, 2) void tree_attn_kernel(AttnArgs a) {
+__device__ __forceinline__ Request request(const AttnArgs& a, int b, int first_row) {   // b uniform
+    return request_of(a, uniform_input(a.ctx + b), a.tree ? uniform_input(a.tree + b) : a.N, first_row);
+}
+
+__device__ __forceinline__ int steps_of_lane(const AttnArgs& a, int b, int first_row) {
+    return b < a.B ? request_of(a, a.ctx[b], a.tree ? a.tree[b] : a.N, first_row).steps : 0;
+}
+
+// RT: row tiles of a wave, WR: waves side by side over the rows.
+template <int D, int RT, int WR>
+__global__ __launch_bounds__(kWaves * 64, RT == 1 && D <= 128 ? 3 : 2) void tree_attn_kernel(AttnArgs a) {
     constexpr int DT = D / 16;            // 16-row tiles of O^T
-    constexpr int ROWS = 16 * RT;
+    constexpr int WROWS = 16 * RT, ROWS = WROWS * WR, KW = kWaves / WR;
+    constexpr int PITCH = D + 4;          // of a row of O in LDS
+    constexpr int PART = ROWS * (D + 2);  // floats of a part
+    __shared__ __attribute__((aligned(16))) float sm_o[KW > 1 ? ROWS * PITCH : 1];
+    __shared__ float sm_ml[KW > 1 ? kWaves : 1][WROWS][2];
     const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int split = blockIdx.x % a.splits, bh = blockIdx.x / a.splits;
-    const int b = bh / a.H, h = bh - b * a.H;
-    const int row0 = blockIdx.y * ROWS;
+    const int wr = wave % WR, kw = wave / WR;
+    // The row blocks of a run follow one another on one XCD (workgroups go to the
+    // eight in turn), whose cache then has their keys.
+    const int in_xcd = blockIdx.x >> 3, rb = in_xcd % a.row_blocks;
+    const int run_head = (in_xcd / a.row_blocks) * 8 + (blockIdx.x & 7);
+    if (run_head >= a.runs * a.H) return;
+    const int run = run_head / a.H, h = run_head - run * a.H;
+    const int block0 = rb * ROWS, row0 = block0 + wr * WROWS;
     const int all_rows = a.N * a.G, Hq = a.H * a.G;
-    int ctx, n;
-    const int L = request_len(a, b, ctx, n);
-    const int rows = n * a.G;
-    const bool whole = a.splits == 1;
 
-    if (row0 >= rows) {                   // nothing but rows past the tree's end
-        if (whole) {
-            for (int i = threadIdx.x; i < ROWS * D; i += blockDim.x) {
-                const int r = row0 + i / D;
-                if (r < all_rows)
-                    a.o[((int64_t)(b * (int64_t)a.N + r / a.G) * Hq + h * a.G + r % a.G) * D + i % D] = 0;
-            }
-            for (int r = row0 + threadIdx.x; r < min(row0 + ROWS, all_rows); r += blockDim.x)
-                a.lse[(int64_t)(b * (int64_t)a.N + r / a.G) * Hq + h * a.G + r % a.G] = -__builtin_inff();
+    // this run's steps of all requests', and the request that they start in
+    int64_t total = 0;
+    for (int base = 0; base < a.B; base += 64) {
+        int v = steps_of_lane(a, base + lane, block0);
+#pragma unroll
+        for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
+        total += __builtin_amdgcn_readfirstlane(v);
+    }
+    const int64_t runs = max((int64_t)1, min((int64_t)a.runs, total / KW));
+    if (run >= runs) return;
+    const int64_t s0 = total * run / runs, s1 = total * (run + 1) / runs;
+    int64_t start = 0;                    // of request b
+    int b = a.B;
+    for (int base = 0; base < a.B; base += 64) {
+        const int steps = steps_of_lane(a, base + lane, block0);
+        int upto = steps;                 // inclusive prefix
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int v = __shfl_up(upto, o);
+            if (lane >= o) upto += v;
         }
-        return;
+        const uint64_t hit = __ballot(base + lane < a.B && (start + upto > s0 || start + upto - steps >= s0));
+        if (hit != 0) {
+            const int at = __builtin_ctzll(hit);
+            b = base + at;
+            start += __builtin_amdgcn_readlane(upto - steps, at);
+            break;
+        }
+        start += __builtin_amdgcn_readlane(upto, 63);
     }
 
-    // this workgroup's steps, dealt to its waves in turn
-    const int steps = (L + kStep - 1) / kStep;
-    const int chunk = (steps + a.splits - 1) / a.splits;
-    const int s_end = min(steps, (split + 1) * chunk);
-    int s = split * chunk + wave;
+    for (; b < a.B && (start < s1 || (run == runs - 1 && start == total)); ++b) {
+    const Request rq = request(a, b, block0);
+    const int ctx = rq.ctx, L = rq.L, rows = rq.n * a.G;
+    const int lo = (int)max(s0 - start, (int64_t)0), hi = (int)min(s1 - start, (int64_t)rq.steps);
+    start += rq.steps;
+    auto out_row = [&](int r) { return ((int64_t)b * a.N + r / a.G) * Hq + h * a.G + r % a.G; };
+    const bool whole = lo == 0 && hi == rq.steps;
+    if (lo == 0 && threadIdx.x == 0 && a.runs > 1) {
+        // the last run that starts at or before the request's last step
+        const int64_t last = whole ? run - 1 : (start * runs + total - 1) / total - 1;
+        a.split[((int64_t)b * a.H + h) * a.row_blocks + rb] = make_int2(run, (int)last);
+    }
+    if (rq.steps == 0) {                  // no row of the block sees anything
+        for (int i = threadIdx.x; i < ROWS * D / 8; i += kWaves * 64) {
+            const int r = block0 + i / (D / 8);
+            if (r >= all_rows) break;
+            const int64_t at = out_row(r);
+            *reinterpret_cast<u32x4_t*>(a.o + at * D + i % (D / 8) * 8) = u32x4_t{0, 0, 0, 0};
+            if (i % (D / 8) == 0) a.lse[at] = -__builtin_inff();
+        }
+        continue;
+    }
 
+    const int qlane = fresh(lane), qr16 = qlane & 15, qg = qlane >> 4;
     // the lane's query row of each row tile, its D values in the keys' order
     bf16x8_t qf[RT][D / 32];
     int tok[RT];
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-        const int r = row0 + 16 * t + r16;
+        const int r = row0 + 16 * t + qr16;
         tok[t] = r / a.G;
         const int hq = h * a.G + r - tok[t] * a.G;
-        const uint16_t* src = a.q + (int64_t)(b * (int64_t)a.N + tok[t]) * a.q_stride + (int64_t)hq * D;
+        const uint16_t* src = a.q + ((int64_t)b * a.N + tok[t]) * a.q_stride + (int64_t)hq * D;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
             u32x4_t w = {0, 0, 0, 0};
-            if (r < rows) w = *reinterpret_cast<const u32x4_t*>(src + (c / 2) * 64 + g * 16 + (c % 2) * 8);
+            if (r < rows) w = *reinterpret_cast<const u32x4_t*>(src + (c / 2) * 64 + qg * 16 + (c % 2) * 8);
             qf[t][c] = __builtin_bit_cast(bf16x8_t, w);
         }
         tok[t] = min(tok[t], a.N - 1);
@@ -153,7 +223,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void tree_attn_kernel(AttnArgs a) {
             w.row[t] = 0;
             w.live[t] = j0 < L;
             if (w.live[t]) {
-                const int page = table[j0 >> a.page_shift];
+                const int page = uniform_input(table + (j0 >> a.page_shift));
                 w.live[t] = page >= 0 && page < a.num_pages;
                 if (w.live[t])
                     w.row[t] = (((int64_t)page * a.H + h) << a.page_shift) + (j0 & ((1 << a.page_shift) - 1));
@@ -161,15 +231,28 @@ __global__ __launch_bounds__(kWaves * 64, 2) void tree_attn_kernel(AttnArgs a) {
         }
         return w;
     };
+    f32x4_t acc[RT][DT];                  // in units of 2^(unit - 14)
+    float m[RT], l[RT];
+    int unit = -1000;
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        m[t] = -__builtin_inff();
+        l[t] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < DT; ++i) acc[t][i] = f32x4_t{0, 0, 0, 0};
+    }
+    const float c2 = a.scale * kLog2e;
+    // The next step's keys are asked for when this step's are in the first
+    // product, its values when they are in the second.  Neither is conditional
+    // (past the last step the last one again), and they stay where they are
+    // written: the compiler then waits for this step's loads alone.
+    if (lo + kw < hi && row0 < rows) {
     Keys<D> x;
-    auto fetch_k = [&](const Place& w) {
+    auto fetch_k = [&](const Place& w, int t) {
+        const uint8_t* kp = a.kc + (w.row[t] + r16) * D + g * 16;
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const uint8_t* kp = a.kc + (w.row[t] + r16) * D + g * 16;
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c) x.k[t][c] = *reinterpret_cast<const u32x4_t*>(kp + 64 * c);
-            x.ks[t] = *reinterpret_cast<const f32x4_t*>(a.ks + w.row[t] + 4 * g);
-        }
+        for (int c = 0; c < D / 64; ++c) x.k[t][c] = *reinterpret_cast<const u32x4_t*>(kp + 64 * c);
+        x.ks[t] = *reinterpret_cast<const f32x4_t*>(a.ks + w.row[t] + 4 * g);
     };
     auto fetch_v = [&](const Place& w) {
 #pragma unroll
@@ -181,78 +264,96 @@ __global__ __launch_bounds__(kWaves * 64, 2) void tree_attn_kernel(AttnArgs a) {
             x.vs[t] = *reinterpret_cast<const f32x4_t*>(a.vs + w.row[t] + 4 * g);
         }
     };
-
-    f32x4_t acc[RT][DT];
-    float m[RT], l[RT];
-#pragma unroll
-    for (int t = 0; t < RT; ++t) {
-        m[t] = -__builtin_inff();
-        l[t] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < DT; ++i) acc[t][i] = f32x4_t{0, 0, 0, 0};
-    }
-    const float c2 = a.scale * kLog2e;
-
-    Place at{}, next{};
-    if (s < s_end) {
-        at = place(s);
-        fetch_k(at);
-        fetch_v(at);
-    }
-    for (; s < s_end; s += kWaves) {
+    const int s_last = hi - 1;
+    Place at = place(lo + kw), next = place(min(lo + kw + KW, s_last));
+    fetch_k(at, 0);
+    fetch_k(at, 1);
+    __builtin_amdgcn_sched_barrier(0);
+    fetch_v(at);
+    __builtin_amdgcn_sched_barrier(0);
+    for (int s = lo + kw; s < hi; s += KW) {
         const int j0 = s * kStep;
-        const bool more = s + kWaves < s_end;
-        if (more) next = place(s + kWaves);
+        const Place after = place(min(s + 2 * KW, s_last));
         const bool all = j0 + kStep <= ctx && at.live[0] && at.live[1];   // uniform: no mask here
-        f32x4_t sc[RT][2];
+        float sc[RT][2][4];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             bf16x8_t kf[D / 32];
+            float kscale[4];
 #pragma unroll
             for (int c = 0; c < D / 64; ++c) {
                 kf[2 * c] = e4m3x8_to_bf16x8(x.k[u][c].x, x.k[u][c].y);
                 kf[2 * c + 1] = e4m3x8_to_bf16x8(x.k[u][c].z, x.k[u][c].w);
             }
 #pragma unroll
+            for (int i = 0; i < 4; ++i) kscale[i] = x.ks[u][i] * c2;
+            __builtin_amdgcn_sched_barrier(0);
+            fetch_k(next, u);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
             for (int t = 0; t < RT; ++t) {
                 f32x4_t p = {0, 0, 0, 0};
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) p = mfma_bf16(kf[c], qf[t][c], p);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sc[t][u][i] = p[i] * (x.ks[u][i] * c2);
+                for (int i = 0; i < 4; ++i) sc[t][u][i] = p[i] * kscale[i];
             }
         }
-        if (more) fetch_k(next);
-        if (!all) {
+        f16x8_t pf[RT];
+        float vscale[2][4];
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+        for (int t = 0; t < RT; ++t) {
+            if (!all) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int j = j0 + 16 * u + 4 * g + i;      // position
-                    const int d = j - ctx;                      // number in the tree
-                    const bool there = at.live[u] && j < L;
+                for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int t = 0; t < RT; ++t) {
-                        bool seen = there;
-                        if (there && d >= 0)
+                    for (int i = 0; i < 4; ++i) {
+                        const int j = j0 + 16 * u + 4 * g + i;      // position
+                        const int d = j - ctx;                      // number in the tree
+                        bool seen = at.live[u] && j < L;
+                        if (seen && d >= 0)
                             seen = a.mask ? (a.mask[((int64_t)b * a.N + tok[t]) * a.mask_words + (d >> 6)] >> (d & 63)) & 1
                                           : d <= tok[t];
                         if (!seen) sc[t][u][i] = -__builtin_inff();
                     }
+            }
+            if (t == 0) {                 // the values' scales, in units of the largest so far
+                if (!all) {
                     // values past the end may hold anything: 0 * NaN must not reach O
-                    if (!there) x.v[u][i] = typename VWord<D>::type(0);
-                }
-        }
-        bf16x8_t pf[RT];
 #pragma unroll
-        for (int t = 0; t < RT; ++t) {
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (!at.live[u] || j0 + 16 * u + 4 * g + i >= L) {
+                                x.vs[u][i] = 0.0f;
+                                x.v[u][i] = typename VWord<D>::type(0);
+                            }
+                }
+                float top = 0.0f;
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) top = __builtin_fmaxf(top, x.vs[u][i]);
+                const int now = __builtin_amdgcn_readfirstlane(__builtin_amdgcn_frexp_expf(max_of_groups(top)));
+                if (now > unit) {
+                    const float f = __builtin_amdgcn_ldexpf(1.0f, max(unit - now, -1000));
+#pragma unroll
+                    for (int r = 0; r < RT; ++r)
+#pragma unroll
+                        for (int i = 0; i < DT; ++i) acc[r][i] *= f;
+                    unit = now;
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) vscale[u][i] = __builtin_amdgcn_ldexpf(x.vs[u][i], 14 - unit);
+            }
             float mx = m[t];
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) mx = __builtin_fmaxf(mx, sc[t][u][i]);
-            mx = __builtin_fmaxf(mx, __shfl_xor(mx, 16));
-            mx = __builtin_fmaxf(mx, __shfl_xor(mx, 32));
+            mx = max_of_groups(mx);
             const float base = mx == -__builtin_inff() ? 0.0f : mx;   // nothing seen yet: exp2 stays 0
             if (__any(mx != m[t])) {
                 const float f = __builtin_amdgcn_exp2f(m[t] - base);
@@ -269,13 +370,13 @@ __global__ __launch_bounds__(kWaves * 64, 2) void tree_attn_kernel(AttnArgs a) {
                 for (int i = 0; i < 4; ++i) {
                     const float e = __builtin_amdgcn_exp2f(sc[t][u][i] - base);
                     l[t] += e;
-                    p[i] = e * x.vs[u][i];
-                    if (!all) p[i] = sc[t][u][i] == -__builtin_inff() ? 0.0f : p[i];   // scales of unseen keys
+                    p[i] = e * vscale[u][i];
+                    if (!all && sc[t][u][i] == -__builtin_inff()) p[i] = 0.0f;   // whatever its scale
                 }
-                w[2 * u] = f32x2_to_bf16x2(p[0], p[1]);
-                w[2 * u + 1] = f32x2_to_bf16x2(p[2], p[3]);
+                w[2 * u] = f32x2_to_f16x2(p[0], p[1]);
+                w[2 * u + 1] = f32x2_to_f16x2(p[2], p[3]);
             }
-            pf[t] = __builtin_bit_cast(bf16x8_t, w);
+            pf[t] = __builtin_bit_cast(f16x8_t, w);
         }
         // V^T: tile i takes D value r16 * DT + i of the lane's 8 keys
 #pragma unroll
@@ -288,173 +389,237 @@ __global__ __launch_bounds__(kWaves * 64, 2) void tree_attn_kernel(AttnArgs a) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const uint32_t ka = x.v[u][2 * i][w], kb = x.v[u][2 * i + 1][w];
-                        const uint32_t va = half ? e4m3x2_to_bf16x2<true>(ka) : e4m3x2_to_bf16x2<false>(ka);
-                        const uint32_t vb = half ? e4m3x2_to_bf16x2<true>(kb) : e4m3x2_to_bf16x2<false>(kb);
+                        const uint32_t va = half ? e4m3x2_to_f16x2<true>(ka) : e4m3x2_to_f16x2<false>(ka);
+                        const uint32_t vb = half ? e4m3x2_to_f16x2<true>(kb) : e4m3x2_to_f16x2<false>(kb);
                         even[2 * u + i] = __builtin_amdgcn_perm(vb, va, 0x05040100u);
                         odd[2 * u + i] = __builtin_amdgcn_perm(vb, va, 0x07060302u);
                     }
                 const int i = 4 * w + 2 * half;
 #pragma unroll
                 for (int t = 0; t < RT; ++t) {
-                    acc[t][i] = mfma_bf16(__builtin_bit_cast(bf16x8_t, even), pf[t], acc[t][i]);
-                    acc[t][i + 1] = mfma_bf16(__builtin_bit_cast(bf16x8_t, odd), pf[t], acc[t][i + 1]);
+                    acc[t][i] = mfma_f16(__builtin_bit_cast(f16x8_t, even), pf[t], acc[t][i]);
+                    acc[t][i + 1] = mfma_f16(__builtin_bit_cast(f16x8_t, odd), pf[t], acc[t][i + 1]);
                 }
             }
-        if (more) fetch_v(next);
+        __builtin_amdgcn_sched_barrier(0);
+        fetch_v(next);
+        __builtin_amdgcn_sched_barrier(0);
         at = next;
+        next = after;
+    }
     }
 
-    // join the waves
-    constexpr int PITCH = D + 4;
-    __shared__ __attribute__((aligned(16))) float sm_o[ROWS * PITCH];
-    __shared__ float sm_m[kWaves][ROWS], sm_l[kWaves][ROWS];
+    const int elane = fresh(lane), er16 = elane & 15, eg = elane >> 4;
+    // Join the waves of the same rows, in order, in the first one's registers; a
+    // row's O becomes relative to the largest maximum and loses its unit.
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-        l[t] += __shfl_xor(l[t], 16);
-        l[t] += __shfl_xor(l[t], 32);
-        if (g == 0) {
-            sm_m[wave][16 * t + r16] = m[t];
-            sm_l[wave][16 * t + r16] = l[t];
-        }
-    }
-    __syncthreads();
+    for (int t = 0; t < RT; ++t) l[t] = sum_of_groups(l[t]);
+    if constexpr (KW > 1) {
+        if (eg == 0)
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-        float top = sm_m[0][16 * t + r16];
-#pragma unroll
-        for (int w = 1; w < kWaves; ++w) top = __builtin_fmaxf(top, sm_m[w][16 * t + r16]);
-        const float f = m[t] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m[t] - top);
-#pragma unroll
-        for (int i = 0; i < DT; ++i) acc[t][i] *= f;
-    }
-#pragma unroll 1
-    for (int w = 0; w < kWaves; ++w) {
-        if (wave == w) {
-#pragma unroll
-            for (int t = 0; t < RT; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int c = 0; c < DT / 4; ++c) {
-                        float* at = sm_o + (16 * t + r16) * PITCH + (4 * g + i) * DT + 4 * c;
-                        f32x4_t v = {acc[t][4 * c][i], acc[t][4 * c + 1][i], acc[t][4 * c + 2][i],
-                                     acc[t][4 * c + 3][i]};
-                        if (w > 0) v += *reinterpret_cast<const f32x4_t*>(at);
-                        *reinterpret_cast<f32x4_t*>(at) = v;
-                    }
-        }
+            for (int t = 0; t < RT; ++t) {
+                sm_ml[wave][16 * t + er16][0] = m[t];
+                sm_ml[wave][16 * t + er16][1] = l[t];
+            }
         __syncthreads();
     }
-    // each thread takes 4 values of a row at a time
-    for (int i = threadIdx.x; i < ROWS * D / 4; i += kWaves * 64) {
-        const int rr = i / (D / 4), d = (i % (D / 4)) * 4, r = row0 + rr;
-        if (r >= all_rows) continue;
-        float top = sm_m[0][rr], sum = 0.0f;
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) top = __builtin_fmaxf(top, sm_m[w][rr]);
+    for (int t = 0; t < RT; ++t) {
+        float top = m[t];
+        if constexpr (KW > 1)
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w)
-            if (sm_m[w][rr] != -__builtin_inff()) sum += sm_l[w][rr] * __builtin_amdgcn_exp2f(sm_m[w][rr] - top);
-        f32x4_t v = *reinterpret_cast<const f32x4_t*>(sm_o + rr * PITCH + d);
-        if (whole) {
-            const bool none = r >= rows || top == -__builtin_inff();
-            const float inv = none ? 0.0f : 1.0f / sum;
-            const int64_t at = (int64_t)(b * (int64_t)a.N + r / a.G) * Hq + h * a.G + r % a.G;
-            u32x2_t w = {0, 0};
-            if (!none) w = u32x2_t{f32x2_to_bf16x2(v.x * inv, v.y * inv), f32x2_to_bf16x2(v.z * inv, v.w * inv)};
-            *reinterpret_cast<u32x2_t*>(a.o + at * D + d) = w;
-            if (d == 0) a.lse[at] = none ? -__builtin_inff() : (top + __builtin_amdgcn_logf(sum)) * kLn2;
-        } else if (r < rows) {
-            const int64_t at = ((int64_t)bh * all_rows + r) * a.splits + split;
-            *reinterpret_cast<f32x4_t*>(a.part_o + at * D + d) = v;
-            if (d == 0) {
-                a.part_ml[2 * at] = top;
-                a.part_ml[2 * at + 1] = sum;
+            for (int k = 0; k < KW; ++k) top = __builtin_fmaxf(top, sm_ml[k * WR + wr][16 * t + er16][0]);
+        const float f = m[t] == -__builtin_inff() ? 0.0f
+                                                  : __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f(m[t] - top), unit - 14);
+#pragma unroll
+        for (int i = 0; i < DT; ++i) acc[t][i] *= f;
+        if constexpr (KW > 1) {
+            l[t] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < KW; ++k) {
+                const float mk = sm_ml[k * WR + wr][16 * t + er16][0];
+                if (mk != -__builtin_inff())
+                    l[t] += sm_ml[k * WR + wr][16 * t + er16][1] * __builtin_amdgcn_exp2f(mk - top);
             }
         }
+        m[t] = top;
+    }
+    if constexpr (KW > 1) {
+        float* mine = sm_o + (wr * WROWS + er16) * PITCH + 4 * eg * DT;
+#pragma unroll 1
+        for (int k = 1; k < KW; ++k) {
+            if (kw == k)
+#pragma unroll
+                for (int t = 0; t < RT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int c = 0; c < DT / 4; ++c)
+                            *reinterpret_cast<f32x4_t*>(mine + 16 * t * PITCH + i * DT + 4 * c) =
+                                f32x4_t{acc[t][4 * c][i], acc[t][4 * c + 1][i], acc[t][4 * c + 2][i], acc[t][4 * c + 3][i]};
+            __syncthreads();
+            if (kw == 0)
+#pragma unroll
+                for (int t = 0; t < RT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int c = 0; c < DT / 4; ++c) {
+                            const f32x4_t v = *reinterpret_cast<const f32x4_t*>(mine + 16 * t * PITCH + i * DT + 4 * c);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) acc[t][4 * c + e][i] += v[e];
+                        }
+            __syncthreads();
+        }
+    }
+
+    // O, sum and maximum of a row, 4 x DT values a elane, as the output
+    auto write = [&](int t, const f32x4_t (&v)[DT], float top, float sum) {
+        const int r = row0 + 16 * t + er16;
+        if (r >= all_rows) return;
+        const bool none = r >= rows || top == -__builtin_inff();
+        const float inv = none ? 0.0f : 1.0f / sum;
+        const int64_t at = out_row(r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < DT / 4; ++c) {
+                u32x2_t w = {0, 0};
+                if (!none)
+                    w = u32x2_t{f32x2_to_bf16x2(v[4 * c][i] * inv, v[4 * c + 1][i] * inv),
+                                f32x2_to_bf16x2(v[4 * c + 2][i] * inv, v[4 * c + 3][i] * inv)};
+                *reinterpret_cast<u32x2_t*>(a.o + at * D + (4 * eg + i) * DT + 4 * c) = w;
+            }
+        if (eg == 0) a.lse[at] = none ? -__builtin_inff() : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+    };
+    if (kw != 0) continue;
+    if (whole) {
+#pragma unroll
+        for (int t = 0; t < RT; ++t) write(t, acc[t], m[t], l[t]);
+        continue;
+    }
+    // A run has one part of a request that goes on from the run before (the first
+    // of its two places) and one of a request that begins in it (the second).
+    float* part = a.parts + (((int64_t)run_head * a.row_blocks + rb) * 2 + (lo > 0 ? 0 : 1)) * PART;
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        const int r = wr * WROWS + 16 * t + er16;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < DT / 4; ++c)
+                *reinterpret_cast<f32x4_t*>(part + r * D + (4 * eg + i) * DT + 4 * c) =
+                    f32x4_t{acc[t][4 * c][i], acc[t][4 * c + 1][i], acc[t][4 * c + 2][i], acc[t][4 * c + 3][i]};
+        if (eg == 0) *reinterpret_cast<f32x2_t*>(part + ROWS * D + 2 * r) = f32x2_t{m[t], l[t]};
+    }
     }
 }
 
-// Joins the splits of a row: D / 4 threads a row, splits in order.
+// Joins the parts of requests that were split: D / 4 threads a row.
 template <int D>
-__global__ __launch_bounds__(256) void tree_attn_join_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256) void tree_attn_join_kernel(AttnArgs a, int rows_of_block) {
     constexpr int TPR = D / 4;
-    const int64_t all_rows = (int64_t)a.N * a.G;
+    const int all_rows = a.N * a.G;
     const int64_t id = (int64_t)blockIdx.x * (256 / TPR) + threadIdx.x / TPR;   // (b, h, row)
     const int d = threadIdx.x % TPR * 4;
     if (id >= (int64_t)a.B * a.H * all_rows) return;
-    const int bh = (int)(id / all_rows), r = (int)(id - bh * all_rows);
-    const int b = bh / a.H, h = bh - b * a.H;
-    int ctx, n;
-    request_len(a, b, ctx, n);
-    const float* ml = a.part_ml + 2 * id * a.splits;
-    const bool row = r < n * a.G;
+    const int64_t bh = id / all_rows;
+    const int r = (int)(id - bh * all_rows), b = (int)(bh / a.H), h = (int)(bh - (int64_t)b * a.H);
+    const int rb = r / rows_of_block, in_block = r - rb * rows_of_block;
+    const int2 split = a.split[bh * a.row_blocks + rb];
+    if (split.y < split.x) return;        // one run, or nothing: written
+    const int n = a.tree ? min(max(a.tree[b], 0), a.N) : a.N;
+    const int64_t part = (int64_t)rows_of_block * (D + 2), next = (int64_t)a.H * a.row_blocks * 2 * part;
+    const float* at = a.parts + ((int64_t)split.x * a.H + h) * a.row_blocks * 2 * part + rb * 2 * part;
+    const int parts = split.y - split.x + 1;
+    // part u: the second place of the first run, then the first places
+    auto of = [&](int u) { return at + u * next + (u == 0 ? part : 0); };
+    const int ml = rows_of_block * D + 2 * in_block, o = in_block * D + d;
     float top = -__builtin_inff();
-    if (row)
-        for (int s = 0; s < a.splits; ++s) top = __builtin_fmaxf(top, ml[2 * s]);
-    const bool none = top == -__builtin_inff();
+#pragma unroll 8
+    for (int u = 0; u < parts; ++u) top = __builtin_fmaxf(top, of(u)[ml]);
+    const bool none = r >= n * a.G || top == -__builtin_inff();
     float sum = 0.0f;
     f32x4_t v = {0, 0, 0, 0};
-    if (!none)
-        for (int s = 0; s < a.splits; ++s) {
-            if (ml[2 * s] == -__builtin_inff()) continue;       // saw nothing
-            const float f = __builtin_amdgcn_exp2f(ml[2 * s] - top);
-            sum += ml[2 * s + 1] * f;
-            v += *reinterpret_cast<const f32x4_t*>(a.part_o + (id * a.splits + s) * D + d) * f;
-        }
+#pragma unroll 8
+    for (int u = 0; u < parts; ++u) {
+        const f32x2_t x = *reinterpret_cast<const f32x2_t*>(of(u) + ml);
+        const f32x4_t w = *reinterpret_cast<const f32x4_t*>(of(u) + o);
+        const float f = x.x == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(x.x - top);   // a part may see nothing
+        sum = __builtin_fmaf(x.y, f, sum);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf(w[i], f, v[i]);
+    }
     const float inv = none ? 0.0f : 1.0f / sum;
-    const int64_t at = ((int64_t)b * a.N + r / a.G) * a.H * a.G + h * a.G + r % a.G;
+    const int64_t to = ((int64_t)b * a.N + r / a.G) * a.H * a.G + h * a.G + r % a.G;
     u32x2_t w = {0, 0};
     if (!none) w = u32x2_t{f32x2_to_bf16x2(v.x * inv, v.y * inv), f32x2_to_bf16x2(v.z * inv, v.w * inv)};
-    *reinterpret_cast<u32x2_t*>(a.o + at * D + d) = w;
-    if (d == 0) a.lse[at] = none ? -__builtin_inff() : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+    *reinterpret_cast<u32x2_t*>(a.o + to * D + d) = w;
+    if (d == 0) a.lse[to] = none ? -__builtin_inff() : (top + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
-// Row tiles a wave holds: up to 256 O values a lane's registers can keep.
-int row_tiles(int64_t N, int64_t G, int64_t D) {
-    const int64_t rows = N * G;
-    const int t = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-    return std::min<int64_t>(t, 256 / D);
+// What a call of these sizes launches.
+struct Shape {
+    int row_tiles, row_waves;             // of a wave, of a workgroup
+    int row_blocks, runs;
+
+    int rows() const { return 16 * row_tiles * row_waves; }
+};
+
+// Rows: 16 a wave up to 16 (and for D = 256, whose O fills the registers), else
+// 32; as many waves over the rows as there are.  Runs: two workgroups a CU of
+// 256, three where the registers allow it (one row tile); no run is shorter than
+// one step a wave.  From the sizes alone: lengths are on the device.
+Shape shape_of(int64_t B, int64_t N, int64_t Hq, int64_t H, int64_t D, int64_t max_pages, int64_t page_size) {
+    const int64_t rows = N * (Hq / H);
+    Shape s;
+    s.row_tiles = rows <= 16 || D == 256 ? 1 : 2;
+    const int64_t waves = (rows + 16 * s.row_tiles - 1) / (16 * s.row_tiles);
+    s.row_waves = waves <= 1 ? 1 : waves <= 2 ? 2 : 4;
+    s.row_blocks = (int)((rows + s.rows() - 1) / s.rows());
+    const int64_t groups = H * s.row_blocks, steps = B * ((max_pages * page_size + kStep - 1) / kStep);
+    const int64_t wanted = s.row_tiles == 1 && D <= 128 ? 768 : 512;
+    s.runs = (int)std::max<int64_t>(1, std::min((wanted + groups - 1) / groups, steps * s.row_waves / kWaves));
+    return s;
 }
 
-// Splits of the keys: enough workgroups for two a CU of 256, none of fewer
-// than four steps a wave.  From the sizes alone, so that a size has one order
-// of sums; the lengths themselves are on the device.
-int64_t split_count(int64_t B, int64_t N, int64_t Hq, int64_t H, int64_t D, int64_t max_pages,
-                    int64_t page_size) {
-    const int64_t G = Hq / H, block = 16 * row_tiles(N, G, D);
-    const int64_t groups = B * H * ((N * G + block - 1) / block);
-    const int64_t steps = (max_pages * page_size + kStep - 1) / kStep;
-    return std::max<int64_t>(1, std::min((512 + groups - 1) / groups, steps / (4 * kWaves)));
+template <int D, int RT>
+hipError_t launch(const AttnArgs& a, int row_waves, hipStream_t stream) {
+    const int64_t groups = ((int64_t)a.runs * a.H + 7) / 8 * 8;
+    const dim3 grid((unsigned)(groups * a.row_blocks)), block(kWaves * 64);
+    if constexpr (RT == 2 || D == 256) {      // else 16 rows are one wave's
+        if (row_waves == 2) hipLaunchKernelGGL((tree_attn_kernel<D, RT, 2>), grid, block, 0, stream, a);
+        if (row_waves == 4) hipLaunchKernelGGL((tree_attn_kernel<D, RT, 4>), grid, block, 0, stream, a);
+    }
+    if (row_waves == 1) hipLaunchKernelGGL((tree_attn_kernel<D, RT, 1>), grid, block, 0, stream, a);
+    return hipGetLastError();
 }
 
 template <int D>
-hipError_t launch(const AttnArgs& a, int rt, hipStream_t stream) {
-    const int all_rows = a.N * a.G;
-    const dim3 grid((unsigned)(a.B * a.H * a.splits), (unsigned)((all_rows + 16 * rt - 1) / (16 * rt)));
-    const dim3 block(kWaves * 64);
-    if constexpr (D == 64)
-        if (rt == 4) hipLaunchKernelGGL((tree_attn_kernel<D, 4>), grid, block, 0, stream, a);
-    if constexpr (D <= 128)
-        if (rt == 2) hipLaunchKernelGGL((tree_attn_kernel<D, 2>), grid, block, 0, stream, a);
-    if (rt == 1) hipLaunchKernelGGL((tree_attn_kernel<D, 1>), grid, block, 0, stream, a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || a.splits == 1) return e;
-    const int64_t rows = (int64_t)a.B * a.H * all_rows, per = 256 / (D / 4);
+hipError_t launch(const AttnArgs& a, const Shape& s, hipStream_t stream) {
+    hipError_t e;
+    if (D <= 128 && s.row_tiles == 2) e = launch<D, D <= 128 ? 2 : 1>(a, s.row_waves, stream);
+    else e = launch<D, 1>(a, s.row_waves, stream);
+    if (e != hipSuccess || a.runs == 1) return e;
+    const int64_t rows = (int64_t)a.B * a.H * a.N * a.G, per = 256 / (D / 4);
     hipLaunchKernelGGL((tree_attn_join_kernel<D>), dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0,
-                       stream, a);
+                       stream, a, s.rows());
     return hipGetLastError();
 }
+
+int64_t split_bytes(int64_t B, int64_t H, const Shape& s) { return (B * H * s.row_blocks * 8 + 15) / 16 * 16; }
 
 }  // namespace
 
 int64_t tree_attn_workspace_bytes(int64_t B, int64_t N, int64_t Hq, int64_t H, int64_t D,
                                   int64_t max_pages, int64_t page_size) {
-    const int64_t splits = split_count(B, N, Hq, H, D, max_pages, page_size);
-    return splits == 1 ? 0 : B * N * Hq * splits * (D + 2) * 4;
+    const Shape s = shape_of(B, N, Hq, H, D, max_pages, page_size);
+    if (s.runs == 1) return 0;            // no request is split
+    return split_bytes(B, H, s) + 2ll * s.runs * H * s.row_blocks * s.rows() * (D + 2) * 4;
 }
 
 hipError_t launch_tree_attn(const TreeAttnProblem& p, hipStream_t stream) {
+    const Shape s = shape_of(p.B, p.N, p.Hq, p.cache.H, p.cache.D, p.max_pages, p.cache.page_size);
     AttnArgs a;
     a.q = p.q; a.q_stride = p.q_stride;
     a.kc = p.cache.k_codes; a.ks = p.cache.k_sf; a.vc = p.cache.v_codes; a.vs = p.cache.v_sf;
@@ -464,14 +629,13 @@ hipError_t launch_tree_attn(const TreeAttnProblem& p, hipStream_t stream) {
     a.num_pages = (int)p.cache.num_pages; a.max_pages = (int)p.max_pages;
     a.page_shift = __builtin_ctzll((unsigned long long)p.cache.page_size);
     a.mask_words = (int)((p.N + 63) / 64);
-    a.splits = (int)split_count(p.B, p.N, p.Hq, p.cache.H, p.cache.D, p.max_pages, p.cache.page_size);
-    a.part_o = static_cast<float*>(p.workspace);
-    a.part_ml = a.part_o + p.B * p.N * p.Hq * a.splits * p.cache.D;
-    const int rt = row_tiles(p.N, a.G, p.cache.D);
+    a.runs = s.runs; a.row_blocks = s.row_blocks;
+    a.split = static_cast<int2*>(p.workspace);
+    a.parts = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + split_bytes(p.B, p.cache.H, s));
     switch (p.cache.D) {
-    case 64: return launch<64>(a, rt, stream);
-    case 128: return launch<128>(a, rt, stream);
-    case 256: return launch<256>(a, rt, stream);
+    case 64: return launch<64>(a, s, stream);
+    case 128: return launch<128>(a, s, stream);
+    case 256: return launch<256>(a, s, stream);
     default: return hipErrorInvalidValue;
     }
 }

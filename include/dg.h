@@ -504,10 +504,10 @@ dg_status dg_fp8_kv_cache_read(const uint8_t* k_codes, const float* k_sf,
  * (NaN) are not allowed at positions below c + n; dg_fp8_kv_cache_write never
  * makes them, and past c + n the cache may hold anything.
  * Rules: max_pages >= 1, max_pages * page_size <= 2^30, N * Hq < 2^20.
- * workspace: dg_fp8_tree_attention_workspace_bytes of the same sizes (0 where
- * the keys are not split over workgroups; never initialised), not shared by
- * calls that may overlap.  A size has one order of sums whatever the lengths
- * of the other requests.  One or two kernel launches.
+ * workspace: dg_fp8_tree_attention_workspace_bytes of the same sizes (0 where no
+ * request is ever split over workgroups), never initialised, not shared by calls
+ * that may overlap.  How a request is split goes by the lengths of all of them;
+ * the same inputs give the same bits.  One or two kernel launches.
  */
 dg_status dg_fp8_tree_attention(const void* q, int64_t q_stride,
                                 const uint8_t* k_codes, const float* k_sf,
