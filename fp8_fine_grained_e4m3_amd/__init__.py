@@ -603,29 +603,39 @@ def make_fp8_kv_cache(num_pages: int, num_kv_heads: int, page_size: int, head_di
                   torch.ones(shape[:3], dtype=torch.float32, device=device)) for _ in range(2))
 
 
+# The few-token calls take microseconds on the device, so their checks are one
+# test of everything first; what is wrong is looked for only when it fails.
+_U8, _I32, _I64, _F32, _BF16 = torch.uint8, torch.int32, torch.int64, torch.float32, torch.bfloat16
+_ROW_TYPES = {_BF16: DG_BF16, _F32: DG_F32}
+
+
 def _cache(cache):
-    """The cache's four tensors, checked, and its sizes."""
+    """The cache's four tensors, checked, its sizes and its device's index."""
     (kc, ks), (vc, vs) = cache
-    kc, vc, ks, vs = _fp8(kc, "k codes"), _fp8(vc, "v codes"), _f32(ks, "k scales"), _f32(vs, "v scales")
-    if kc.dim() != 4 or kc.shape != vc.shape or ks.shape != kc.shape[:3] or vs.shape != kc.shape[:3]:
-        raise ValueError(f"cache shapes: codes {tuple(kc.shape)} {tuple(vc.shape)}, scales {tuple(ks.shape)} "
-                         f"{tuple(vs.shape)}, want [pages, heads, page_size, head_dim] and its first three")
-    return kc, ks, vc, vs, kc.shape
+    shape, sf_shape, on = kc.shape, ks.shape, kc.get_device()
+    if not (kc.dtype is _U8 and vc.dtype is _U8 and ks.dtype is _F32 and vs.dtype is _F32 and on >= 0
+            and vc.shape == shape and len(shape) == 4 and shape[:3] == sf_shape and vs.shape == sf_shape
+            and kc.is_contiguous() and vc.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()
+            and ks.get_device() == on and vc.get_device() == on and vs.get_device() == on):
+        kc, vc, ks, vs = _fp8(kc, "k codes"), _fp8(vc, "v codes"), _f32(ks, "k scales"), _f32(vs, "v scales")
+        if kc.dim() != 4 or kc.shape != vc.shape or ks.shape != kc.shape[:3] or vs.shape != kc.shape[:3]:
+            raise ValueError(f"cache shapes: codes {tuple(kc.shape)} {tuple(vc.shape)}, scales {tuple(ks.shape)} "
+                             f"{tuple(vs.shape)}, want [pages, heads, page_size, head_dim] and its first three")
+        _same_device(kc, ks, vc, vs)
+        shape, on = kc.shape, kc.get_device()
+    return kc, ks, vc, vs, shape, on
 
 
-def _rows(t: torch.Tensor, name: str) -> torch.Tensor:
-    """Device rows whose last two dimensions are dense and whose tokens are evenly spaced."""
+def _rows(t: torch.Tensor, name: str) -> int:
+    """Elements between the tokens of device rows [..., tokens, heads, D] whose
+    last two dimensions are dense; what a single token has there says nothing."""
+    shape, strides = t.shape, t.stride()
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if t.numel() and (t.stride(-1) != 1 or (t.shape[-2] > 1 and t.stride(-2) != t.shape[-1])):
-        raise ValueError(f"{name}: heads and head_dim must be dense, strides are {t.stride()}")
-    return t
-
-
-def _token_stride(t: torch.Tensor) -> int:
-    """Elements between tokens; what a single token has there says nothing."""
-    dense = t.shape[-1] * t.shape[-2]
-    return t.stride(-3) if t.shape[-3] > 1 else dense
+    dense = shape[-1] * shape[-2]
+    if dense and (strides[-1] != 1 or (shape[-2] > 1 and strides[-2] != shape[-1])):
+        raise ValueError(f"{name}: heads and head_dim must be dense, strides are {strides}")
+    return strides[-3] if shape[-3] > 1 else dense
 
 
 def _same_device(first: torch.Tensor, *others):
@@ -634,7 +644,20 @@ def _same_device(first: torch.Tensor, *others):
             raise ValueError(f"tensors on {first.device} and {t.device}")
 
 
-_ROW_TYPES = {torch.bfloat16: DG_BF16, torch.float32: DG_F32}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _call(fn: str, device: int, *args):
+    """An entry point on the device's current stream."""
+    f = getattr(load_library(), fn)
+    if torch.cuda.current_device() == device:
+        status = f(*args, _raw_stream(device))
+    else:
+        with torch.cuda.device(device):
+            status = f(*args, _raw_stream(device))
+    if status != DG_OK:
+        _check(status)
 
 
 def fp8_kv_cache_write(k: torch.Tensor, v: torch.Tensor, cache, slots: torch.Tensor):
@@ -643,20 +666,21 @@ def fp8_kv_cache_write(k: torch.Tensor, v: torch.Tensor, cache, slots: torch.Ten
     page_size + offset; a slot outside the cache stores nothing).  One fp32
     scale per token and head.  Changes and returns the cache
     (make_fp8_kv_cache)."""
-    kc, ks, vc, vs, (P, H, page, D) = _cache(cache)
-    k, v, slots = _rows(k, "k"), _rows(v, "v"), _i32(slots, "slots")
-    if k.dtype not in _ROW_TYPES or v.dtype != k.dtype:
-        raise TypeError(f"k and v must both be bfloat16 or float32, got {k.dtype} and {v.dtype}")
+    kc, ks, vc, vs, (P, H, page, D), on = _cache(cache)
     T = slots.shape[0] if slots.dim() == 1 else -1
-    if tuple(k.shape) != (T, H, D) or v.shape != k.shape:
-        raise ValueError(f"shape mismatch: k {tuple(k.shape)} v {tuple(v.shape)} slots {tuple(slots.shape)}, "
-                         f"the cache has {H} heads of {D}")
-    _same_device(kc, ks, vc, vs, k, v, slots)
-    with torch.cuda.device(kc.device):
-        _check(load_library().dg_fp8_kv_cache_write(
-            k.data_ptr(), v.data_ptr(), _ROW_TYPES[k.dtype], _token_stride(k), _token_stride(v),
-            slots.data_ptr(), kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), T, H, D, P, page,
-            _stream(kc)))
+    if not (k.dtype in _ROW_TYPES and v.dtype is k.dtype and k.shape == (T, H, D) and v.shape == k.shape
+            and slots.dtype is _I32 and slots.is_contiguous()
+            and k.get_device() == on and v.get_device() == on and slots.get_device() == on):
+        _i32(slots, "slots")
+        if k.dtype not in _ROW_TYPES or v.dtype != k.dtype:
+            raise TypeError(f"k and v must both be bfloat16 or float32, got {k.dtype} and {v.dtype}")
+        if tuple(k.shape) != (T, H, D) or v.shape != k.shape:
+            raise ValueError(f"shape mismatch: k {tuple(k.shape)} v {tuple(v.shape)} slots {tuple(slots.shape)}, "
+                             f"the cache has {H} heads of {D}")
+        _dev(slots, "slots"), _rows(k, "k"), _rows(v, "v")
+        _same_device(kc, k, v, slots)
+    _call("dg_fp8_kv_cache_write", on, k.data_ptr(), v.data_ptr(), _ROW_TYPES[k.dtype], _rows(k, "k"), _rows(v, "v"),
+          slots.data_ptr(), kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), T, H, D, P, page)
     return cache
 
 
@@ -665,10 +689,11 @@ def fp8_kv_cache_read(cache, slots: torch.Tensor, dtype: torch.dtype = torch.bfl
     """The keys and values at slots (int32 [T]) of the cache as (k, v) [T, H, D]
     of dtype (bfloat16 or float32), or into out; a slot outside the cache gives
     zeros."""
-    kc, ks, vc, vs, (P, H, page, D) = _cache(cache)
-    slots = _i32(slots, "slots")
-    if slots.dim() != 1:
-        raise ValueError(f"slots must be [T], got {tuple(slots.shape)}")
+    kc, ks, vc, vs, (P, H, page, D), on = _cache(cache)
+    if not (slots.dtype is _I32 and slots.dim() == 1 and slots.is_contiguous() and slots.get_device() == on):
+        if _i32(slots, "slots").dim() != 1:
+            raise ValueError(f"slots must be [T], got {tuple(slots.shape)}")
+        _same_device(kc, slots)
     T = slots.shape[0]
     if out is None:
         if dtype not in _ROW_TYPES:
@@ -681,23 +706,22 @@ def fp8_kv_cache_read(cache, slots: torch.Tensor, dtype: torch.dtype = torch.bfl
             raise TypeError(f"out must both be bfloat16 or float32, got {k.dtype} and {v.dtype}")
         if tuple(k.shape) != (T, H, D) or v.shape != k.shape:
             raise ValueError(f"out shapes {tuple(k.shape)} {tuple(v.shape)}, want {(T, H, D)}")
-    _same_device(kc, ks, vc, vs, slots, k, v)
-    with torch.cuda.device(kc.device):
-        _check(load_library().dg_fp8_kv_cache_read(
-            kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), slots.data_ptr(), k.data_ptr(),
-            v.data_ptr(), _ROW_TYPES[k.dtype], T, H, D, P, page, _stream(kc)))
+        _same_device(kc, k, v)
+    _call("dg_fp8_kv_cache_read", on, kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), slots.data_ptr(),
+          k.data_ptr(), v.data_ptr(), _ROW_TYPES[k.dtype], T, H, D, P, page)
     return k, v
 
 
-def _workspace(given: Optional[torch.Tensor], need: int, device):
-    """The caller's workspace, or one of torch's allocator for this call; (tensor, address, bytes)."""
+def _workspace(given: Optional[torch.Tensor], on: int, need) -> Tuple[torch.Tensor, int, int]:
+    """The caller's workspace, or one of torch's allocator for this call (need()
+    says how large): itself, its address and its bytes."""
     if given is None:
-        if need == 0:
-            return None, 0, 0
-        given = torch.empty(need, dtype=torch.uint8, device=device)
-    elif given.dtype != torch.uint8:
-        raise TypeError("workspace must be uint8")
-    return _dev(given, "workspace"), given.data_ptr(), given.numel()
+        given = torch.empty(need(), dtype=_U8, device=on)
+    elif not (given.dtype is _U8 and given.get_device() == on and given.is_contiguous()):
+        if given.dtype != _U8:
+            raise TypeError("workspace must be uint8")
+        raise ValueError(f"workspace must be contiguous and on device {on}, is on {_dev(given, 'workspace').device}")
+    return given, given.data_ptr(), given.numel()
 
 
 def get_fp8_tree_attention_workspace_bytes(B: int, N: int, Hq: int, num_kv_heads: int, head_dim: int,
@@ -731,46 +755,54 @@ def fp8_tree_attention(q: torch.Tensor, cache, page_table: torch.Tensor, context
     that see nothing, are 0 and -inf.  workspace: a uint8 buffer
     (make_fp8_tree_attention_workspace); when None, one is allocated for the
     call."""
-    kc, ks, vc, vs, (P, H, page, D) = _cache(cache)
-    q = _rows(q, "q")
-    if q.dtype != torch.bfloat16:
-        raise TypeError(f"q must be bfloat16, got {q.dtype}")
+    kc, ks, vc, vs, (P, H, page, D), on = _cache(cache)
+    table, ctx = page_table, context_lens
     if q.dim() != 4 or q.shape[3] != D:
         raise ValueError(f"q {tuple(q.shape)} must be [B, N, Hq, {D}]")
     B, N, Hq, _ = q.shape
-    stride = _token_stride(q) if N > 1 or B <= 1 else q.stride(0)
-    if B > 1 and q.stride(0) != N * stride:
-        raise ValueError(f"q: tokens must be evenly spaced over requests, strides are {q.stride()}")
-    table, ctx = _i32(page_table, "page_table"), _i32(context_lens, "context_lens")
-    if table.dim() != 2 or table.shape[0] != B or tuple(ctx.shape) != (B,):
-        raise ValueError(f"page_table {tuple(table.shape)} and context_lens {tuple(ctx.shape)} must be "
-                         f"[{B}, max_pages] and [{B}]")
-    if tree_lens is not None and tuple(_i32(tree_lens, "tree_lens").shape) != (B,):
-        raise ValueError(f"tree_lens {tuple(tree_lens.shape)} must be [{B}]")
-    if tree_mask is not None:
-        if tree_mask.dtype != torch.int64:
-            raise TypeError(f"tree_mask must be int64, got {tree_mask.dtype}")
-        if tuple(_dev(tree_mask, "tree_mask").shape) != (B, N, (N + 63) // 64):
-            raise ValueError(f"tree_mask {tuple(tree_mask.shape)} must be {(B, N, (N + 63) // 64)}")
+    stride = _rows(q, "q") if N > 1 or B <= 1 else q.stride(0)
+    mask_shape = (B, N, (N + 63) // 64)
+    if not (q.dtype is _BF16 and table.dtype is _I32 and ctx.dtype is _I32 and table.dim() == 2
+            and table.shape[0] == B and ctx.shape == (B,) and table.is_contiguous() and ctx.is_contiguous()
+            and q.get_device() == on and table.get_device() == on and ctx.get_device() == on
+            and (B <= 1 or q.stride(0) == N * stride)
+            and (tree_lens is None or (tree_lens.dtype is _I32 and tree_lens.shape == (B,)
+                                       and tree_lens.is_contiguous() and tree_lens.get_device() == on))
+            and (tree_mask is None or (tree_mask.dtype is _I64 and tree_mask.shape == mask_shape
+                                       and tree_mask.is_contiguous() and tree_mask.get_device() == on))):
+        if q.dtype != torch.bfloat16:
+            raise TypeError(f"q must be bfloat16, got {q.dtype}")
+        _rows(q, "q")
+        if B > 1 and q.stride(0) != N * stride:
+            raise ValueError(f"q: tokens must be evenly spaced over requests, strides are {q.stride()}")
+        _i32(table, "page_table"), _i32(ctx, "context_lens")
+        if table.dim() != 2 or table.shape[0] != B or tuple(ctx.shape) != (B,):
+            raise ValueError(f"page_table {tuple(table.shape)} and context_lens {tuple(ctx.shape)} must be "
+                             f"[{B}, max_pages] and [{B}]")
+        if tree_lens is not None and tuple(_i32(tree_lens, "tree_lens").shape) != (B,):
+            raise ValueError(f"tree_lens {tuple(tree_lens.shape)} must be [{B}]")
+        if tree_mask is not None:
+            if tree_mask.dtype != torch.int64:
+                raise TypeError(f"tree_mask must be int64, got {tree_mask.dtype}")
+            if tuple(_dev(tree_mask, "tree_mask").shape) != mask_shape:
+                raise ValueError(f"tree_mask {tuple(tree_mask.shape)} must be {mask_shape}")
+        _same_device(kc, q, table, ctx, tree_lens, tree_mask)
     if out is None:
-        o = torch.empty((B, N, Hq, D), dtype=torch.bfloat16, device=q.device)
-        lse = torch.empty((B, N, Hq), dtype=torch.float32, device=q.device)
+        o = torch.empty((B, N, Hq, D), dtype=_BF16, device=on)
+        lse = torch.empty((B, N, Hq), dtype=_F32, device=on)
     else:
         o, lse = _dev(out[0], "out"), _f32(out[1], "lse")
         if o.dtype != torch.bfloat16:
             raise TypeError("out must be bfloat16")
         if o.shape != q.shape or tuple(lse.shape) != (B, N, Hq):
             raise ValueError(f"out shapes {tuple(o.shape)} {tuple(lse.shape)}, want {tuple(q.shape)} and {(B, N, Hq)}")
-    need = get_fp8_tree_attention_workspace_bytes(B, N, Hq, H, D, page, table.shape[1])
-    workspace, ws, ws_bytes = _workspace(workspace, need, q.device)
-    _same_device(q, kc, ks, vc, vs, table, ctx, tree_lens, tree_mask, o, lse, workspace)
-    with torch.cuda.device(q.device):
-        _check(load_library().dg_fp8_tree_attention(
-            q.data_ptr(), stride, kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(),
-            table.data_ptr(), ctx.data_ptr(), 0 if tree_lens is None else tree_lens.data_ptr(),
-            0 if tree_mask is None else tree_mask.data_ptr(), o.data_ptr(), lse.data_ptr(),
-            D ** -0.5 if scale is None else scale, B, N, Hq, H, D, P, page, table.shape[1], ws, ws_bytes,
-            _stream(q)))
+        _same_device(kc, o, lse)
+    workspace, ws, ws_bytes = _workspace(workspace, on, lambda: get_fp8_tree_attention_workspace_bytes(
+        B, N, Hq, H, D, page, table.shape[1]))
+    _call("dg_fp8_tree_attention", on, q.data_ptr(), stride, kc.data_ptr(), ks.data_ptr(), vc.data_ptr(),
+          vs.data_ptr(), table.data_ptr(), ctx.data_ptr(), 0 if tree_lens is None else tree_lens.data_ptr(),
+          0 if tree_mask is None else tree_mask.data_ptr(), o.data_ptr(), lse.data_ptr(),
+          D ** -0.5 if scale is None else scale, B, N, Hq, H, D, P, page, table.shape[1], ws, ws_bytes)
     return o, lse
 
 
@@ -801,37 +833,44 @@ def fp8_moe_few_tokens(x: torch.Tensor, w1: Tuple[torch.Tensor, torch.Tensor],
     multiples of 128.  Returns y [T, H] of dtype (bfloat16 or float32), or fills
     out.  workspace: a uint8 buffer (make_fp8_moe_few_tokens_workspace); when
     None, one is allocated for the call."""
-    x = _dev(x, "x")
-    if x.dtype != torch.bfloat16:
-        raise TypeError(f"x must be bfloat16, got {x.dtype}")
-    W1, S1, W2, S2 = _fp8(w1[0], "W1"), _f32(w1[1], "S1"), _fp8(w2[0], "W2"), _f32(w2[1], "S2")
-    ids, weights = _i32(topk_ids, "topk_ids"), _f32(topk_weights, "topk_weights")
+    (W1, S1), (W2, S2), ids, weights, on = w1, w2, topk_ids, topk_weights, x.get_device()
     if x.dim() != 2 or W1.dim() != 3 or W2.dim() != 3 or ids.dim() != 2:
         raise ValueError("x and topk_ids must be 2-D, W1 and W2 3-D")
     T, H = x.shape
     E, H2, I = W2.shape
-    if H2 != H or tuple(W1.shape) != (E, 2 * I, H) or ids.shape[0] != T or weights.shape != ids.shape:
-        raise ValueError(f"shape mismatch: x {tuple(x.shape)} W1 {tuple(W1.shape)} W2 {tuple(W2.shape)} "
-                         f"topk_ids {tuple(ids.shape)} topk_weights {tuple(weights.shape)}")
-    if tuple(S1.shape) != (E, 2 * I // 128, H // 128) or tuple(S2.shape) != (E, H // 128, I // 128):
-        raise ValueError(f"scale shapes: S1 {tuple(S1.shape)} S2 {tuple(S2.shape)}, want "
-                         f"{(E, 2 * I // 128, H // 128)} and {(E, H // 128, I // 128)}")
+    topk = ids.shape[1]
+    if not (x.dtype is _BF16 and W1.dtype is _U8 and W2.dtype is _U8 and S1.dtype is _F32 and S2.dtype is _F32
+            and ids.dtype is _I32 and weights.dtype is _F32 and H2 == H and W1.shape == (E, 2 * I, H)
+            and ids.shape[0] == T and weights.shape == ids.shape
+            and S1.shape == (E, 2 * I // 128, H // 128) and S2.shape == (E, H // 128, I // 128)
+            and x.is_contiguous() and W1.is_contiguous() and S1.is_contiguous() and W2.is_contiguous()
+            and S2.is_contiguous() and ids.is_contiguous() and weights.is_contiguous()
+            and on >= 0 and W1.get_device() == on and S1.get_device() == on and W2.get_device() == on
+            and S2.get_device() == on and ids.get_device() == on and weights.get_device() == on):
+        if _dev(x, "x").dtype != torch.bfloat16:
+            raise TypeError(f"x must be bfloat16, got {x.dtype}")
+        W1, S1, W2, S2 = _fp8(W1, "W1"), _f32(S1, "S1"), _fp8(W2, "W2"), _f32(S2, "S2")
+        _i32(ids, "topk_ids"), _f32(weights, "topk_weights")
+        if H2 != H or tuple(W1.shape) != (E, 2 * I, H) or ids.shape[0] != T or weights.shape != ids.shape:
+            raise ValueError(f"shape mismatch: x {tuple(x.shape)} W1 {tuple(W1.shape)} W2 {tuple(W2.shape)} "
+                             f"topk_ids {tuple(ids.shape)} topk_weights {tuple(weights.shape)}")
+        if tuple(S1.shape) != (E, 2 * I // 128, H // 128) or tuple(S2.shape) != (E, H // 128, I // 128):
+            raise ValueError(f"scale shapes: S1 {tuple(S1.shape)} S2 {tuple(S2.shape)}, want "
+                             f"{(E, 2 * I // 128, H // 128)} and {(E, H // 128, I // 128)}")
+        _same_device(x, W1, S1, W2, S2, ids, weights)
     if out is None:
         if dtype not in _ROW_TYPES:
             raise TypeError(f"dtype must be bfloat16 or float32, got {dtype}")
-        out = torch.empty((T, H), dtype=dtype, device=x.device)
+        out = torch.empty((T, H), dtype=dtype, device=on)
     else:
         out = _dev(out, "out")
         if out.dtype not in _ROW_TYPES:
             raise TypeError(f"out must be bfloat16 or float32, got {out.dtype}")
         if out.shape != x.shape:
             raise ValueError(f"out {tuple(out.shape)} must be {tuple(x.shape)}")
-    need = get_fp8_moe_few_tokens_workspace_bytes(T, ids.shape[1], E, H, I)
-    workspace, ws, ws_bytes = _workspace(workspace, need, x.device)
-    _same_device(x, W1, S1, W2, S2, ids, weights, out, workspace)
-    with torch.cuda.device(x.device):
-        _check(load_library().dg_fp8_moe_few_tokens(
-            x.data_ptr(), W1.data_ptr(), S1.data_ptr(), W2.data_ptr(), S2.data_ptr(), ids.data_ptr(),
-            weights.data_ptr(), out.data_ptr(), _ROW_TYPES[out.dtype], T, ids.shape[1], E, H, I, ws, ws_bytes,
-            _stream(x)))
+        _same_device(x, out)
+    workspace, ws, ws_bytes = _workspace(workspace, on, lambda: get_fp8_moe_few_tokens_workspace_bytes(
+        T, topk, E, H, I))
+    _call("dg_fp8_moe_few_tokens", on, x.data_ptr(), W1.data_ptr(), S1.data_ptr(), W2.data_ptr(), S2.data_ptr(),
+          ids.data_ptr(), weights.data_ptr(), out.data_ptr(), _ROW_TYPES[out.dtype], T, topk, E, H, I, ws, ws_bytes)
     return out

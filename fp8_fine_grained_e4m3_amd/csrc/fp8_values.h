@@ -95,6 +95,23 @@ __device__ __forceinline__ int fresh(int v) {
     return r;
 }
 
+// The value of lane 4 (l / 4) + I, in every lane l.
+template <int I>
+__device__ __forceinline__ float of_quad(float v) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), I * 0x55, 0xF, 0xF, true));
+}
+
+// Inclusive sum of v over the wave's lanes up to each.
+__device__ __forceinline__ int sum_up_to_lane(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);   // row_shr:1
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);   // row_shr:2
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);   // row_shr:4
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);   // row_shr:8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // row_bcast:15 into rows 1 and 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // row_bcast:31 into rows 2 and 3
+    return v;
+}
+
 // Between a wave's LDS writes and reads of the same place by its other lanes:
 // the hardware keeps their order, this keeps the compiler from changing it.
 __device__ __forceinline__ void wave_lds_order() {

@@ -13,7 +13,9 @@
 // pass with 16-byte accesses: a lane holds 8 values of a row, D / 8 lanes a
 // row, and the row's maximum is log2(D / 8) exchanges between lanes.  Keys and
 // values share a launch (gridDim.y = 2), which halves the launches of a decode
-// step.
+// step.  Read rows are stored past the caches (40000 tokens of 8 heads of 128
+// values as bf16, 249 MB: 47 us, 5.2 TB/s, against 64 us with plain stores);
+// written codes are not, the attention that follows reads them.
 #include "fp8_values.h"
 #include "serve_internal.h"
 
@@ -54,15 +56,28 @@ __device__ __forceinline__ void store8(uint16_t* p, const float (&x)[8]) {
     u32x4_t w;
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = f32x2_to_bf16x2(x[2 * i], x[2 * i + 1]);
-    *reinterpret_cast<u32x4_t*>(p) = w;
+    __builtin_nontemporal_store(w, reinterpret_cast<u32x4_t*>(p));
 }
 
 __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
     f32x4_t a, b;
 #pragma unroll
     for (int i = 0; i < 4; ++i) a[i] = x[i], b[i] = x[4 + i];
-    reinterpret_cast<f32x4_t*>(p)[0] = a;
-    reinterpret_cast<f32x4_t*>(p)[1] = b;
+    __builtin_nontemporal_store(a, reinterpret_cast<f32x4_t*>(p));
+    __builtin_nontemporal_store(b, reinterpret_cast<f32x4_t*>(p) + 1);
+}
+
+// x / s, correctly rounded, given y = 1 / s correctly rounded: each correction adds
+// the exact remainder x - q s times y, the first leaves q within a unit in the
+// last place, and from such a q a correction with a correctly rounded reciprocal
+// gives the rounded quotient (Markstein).  s is normal; quotients too small for
+// the remainder to be exact are far below half the smallest code.
+__device__ __forceinline__ float quotient(float x, float s, float y) {
+#pragma clang fp contract(off)
+    float q = x * y;
+    q = __builtin_fmaf(__builtin_fmaf(-q, s, x), y, q);
+    q = __builtin_fmaf(__builtin_fmaf(-q, s, x), y, q);
+    return __builtin_copysignf(q, x);         // the corrections lose the sign of a zero
 }
 
 // Row of the pool ([page][head][offset], in rows) of a slot and head.
@@ -93,10 +108,14 @@ __global__ __launch_bounds__(kThreads) void kv_cache_write_kernel(CopyArgs a) {
     const bool finite = m < 0x7F800000u;
     float s = __uint_as_float(m) / kMaxE4m3;
     if (s == 0.0f) s = 1.0f;
+    const float y = 1.0f / s;
+    const bool normal = s >= 1.17549435e-38f;     // else 1 / s may be no number
     float q[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        q[i] = finite ? __builtin_fminf(__builtin_fmaxf(x[i] / s, -kMaxE4m3), kMaxE4m3) : 0.0f;
+    for (int i = 0; i < 8; ++i) {
+        q[i] = normal ? quotient(x[i], s, y) : x[i] / s;
+        q[i] = finite ? __builtin_fminf(__builtin_fmaxf(q[i], -kMaxE4m3), kMaxE4m3) : 0.0f;
+    }
     if (slot < 0 || slot >= a.slot_count) return;
     const int64_t row = pool_row(slot, h, a.H, a.page_shift);
     u32x2_t w;

@@ -15,8 +15,8 @@
 // a wave takes 32 keys a step, holds its own running maximum and sum, and asks
 // for the next step's keys and values while it computes.
 //  * S^T = K q^T by 16x16x32 bf16 MFMA (e4m3 and the query are exact in bf16):
-//    lane l converts the 16-byte pieces of key l & 15 that it loaded itself;
-//    the query has the same order of D in its fragments.
+//    lane l converts the 16-byte pieces of key l & 15 that it loaded itself; the
+//    query has the same order of D in its fragments.
 //  * S^T leaves lane l with keys 4 (l >> 4) + i of both 16-key tiles for row
 //    l & 15, which is the operand layout of O^T = V^T P^T when the 32 keys are
 //    summed in that order: P never leaves its lane.  V's operand needs 8 keys
@@ -88,7 +88,7 @@ template <int D>
 struct Keys {
     u32x4_t k[2][D / 64];
     typename VWord<D>::type v[2][4];
-    f32x4_t ks[2], vs[2];
+    float ks[2], vs[2];                   // of keys 4 g + lane % 4 of each tile
 };
 
 // Where a step's two 16-key tiles lie (rows of the pool), uniform.
@@ -122,7 +122,7 @@ __device__ __forceinline__ int steps_of_lane(const AttnArgs& a, int b, int first
 
 // RT: row tiles of a wave, WR: waves side by side over the rows.
 template <int D, int RT, int WR>
-__global__ __launch_bounds__(kWaves * 64, RT == 1 && D <= 128 ? 3 : 2) void tree_attn_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : RT == 1 ? 3 : 2) void tree_attn_kernel(AttnArgs a) {
     constexpr int DT = D / 16;            // 16-row tiles of O^T
     constexpr int WROWS = 16 * RT, ROWS = WROWS * WR, KW = kWaves / WR;
     constexpr int PITCH = D + 4;          // of a row of O in LDS
@@ -143,11 +143,10 @@ __global__ __launch_bounds__(kWaves * 64, RT == 1 && D <= 128 ? 3 : 2) void tree
 
     // this run's steps of all requests', and the request that they start in
     int64_t total = 0;
+    int upto = 0;                         // of the lane's request and those before it of its 64
     for (int base = 0; base < a.B; base += 64) {
-        int v = steps_of_lane(a, base + lane, block0);
-#pragma unroll
-        for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
-        total += __builtin_amdgcn_readfirstlane(v);
+        upto = sum_up_to_lane(steps_of_lane(a, base + lane, block0));
+        total += __builtin_amdgcn_readlane(upto, 63);
     }
     const int64_t runs = max((int64_t)1, min((int64_t)a.runs, total / KW));
     if (run >= runs) return;
@@ -155,18 +154,14 @@ __global__ __launch_bounds__(kWaves * 64, RT == 1 && D <= 128 ? 3 : 2) void tree
     int64_t start = 0;                    // of request b
     int b = a.B;
     for (int base = 0; base < a.B; base += 64) {
-        const int steps = steps_of_lane(a, base + lane, block0);
-        int upto = steps;                 // inclusive prefix
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int v = __shfl_up(upto, o);
-            if (lane >= o) upto += v;
-        }
-        const uint64_t hit = __ballot(base + lane < a.B && (start + upto > s0 || start + upto - steps >= s0));
+        if (a.B > 64) upto = sum_up_to_lane(steps_of_lane(a, base + lane, block0));
+        const int before = __shfl_up(upto, 1);
+        const int64_t from = start + (lane > 0 ? before : 0);
+        const uint64_t hit = __ballot(base + lane < a.B && (start + upto > s0 || from >= s0));
         if (hit != 0) {
             const int at = __builtin_ctzll(hit);
             b = base + at;
-            start += __builtin_amdgcn_readlane(upto - steps, at);
+            if (at > 0) start += __builtin_amdgcn_readlane(upto, at - 1);
             break;
         }
         start += __builtin_amdgcn_readlane(upto, 63);
@@ -215,19 +210,19 @@ __global__ __launch_bounds__(kWaves * 64, RT == 1 && D <= 128 ? 3 : 2) void tree
     }
 
     const int32_t* table = a.table + (int64_t)b * a.max_pages;
-    auto place = [&](int step) {
+    // Lanes 2 n and 2 n + 1 ask for the pages of a step's two tiles: vector loads,
+    // in the order of the others, two steps ahead.  (Scalar loads are waited for
+    // where the page is first looked at, twice a step.)
+    auto ask = [&](int step) {
+        return table[min((step * kStep + 16 * (lane & 1)) >> a.page_shift, a.max_pages - 1)];
+    };
+    auto place = [&](int step, int pages) {
         Place w;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const int j0 = step * kStep + 16 * t;
-            w.row[t] = 0;
-            w.live[t] = j0 < L;
-            if (w.live[t]) {
-                const int page = uniform_input(table + (j0 >> a.page_shift));
-                w.live[t] = page >= 0 && page < a.num_pages;
-                if (w.live[t])
-                    w.row[t] = (((int64_t)page * a.H + h) << a.page_shift) + (j0 & ((1 << a.page_shift) - 1));
-            }
+            const int j0 = step * kStep + 16 * t, page = __builtin_amdgcn_readlane(pages, t);
+            w.live[t] = j0 < L && page >= 0 && page < a.num_pages;
+            w.row[t] = w.live[t] ? (((int64_t)page * a.H + h) << a.page_shift) + (j0 & ((1 << a.page_shift) - 1)) : 0;
         }
         return w;
     };
@@ -247,25 +242,29 @@ __global__ __launch_bounds__(kWaves * 64, RT == 1 && D <= 128 ? 3 : 2) void tree
     // (past the last step the last one again), and they stay where they are
     // written: the compiler then waits for this step's loads alone.
     if (lo + kw < hi && row0 < rows) {
+    // uniform bases, a lane's place in 32 bits
+    const uint32_t k_off = r16 * D + g * 16, v_off = 4 * g * D + r16 * DT, s_off = 4 * (4 * g + (lane & 3));
     Keys<D> x;
     auto fetch_k = [&](const Place& w, int t) {
-        const uint8_t* kp = a.kc + (w.row[t] + r16) * D + g * 16;
+        const uint8_t* base = a.kc + w.row[t] * D;
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) x.k[t][c] = *reinterpret_cast<const u32x4_t*>(kp + 64 * c);
-        x.ks[t] = *reinterpret_cast<const f32x4_t*>(a.ks + w.row[t] + 4 * g);
+        for (int c = 0; c < D / 64; ++c) x.k[t][c] = *reinterpret_cast<const u32x4_t*>(base + 64 * c + k_off);
+        x.ks[t] = *reinterpret_cast<const float*>(reinterpret_cast<const char*>(a.ks + w.row[t]) + s_off);
     };
     auto fetch_v = [&](const Place& w) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const uint8_t* vp = a.vc + (w.row[t] + 4 * g) * D + r16 * DT;
+            const uint8_t* base = a.vc + w.row[t] * D;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                x.v[t][i] = *reinterpret_cast<const typename VWord<D>::type*>(vp + i * D);
-            x.vs[t] = *reinterpret_cast<const f32x4_t*>(a.vs + w.row[t] + 4 * g);
+                x.v[t][i] = *reinterpret_cast<const typename VWord<D>::type*>(base + i * D + v_off);
+            x.vs[t] = *reinterpret_cast<const float*>(reinterpret_cast<const char*>(a.vs + w.row[t]) + s_off);
         }
     };
     const int s_last = hi - 1;
-    Place at = place(lo + kw), next = place(min(lo + kw + KW, s_last));
+    int pages = ask(min(lo + kw, s_last)), pages_next = ask(min(lo + kw + KW, s_last));
+    Place at = place(min(lo + kw, s_last), pages);
+    pages = ask(min(lo + kw + 2 * KW, s_last));
     fetch_k(at, 0);
     fetch_k(at, 1);
     __builtin_amdgcn_sched_barrier(0);
@@ -273,20 +272,22 @@ __global__ __launch_bounds__(kWaves * 64, RT == 1 && D <= 128 ? 3 : 2) void tree
     __builtin_amdgcn_sched_barrier(0);
     for (int s = lo + kw; s < hi; s += KW) {
         const int j0 = s * kStep;
-        const Place after = place(min(s + 2 * KW, s_last));
+        const Place next = place(min(s + KW, s_last), pages_next);
+        pages_next = pages;
+        pages = ask(min(s + 3 * KW, s_last));
+        __builtin_amdgcn_sched_barrier(0);
         const bool all = j0 + kStep <= ctx && at.live[0] && at.live[1];   // uniform: no mask here
         float sc[RT][2][4];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             bf16x8_t kf[D / 32];
-            float kscale[4];
 #pragma unroll
             for (int c = 0; c < D / 64; ++c) {
                 kf[2 * c] = e4m3x8_to_bf16x8(x.k[u][c].x, x.k[u][c].y);
                 kf[2 * c + 1] = e4m3x8_to_bf16x8(x.k[u][c].z, x.k[u][c].w);
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) kscale[i] = x.ks[u][i] * c2;
+            const float own = x.ks[u] * c2;
+            const float kscale[4] = {of_quad<0>(own), of_quad<1>(own), of_quad<2>(own), of_quad<3>(own)};
             __builtin_amdgcn_sched_barrier(0);
             fetch_k(next, u);
             __builtin_amdgcn_sched_barrier(0);
@@ -321,19 +322,16 @@ __global__ __launch_bounds__(kWaves * 64, RT == 1 && D <= 128 ? 3 : 2) void tree
                 if (!all) {
                     // values past the end may hold anything: 0 * NaN must not reach O
 #pragma unroll
-                    for (int u = 0; u < 2; ++u)
+                    for (int u = 0; u < 2; ++u) {
+                        if (!at.live[u] || j0 + 16 * u + 4 * g + (lane & 3) >= L) x.vs[u] = 0.0f;
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            if (!at.live[u] || j0 + 16 * u + 4 * g + i >= L) {
-                                x.vs[u][i] = 0.0f;
-                                x.v[u][i] = typename VWord<D>::type(0);
-                            }
+                            if (!at.live[u] || j0 + 16 * u + 4 * g + i >= L) x.v[u][i] = typename VWord<D>::type(0);
+                    }
                 }
-                float top = 0.0f;
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) top = __builtin_fmaxf(top, x.vs[u][i]);
+                float top = __builtin_fmaxf(x.vs[0], x.vs[1]);       // over the lanes of a row, too
+                top = __builtin_fmaxf(__builtin_fmaxf(of_quad<0>(top), of_quad<1>(top)),
+                                      __builtin_fmaxf(of_quad<2>(top), of_quad<3>(top)));
                 const int now = __builtin_amdgcn_readfirstlane(__builtin_amdgcn_frexp_expf(max_of_groups(top)));
                 if (now > unit) {
                     const float f = __builtin_amdgcn_ldexpf(1.0f, max(unit - now, -1000));
@@ -344,9 +342,13 @@ __global__ __launch_bounds__(kWaves * 64, RT == 1 && D <= 128 ? 3 : 2) void tree
                     unit = now;
                 }
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) vscale[u][i] = __builtin_amdgcn_ldexpf(x.vs[u][i], 14 - unit);
+                for (int u = 0; u < 2; ++u) {
+                    const float v = __builtin_amdgcn_ldexpf(x.vs[u], 14 - unit);
+                    vscale[u][0] = of_quad<0>(v);
+                    vscale[u][1] = of_quad<1>(v);
+                    vscale[u][2] = of_quad<2>(v);
+                    vscale[u][3] = of_quad<3>(v);
+                }
             }
             float mx = m[t];
 #pragma unroll
@@ -362,19 +364,28 @@ __global__ __launch_bounds__(kWaves * 64, RT == 1 && D <= 128 ? 3 : 2) void tree
                 for (int i = 0; i < DT; ++i) acc[t][i] *= f;
                 m[t] = mx;
             }
-            u32x4_t w;
+            float p[2][4];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                float p[4];
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float e = __builtin_amdgcn_exp2f(sc[t][u][i] - base);
                     l[t] += e;
-                    p[i] = e * vscale[u][i];
-                    if (!all && sc[t][u][i] == -__builtin_inff()) p[i] = 0.0f;   // whatever its scale
+                    p[u][i] = e * vscale[u][i];
                 }
-                w[2 * u] = f32x2_to_f16x2(p[0], p[1]);
-                w[2 * u + 1] = f32x2_to_f16x2(p[2], p[3]);
+            if (!all) {
+                asm volatile("");         // a branch, not selects in every step
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (sc[t][u][i] == -__builtin_inff()) p[u][i] = 0.0f;   // whatever its scale
+            }
+            u32x4_t w;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                w[2 * u] = f32x2_to_f16x2(p[u][0], p[u][1]);
+                w[2 * u + 1] = f32x2_to_f16x2(p[u][2], p[u][3]);
             }
             pf[t] = __builtin_bit_cast(f16x8_t, w);
         }
@@ -405,7 +416,6 @@ __global__ __launch_bounds__(kWaves * 64, RT == 1 && D <= 128 ? 3 : 2) void tree
         fetch_v(next);
         __builtin_amdgcn_sched_barrier(0);
         at = next;
-        next = after;
     }
     }
 
@@ -515,41 +525,68 @@ __global__ __launch_bounds__(kWaves * 64, RT == 1 && D <= 128 ? 3 : 2) void tree
     }
 }
 
-// Joins the parts of requests that were split: D / 4 threads a row.
-template <int D>
+// Joins the parts of requests that were split: D / 4 threads a row and SIDE of
+// them side by side, which go through the parts with a running maximum, four at
+// a time, and meet in LDS.
+template <int D, int SIDE>
 __global__ __launch_bounds__(256) void tree_attn_join_kernel(AttnArgs a, int rows_of_block) {
-    constexpr int TPR = D / 4;
+    constexpr int TPR = D / 4, RPB = 256 / (TPR * SIDE);
+    static_assert(SIDE == 1 || RPB == 1, "threads that meet return together");
+    __shared__ f32x4_t sm_v[SIDE > 1 ? 256 : 1];
+    __shared__ float sm_ml[SIDE > 1 ? 256 : 1][2];
     const int all_rows = a.N * a.G;
-    const int64_t id = (int64_t)blockIdx.x * (256 / TPR) + threadIdx.x / TPR;   // (b, h, row)
-    const int d = threadIdx.x % TPR * 4;
+    const int side = threadIdx.x / TPR % SIDE, d = threadIdx.x % TPR * 4;
+    const int64_t id = (int64_t)blockIdx.x * RPB + threadIdx.x / (TPR * SIDE);   // (b, h, row)
     if (id >= (int64_t)a.B * a.H * all_rows) return;
     const int64_t bh = id / all_rows;
     const int r = (int)(id - bh * all_rows), b = (int)(bh / a.H), h = (int)(bh - (int64_t)b * a.H);
     const int rb = r / rows_of_block, in_block = r - rb * rows_of_block;
     const int2 split = a.split[bh * a.row_blocks + rb];
-    if (split.y < split.x) return;        // one run, or nothing: written
     const int n = a.tree ? min(max(a.tree[b], 0), a.N) : a.N;
+    if (split.y < split.x) return;        // one run, or nothing: written
     const int64_t part = (int64_t)rows_of_block * (D + 2), next = (int64_t)a.H * a.row_blocks * 2 * part;
     const float* at = a.parts + ((int64_t)split.x * a.H + h) * a.row_blocks * 2 * part + rb * 2 * part;
     const int parts = split.y - split.x + 1;
-    // part u: the second place of the first run, then the first places
-    auto of = [&](int u) { return at + u * next + (u == 0 ? part : 0); };
     const int ml = rows_of_block * D + 2 * in_block, o = in_block * D + d;
-    float top = -__builtin_inff();
-#pragma unroll 8
-    for (int u = 0; u < parts; ++u) top = __builtin_fmaxf(top, of(u)[ml]);
-    const bool none = r >= n * a.G || top == -__builtin_inff();
-    float sum = 0.0f;
+    float top = -__builtin_inff(), sum = 0.0f;
     f32x4_t v = {0, 0, 0, 0};
-#pragma unroll 8
-    for (int u = 0; u < parts; ++u) {
-        const f32x2_t x = *reinterpret_cast<const f32x2_t*>(of(u) + ml);
-        const f32x4_t w = *reinterpret_cast<const f32x4_t*>(of(u) + o);
-        const float f = x.x == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(x.x - top);   // a part may see nothing
-        sum = __builtin_fmaf(x.y, f, sum);
+    // adds a partial sum with its maximum; a part that saw nothing has none
+    auto add = [&](float m, float l, f32x4_t w) {
+        if (m == -__builtin_inff()) return;
+        const float t = __builtin_fmaxf(top, m);
+        const float f = __builtin_amdgcn_exp2f(top - t), g = __builtin_amdgcn_exp2f(m - t);
+        top = t;
+        sum = sum * f + l * g;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf(w[i], f, v[i]);
+        for (int i = 0; i < 4; ++i) v[i] = v[i] * f + w[i] * g;
+    };
+    for (int u0 = side; u0 < parts; u0 += 4 * SIDE) {
+        f32x2_t x[4];
+        f32x4_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            // part u: the second place of the first run, then the first places
+            const int u = min(u0 + k * SIDE, parts - 1);
+            const float* from = at + u * next + (u == 0 ? part : 0);
+            x[k] = *reinterpret_cast<const f32x2_t*>(from + ml);
+            w[k] = *reinterpret_cast<const f32x4_t*>(from + o);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (u0 + k * SIDE < parts) add(x[k].x, x[k].y, w[k]);
     }
+    if constexpr (SIDE > 1) {
+        sm_v[threadIdx.x] = v;
+        sm_ml[threadIdx.x][0] = top;
+        sm_ml[threadIdx.x][1] = sum;
+        __syncthreads();
+        if (side > 0) return;
+        for (int k = 1; k < SIDE; ++k) {
+            const int from = threadIdx.x + k * TPR;
+            add(sm_ml[from][0], sm_ml[from][1], sm_v[from]);
+        }
+    }
+    const bool none = r >= n * a.G || top == -__builtin_inff();
     const float inv = none ? 0.0f : 1.0f / sum;
     const int64_t to = ((int64_t)b * a.N + r / a.G) * a.H * a.G + h * a.G + r % a.G;
     u32x2_t w = {0, 0};
@@ -568,8 +605,9 @@ struct Shape {
 
 // Rows: 16 a wave up to 16 (and for D = 256, whose O fills the registers), else
 // 32; as many waves over the rows as there are.  Runs: two workgroups a CU of
-// 256, three where the registers allow it (one row tile); no run is shorter than
-// one step a wave.  From the sizes alone: lengths are on the device.
+// 256 (one for D = 256); no run is shorter than one step a wave.  Three a CU fit
+// for one row tile, but more parts to join and more places read at once cost 3 to
+// 10%.  From the sizes alone: lengths are on the device.
 Shape shape_of(int64_t B, int64_t N, int64_t Hq, int64_t H, int64_t D, int64_t max_pages, int64_t page_size) {
     const int64_t rows = N * (Hq / H);
     Shape s;
@@ -578,7 +616,7 @@ Shape shape_of(int64_t B, int64_t N, int64_t Hq, int64_t H, int64_t D, int64_t m
     s.row_waves = waves <= 1 ? 1 : waves <= 2 ? 2 : 4;
     s.row_blocks = (int)((rows + s.rows() - 1) / s.rows());
     const int64_t groups = H * s.row_blocks, steps = B * ((max_pages * page_size + kStep - 1) / kStep);
-    const int64_t wanted = s.row_tiles == 1 && D <= 128 ? 768 : 512;
+    const int64_t wanted = D == 256 ? 256 : 512;
     s.runs = (int)std::max<int64_t>(1, std::min((wanted + groups - 1) / groups, steps * s.row_waves / kWaves));
     return s;
 }
@@ -601,9 +639,13 @@ hipError_t launch(const AttnArgs& a, const Shape& s, hipStream_t stream) {
     if (D <= 128 && s.row_tiles == 2) e = launch<D, D <= 128 ? 2 : 1>(a, s.row_waves, stream);
     else e = launch<D, 1>(a, s.row_waves, stream);
     if (e != hipSuccess || a.runs == 1) return e;
+    // few rows have many parts each: a workgroup a row, else a thread for each four values
     const int64_t rows = (int64_t)a.B * a.H * a.N * a.G, per = 256 / (D / 4);
-    hipLaunchKernelGGL((tree_attn_join_kernel<D>), dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0,
-                       stream, a, s.rows());
+    if (rows <= 4096)
+        hipLaunchKernelGGL((tree_attn_join_kernel<D, 1024 / D>), dim3((unsigned)rows), dim3(256), 0, stream, a, s.rows());
+    else
+        hipLaunchKernelGGL((tree_attn_join_kernel<D, 1>), dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0,
+                           stream, a, s.rows());
     return hipGetLastError();
 }
 
