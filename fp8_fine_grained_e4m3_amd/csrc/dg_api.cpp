@@ -677,7 +677,7 @@ static dg_status kv_cache_copy(dg::KvCopy p, dg_dtype dtype, bool write, void* s
     const int32_t* slots = p.slots;
     REQUIRE_PTR(k, 16);
     REQUIRE_PTR(v, 16);
-    REQUIRE_PTR(slots, 16);
+    REQUIRE_PTR(slots, 4);
     st = check_cache(p.cache);
     if (st != DG_OK) return st;
     REQUIRE(p.T <= INT_MAX / H, "T * H must stay below 2^31");
@@ -779,12 +779,12 @@ dg_status dg_fp8_tree_attention(const void* q, int64_t q_stride, const uint8_t* 
     REQUIRE_PTR(q, 16);
     dg_status st = check_cache(p.cache);
     if (st != DG_OK) return st;
-    REQUIRE_PTR(page_table, 16);
-    REQUIRE_PTR(context_lens, 16);
-    if (tree_lens) REQUIRE_PTR(tree_lens, 16);
-    if (tree_mask) REQUIRE_PTR(tree_mask, 16);
+    REQUIRE_PTR(page_table, 4);
+    REQUIRE_PTR(context_lens, 4);
+    if (tree_lens) REQUIRE_PTR(tree_lens, 4);
+    if (tree_mask) REQUIRE_PTR(tree_mask, 8);
     REQUIRE_PTR(o, 16);
-    REQUIRE_PTR(lse, 16);
+    REQUIRE_PTR(lse, 4);
     const int64_t need = dg::tree_attn_workspace_bytes(B, N, Hq, H, D, max_pages, page_size);
     REQUIRE(workspace_bytes >= need, "workspace_bytes=%lld < %lld needed for these sizes",
             (long long)workspace_bytes, (long long)need);
@@ -848,8 +848,8 @@ dg_status dg_fp8_moe_few_tokens(const void* x, const uint8_t* w1, const float* s
     REQUIRE_PTR(s1, 16);
     REQUIRE_PTR(w2, 16);
     REQUIRE_PTR(s2, 16);
-    REQUIRE_PTR(topk_ids, 16);
-    REQUIRE_PTR(topk_weights, 16);
+    REQUIRE_PTR(topk_ids, 4);
+    REQUIRE_PTR(topk_weights, 4);
     REQUIRE_PTR(y, 16);
     const int64_t need = dg::moe_few_workspace_bytes(T, topk, E, H, I);
     REQUIRE(workspace != nullptr, "workspace is NULL: %lld bytes are needed "

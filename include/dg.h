@@ -433,7 +433,9 @@ dg_status dg_fp8_mqa_logits(const uint8_t* q, const uint8_t* kv, const float* kv
  * Few tokens at a time: the FP8 key/value cache, attention for drafted tokens
  * over it, and a mixture-of-experts layer.  The conventions above hold (device
  * pointers, 16-byte alignment, stream, errors, no allocation, no
- * synchronisation); calls may be captured into a HIP graph.
+ * synchronisation); calls may be captured into a HIP graph.  Indices, lengths,
+ * masks, topk_weights and lse need their own type's alignment only, so that
+ * slices of a longer array will do.
  *
  * The cache is paged.  For the keys and for the values:
  *   codes [num_pages, H, page_size, D]  e4m3

@@ -525,3 +525,31 @@ def test_on_another_stream():
         step(s)
     torch.cuda.current_stream().wait_stream(other)
     assert all(same_bits(a, b) for a, b in zip(want, outputs(s)))
+
+
+def test_slices_of_indices_lengths_masks_and_weights():
+    """Small arrays at any element of a longer one."""
+    announce("slices")
+    s = decode_state(2)
+    N = s["q"].shape[1]
+    s["mask"] = dev(ft.pack_mask(np.stack([ft.random_tree(np.random.default_rng(b), N) for b in range(5)])))
+
+    def run(s, o):
+        step(s)
+        dg.fp8_tree_attention(s["q"], s["cache"], s["table"], s["ctx"], s["lens"], s["mask"], out=o, workspace=s["ws_a"])
+
+    def aside(t):
+        wide = torch.zeros(t.numel() + 1, dtype=t.dtype, device="cuda")
+        wide[1:] = t.reshape(-1)
+        return wide[1:].view(t.shape)
+
+    want_o = tuple(torch.empty_like(t) for t in s["o"])
+    run(s, want_o)
+    want = [t.clone() for t in (*outputs(s), *want_o)]
+    for name in ("slots", "table", "ctx", "lens", "mask", "ids", "wt"):
+        s[name] = aside(s[name])
+        assert s[name].data_ptr() % 16
+    s["o"] = (s["o"][0], aside(s["o"][1]))
+    o = (torch.empty_like(want_o[0]), aside(want_o[1]))
+    run(s, o)
+    assert all(same_bits(a, b) for a, b in zip(want, (*outputs(s), *o)))
