@@ -67,14 +67,17 @@ class Decoder:
         live = at < tree_lens[:, None]
         slots = self.slots(table, torch.where(live, context_lens[:, None] + at, -1)).reshape(-1)
         Q, KV, D = self.heads, self.kv_heads, self.head_dim
-        x = self.embed[tokens].reshape(B * N, -1)
+        embedded = self.embed[tokens].reshape(B * N, -1)
+        x = embedded
         for layer in self.layers:
             qkv = self.linear(self.norm(x), layer["qkv"]).view(B * N, Q + 2 * KV, D)
             dg.fp8_kv_cache_write(qkv[:, Q:Q + KV], qkv[:, Q + KV:], layer["cache"], slots)
             o, _ = dg.fp8_tree_attention(qkv[:, :Q].unflatten(0, (B, N)), layer["cache"], table, context_lens, tree_lens, mask)
             x = x + self.linear(o.view(B * N, Q * D), layer["out"])
             rows = self.norm(x)
-            weights, ids = torch.topk(torch.softmax(rows.float() @ layer["router"].t(), -1), self.topk)
+            # routed by the token alone: by the hidden row, a near tie would send a row to other
+            # experts on one way than on the other, and they could not be compared
+            weights, ids = torch.topk(torch.softmax(embedded.float() @ layer["router"].t(), -1), self.topk)
             weights = weights / weights.sum(-1, keepdim=True)
             ids = torch.where(live.reshape(-1, 1), ids, -1).int()
             x = x + dg.fp8_moe_few_tokens(rows, layer["up"], layer["down"], ids, weights)
