@@ -25,14 +25,20 @@
 //    keeps its row order.
 //  * P, times the values' scales, is rounded to fp16 for the second product (e4m3
 //    is exact in fp16 too): 11 bits, against bf16's 8, keep its rounding below
-//    the output's.  fp16 has few exponents, so P vs 2^(14 - x) is what is
+//    the output's.  fp16 has few exponents, so P vs 2^(11 - x) is what is
 //    rounded, x the exponent of the largest scale that the wave has met: terms
-//    down to 2^-38 of the largest possible one count.  Maximum, sum and O are
+//    down to 2^-35 of the largest possible one count.  Maximum, sum and O are
 //    fp32.
-// A wave has 16 or 32 rows.  A workgroup's four waves share the steps of up to 32
-// rows and add up in LDS, or take two times 32 rows, or four times, where there
-// are more: then a fetched key serves 128 rows from the caches, and the VALU
-// (widening keys and values, exponentials) is the bound.
+//  * Scores are checked against the running maximum in their own lanes, and the
+//    maximum follows, with the exchange and the scaling of O that this takes, only
+//    where one passes it by 2^4 or more: in nearly every step it does not.  P's
+//    range leaves those 4 powers of two free.
+// A workgroup has 16 or 32 rows, and its four waves share their steps and add up
+// in LDS.  More rows than that are further workgroups beside it, which find the
+// keys in the XCD's cache: all of 128 rows' waves in one workgroup, each with 32
+// of them and all steps, leave less to join within it but four times the parts
+// to join through memory (one request of 40 tokens over 20000: 55 us against 40).
+// With many rows the VALU (widening keys and values, exponentials) is the bound.
 //
 // Requests differ in length, so the steps of all of them, end to end, are cut
 // into equal runs, one a workgroup for each key head: a workgroup goes through
@@ -45,12 +51,15 @@
 #include "serve_internal.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace dg {
 namespace {
 
 constexpr int kWaves = 4;
 constexpr int kStep = 32;                 // keys of a wave's step
+constexpr int kTop = 11;                  // P of a value with the largest scale is below 2^(kTop + kLazy)
+constexpr float kLazy = 4.0f;             // how far, in powers of two, scores pass m before m follows
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -120,41 +129,40 @@ __device__ __forceinline__ int steps_of_lane(const AttnArgs& a, int b, int first
     return b < a.B ? request_of(a, a.ctx[b], a.tree ? a.tree[b] : a.N, first_row).steps : 0;
 }
 
-// RT: row tiles of a wave, WR: waves side by side over the rows.
-template <int D, int RT, int WR>
-__global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : RT == 1 ? 3 : 2) void tree_attn_kernel(AttnArgs a) {
+// RT: row tiles, of each of a workgroup's waves the same.
+template <int D, int RT>
+__global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : D == 128 ? 2 : 3) void tree_attn_kernel(AttnArgs a) {
     constexpr int DT = D / 16;            // 16-row tiles of O^T
-    constexpr int WROWS = 16 * RT, ROWS = WROWS * WR, KW = kWaves / WR;
+    constexpr int ROWS = 16 * RT;
     constexpr int PITCH = D + 4;          // of a row of O in LDS
     constexpr int PART = ROWS * (D + 2);  // floats of a part
-    __shared__ __attribute__((aligned(16))) float sm_o[KW > 1 ? ROWS * PITCH : 1];
-    __shared__ float sm_ml[KW > 1 ? kWaves : 1][WROWS][2];
+    __shared__ __attribute__((aligned(16))) float sm_o[kWaves][ROWS * PITCH];
+    __shared__ f32x2_t sm_ml[kWaves][ROWS];
     const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wr = wave % WR, kw = wave / WR;
     // The row blocks of a run follow one another on one XCD (workgroups go to the
     // eight in turn), whose cache then has their keys.
     const int in_xcd = blockIdx.x >> 3, rb = in_xcd % a.row_blocks;
     const int run_head = (in_xcd / a.row_blocks) * 8 + (blockIdx.x & 7);
     if (run_head >= a.runs * a.H) return;
     const int run = run_head / a.H, h = run_head - run * a.H;
-    const int block0 = rb * ROWS, row0 = block0 + wr * WROWS;
+    const int row0 = rb * ROWS;
     const int all_rows = a.N * a.G, Hq = a.H * a.G;
 
     // this run's steps of all requests', and the request that they start in
     int64_t total = 0;
     int upto = 0;                         // of the lane's request and those before it of its 64
     for (int base = 0; base < a.B; base += 64) {
-        upto = sum_up_to_lane(steps_of_lane(a, base + lane, block0));
+        upto = sum_up_to_lane(steps_of_lane(a, base + lane, row0));
         total += __builtin_amdgcn_readlane(upto, 63);
     }
-    const int64_t runs = max((int64_t)1, min((int64_t)a.runs, total / KW));
+    const int64_t runs = max((int64_t)1, min((int64_t)a.runs, total / kWaves));
     if (run >= runs) return;
     const int64_t s0 = total * run / runs, s1 = total * (run + 1) / runs;
     int64_t start = 0;                    // of request b
     int b = a.B;
     for (int base = 0; base < a.B; base += 64) {
-        if (a.B > 64) upto = sum_up_to_lane(steps_of_lane(a, base + lane, block0));
+        if (a.B > 64) upto = sum_up_to_lane(steps_of_lane(a, base + lane, row0));
         const int before = __shfl_up(upto, 1);
         const int64_t from = start + (lane > 0 ? before : 0);
         const uint64_t hit = __ballot(base + lane < a.B && (start + upto > s0 || from >= s0));
@@ -168,7 +176,7 @@ __global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : RT == 1 ? 3 : 2) void t
     }
 
     for (; b < a.B && (start < s1 || (run == runs - 1 && start == total)); ++b) {
-    const Request rq = request(a, b, block0);
+    const Request rq = request(a, b, row0);
     const int ctx = rq.ctx, L = rq.L, rows = rq.n * a.G;
     const int lo = (int)max(s0 - start, (int64_t)0), hi = (int)min(s1 - start, (int64_t)rq.steps);
     start += rq.steps;
@@ -181,7 +189,7 @@ __global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : RT == 1 ? 3 : 2) void t
     }
     if (rq.steps == 0) {                  // no row of the block sees anything
         for (int i = threadIdx.x; i < ROWS * D / 8; i += kWaves * 64) {
-            const int r = block0 + i / (D / 8);
+            const int r = row0 + i / (D / 8);
             if (r >= all_rows) break;
             const int64_t at = out_row(r);
             *reinterpret_cast<u32x4_t*>(a.o + at * D + i % (D / 8) * 8) = u32x4_t{0, 0, 0, 0};
@@ -226,13 +234,14 @@ __global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : RT == 1 ? 3 : 2) void t
         }
         return w;
     };
-    f32x4_t acc[RT][DT];                  // in units of 2^(unit - 14)
-    float m[RT], l[RT];
+    f32x4_t acc[RT][DT];                  // in units of 2^(unit - kTop)
+    float m[RT], base[RT], l[RT];         // base: m, or 0 while nothing was seen, so that exp2 stays 0
     int unit = -1000;
+    float largest = 0.0f;                 // 2^unit
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
         m[t] = -__builtin_inff();
-        l[t] = 0.0f;
+        base[t] = l[t] = 0.0f;
 #pragma unroll
         for (int i = 0; i < DT; ++i) acc[t][i] = f32x4_t{0, 0, 0, 0};
     }
@@ -241,7 +250,7 @@ __global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : RT == 1 ? 3 : 2) void t
     // product, its values when they are in the second.  Neither is conditional
     // (past the last step the last one again), and they stay where they are
     // written: the compiler then waits for this step's loads alone.
-    if (lo + kw < hi && row0 < rows) {
+    if (lo + wave < hi) {
     // uniform bases, a lane's place in 32 bits
     const uint32_t k_off = r16 * D + g * 16, v_off = 4 * g * D + r16 * DT, s_off = 4 * (4 * g + (lane & 3));
     Keys<D> x;
@@ -262,19 +271,19 @@ __global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : RT == 1 ? 3 : 2) void t
         }
     };
     const int s_last = hi - 1;
-    int pages = ask(min(lo + kw, s_last)), pages_next = ask(min(lo + kw + KW, s_last));
-    Place at = place(min(lo + kw, s_last), pages);
-    pages = ask(min(lo + kw + 2 * KW, s_last));
+    int pages = ask(min(lo + wave, s_last)), pages_next = ask(min(lo + wave + kWaves, s_last));
+    Place at = place(min(lo + wave, s_last), pages);
+    pages = ask(min(lo + wave + 2 * kWaves, s_last));
     fetch_k(at, 0);
     fetch_k(at, 1);
     __builtin_amdgcn_sched_barrier(0);
     fetch_v(at);
     __builtin_amdgcn_sched_barrier(0);
-    for (int s = lo + kw; s < hi; s += KW) {
+    for (int s = lo + wave; s < hi; s += kWaves) {
         const int j0 = s * kStep;
-        const Place next = place(min(s + KW, s_last), pages_next);
+        const Place next = place(min(s + kWaves, s_last), pages_next);
         pages_next = pages;
-        pages = ask(min(s + 3 * KW, s_last));
+        pages = ask(min(s + 3 * kWaves, s_last));
         __builtin_amdgcn_sched_barrier(0);
         const bool all = j0 + kStep <= ctx && at.live[0] && at.live[1];   // uniform: no mask here
         float sc[RT][2][4];
@@ -300,11 +309,10 @@ __global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : RT == 1 ? 3 : 2) void t
                 for (int i = 0; i < 4; ++i) sc[t][u][i] = p[i] * kscale[i];
             }
         }
-        f16x8_t pf[RT];
-        float vscale[2][4];
+        if (!all) {
+            const int g = fresh(lane) >> 4;
 #pragma unroll
-        for (int t = 0; t < RT; ++t) {
-            if (!all) {
+            for (int t = 0; t < RT; ++t)
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -317,78 +325,87 @@ __global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : RT == 1 ? 3 : 2) void t
                                           : d <= tok[t];
                         if (!seen) sc[t][u][i] = -__builtin_inff();
                     }
+            // values past the end may hold anything: 0 * NaN must not reach O
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (!at.live[u] || j0 + 16 * u + 4 * g + (lane & 3) >= L) x.vs[u] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (!at.live[u] || j0 + 16 * u + 4 * g + i >= L) x.v[u][i] = typename VWord<D>::type(0);
             }
-            if (t == 0) {                 // the values' scales, in units of the largest so far
-                if (!all) {
-                    // values past the end may hold anything: 0 * NaN must not reach O
+        }
+        // A wave in its softmax goes before one in its products, which the matrix unit
+        // holds up anyway (1 to 2%).
+        __builtin_amdgcn_s_setprio(1);
+        // Whether a score or a value's scale outgrows what O is relative to.  The
+        // lanes look at their own; only then is the row's maximum exchanged.
+        float mx[RT];
+        const float top = __builtin_fmaxf(x.vs[0], x.vs[1]);
+        bool over = top > largest;
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        if (!at.live[u] || j0 + 16 * u + 4 * g + (lane & 3) >= L) x.vs[u] = 0.0f;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (!at.live[u] || j0 + 16 * u + 4 * g + i >= L) x.v[u][i] = typename VWord<D>::type(0);
-                    }
-                }
-                float top = __builtin_fmaxf(x.vs[0], x.vs[1]);       // over the lanes of a row, too
-                top = __builtin_fmaxf(__builtin_fmaxf(of_quad<0>(top), of_quad<1>(top)),
-                                      __builtin_fmaxf(of_quad<2>(top), of_quad<3>(top)));
-                const int now = __builtin_amdgcn_readfirstlane(__builtin_amdgcn_frexp_expf(max_of_groups(top)));
-                if (now > unit) {
-                    const float f = __builtin_amdgcn_ldexpf(1.0f, max(unit - now, -1000));
-#pragma unroll
-                    for (int r = 0; r < RT; ++r)
-#pragma unroll
-                        for (int i = 0; i < DT; ++i) acc[r][i] *= f;
-                    unit = now;
-                }
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const float v = __builtin_amdgcn_ldexpf(x.vs[u], 14 - unit);
-                    vscale[u][0] = of_quad<0>(v);
-                    vscale[u][1] = of_quad<1>(v);
-                    vscale[u][2] = of_quad<2>(v);
-                    vscale[u][3] = of_quad<3>(v);
-                }
-            }
-            float mx = m[t];
+        for (int t = 0; t < RT; ++t) {
+            mx[t] = sc[t][0][0];
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) mx = __builtin_fmaxf(mx, sc[t][u][i]);
-            mx = max_of_groups(mx);
-            const float base = mx == -__builtin_inff() ? 0.0f : mx;   // nothing seen yet: exp2 stays 0
-            if (__any(mx != m[t])) {
-                const float f = __builtin_amdgcn_exp2f(m[t] - base);
+                for (int i = 0; i < 4; ++i) mx[t] = __builtin_fmaxf(mx[t], sc[t][u][i]);
+            over |= mx[t] > m[t] + kLazy;
+        }
+        if (__any(over)) {
+            float far = __builtin_fmaxf(__builtin_fmaxf(of_quad<0>(top), of_quad<1>(top)),
+                                        __builtin_fmaxf(of_quad<2>(top), of_quad<3>(top)));
+            far = max_of_groups(__builtin_fmaxf(far, largest));
+            const int now = far > largest ? __builtin_amdgcn_readfirstlane(__builtin_amdgcn_frexp_expf(far)) : unit;
+            const float shrink = __builtin_amdgcn_ldexpf(1.0f, max(unit - now, -1000));
+            unit = now;
+            if (far > largest) largest = __builtin_amdgcn_ldexpf(1.0f, now);
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+                mx[t] = __builtin_fmaxf(max_of_groups(mx[t]), m[t]);
+                if (mx[t] != -__builtin_inff()) base[t] = mx[t];
+                const float f = __builtin_amdgcn_exp2f(m[t] - base[t]);
                 l[t] *= f;
 #pragma unroll
-                for (int i = 0; i < DT; ++i) acc[t][i] *= f;
-                m[t] = mx;
+                for (int i = 0; i < DT; ++i) acc[t][i] *= f * shrink;
+                m[t] = mx[t];
             }
-            float p[2][4];
+        }
+        float vscale[2][4];               // in units of the largest so far
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < 2; ++u) {
+            const float v = __builtin_amdgcn_ldexpf(x.vs[u], kTop - unit);
+            vscale[u][0] = of_quad<0>(v);
+            vscale[u][1] = of_quad<1>(v);
+            vscale[u][2] = of_quad<2>(v);
+            vscale[u][3] = of_quad<3>(v);
+        }
+        f16x8_t pf[RT];
+        auto weigh = [&](auto some_hidden) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float e = __builtin_amdgcn_exp2f(sc[t][u][i] - base);
-                    l[t] += e;
-                    p[u][i] = e * vscale[u][i];
-                }
-            if (!all) {
-                asm volatile("");         // a branch, not selects in every step
+            for (int t = 0; t < RT; ++t) {
+                float p[2][4];
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (sc[t][u][i] == -__builtin_inff()) p[u][i] = 0.0f;   // whatever its scale
-            }
-            u32x4_t w;
+                    for (int i = 0; i < 4; ++i) {
+                        const float e = __builtin_amdgcn_exp2f(sc[t][u][i] - base[t]);
+                        l[t] += e;
+                        p[u][i] = e * vscale[u][i];
+                        // a hidden key's weight is 0 whatever its value's scale
+                        if (decltype(some_hidden)::value && sc[t][u][i] == -__builtin_inff()) p[u][i] = 0.0f;
+                    }
+                u32x4_t w;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                w[2 * u] = f32x2_to_f16x2(p[u][0], p[u][1]);
-                w[2 * u + 1] = f32x2_to_f16x2(p[u][2], p[u][3]);
+                for (int u = 0; u < 2; ++u) {
+                    w[2 * u] = f32x2_to_f16x2(p[u][0], p[u][1]);
+                    w[2 * u + 1] = f32x2_to_f16x2(p[u][2], p[u][3]);
+                }
+                pf[t] = __builtin_bit_cast(f16x8_t, w);
             }
-            pf[t] = __builtin_bit_cast(f16x8_t, w);
-        }
+        };
+        if (all) weigh(std::false_type());
+        else weigh(std::true_type());
+        __builtin_amdgcn_s_setprio(0);
         // V^T: tile i takes D value r16 * DT + i of the lane's 8 keys
 #pragma unroll
         for (int w = 0; w < DT / 4; ++w)
@@ -400,10 +417,9 @@ __global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : RT == 1 ? 3 : 2) void t
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const uint32_t ka = x.v[u][2 * i][w], kb = x.v[u][2 * i + 1][w];
-                        const uint32_t va = half ? e4m3x2_to_f16x2<true>(ka) : e4m3x2_to_f16x2<false>(ka);
-                        const uint32_t vb = half ? e4m3x2_to_f16x2<true>(kb) : e4m3x2_to_f16x2<false>(kb);
-                        even[2 * u + i] = __builtin_amdgcn_perm(vb, va, 0x05040100u);
-                        odd[2 * u + i] = __builtin_amdgcn_perm(vb, va, 0x07060302u);
+                        const uint32_t both = __builtin_amdgcn_perm(kb, ka, half ? 0x07030602u : 0x05010400u);
+                        even[2 * u + i] = e4m3x2_to_f16x2<false>(both);
+                        odd[2 * u + i] = e4m3x2_to_f16x2<true>(both);
                     }
                 const int i = 4 * w + 2 * half;
 #pragma unroll
@@ -419,109 +435,53 @@ __global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : RT == 1 ? 3 : 2) void t
     }
     }
 
+    // The waves put down their O and meet: a thread then adds up four values of a
+    // row, wave by wave, relative to the largest of the four maxima.
     const int elane = fresh(lane), er16 = elane & 15, eg = elane >> 4;
-    // Join the waves of the same rows, in order, in the first one's registers; a
-    // row's O becomes relative to the largest maximum and loses its unit.
-#pragma unroll
-    for (int t = 0; t < RT; ++t) l[t] = sum_of_groups(l[t]);
-    if constexpr (KW > 1) {
-        if (eg == 0)
-#pragma unroll
-            for (int t = 0; t < RT; ++t) {
-                sm_ml[wave][16 * t + er16][0] = m[t];
-                sm_ml[wave][16 * t + er16][1] = l[t];
-            }
-        __syncthreads();
-    }
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-        float top = m[t];
-        if constexpr (KW > 1)
-#pragma unroll
-            for (int k = 0; k < KW; ++k) top = __builtin_fmaxf(top, sm_ml[k * WR + wr][16 * t + er16][0]);
-        const float f = m[t] == -__builtin_inff() ? 0.0f
-                                                  : __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f(m[t] - top), unit - 14);
-#pragma unroll
-        for (int i = 0; i < DT; ++i) acc[t][i] *= f;
-        if constexpr (KW > 1) {
-            l[t] = 0.0f;
-#pragma unroll
-            for (int k = 0; k < KW; ++k) {
-                const float mk = sm_ml[k * WR + wr][16 * t + er16][0];
-                if (mk != -__builtin_inff())
-                    l[t] += sm_ml[k * WR + wr][16 * t + er16][1] * __builtin_amdgcn_exp2f(mk - top);
-            }
-        }
-        m[t] = top;
-    }
-    if constexpr (KW > 1) {
-        float* mine = sm_o + (wr * WROWS + er16) * PITCH + 4 * eg * DT;
-#pragma unroll 1
-        for (int k = 1; k < KW; ++k) {
-            if (kw == k)
-#pragma unroll
-                for (int t = 0; t < RT; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int c = 0; c < DT / 4; ++c)
-                            *reinterpret_cast<f32x4_t*>(mine + 16 * t * PITCH + i * DT + 4 * c) =
-                                f32x4_t{acc[t][4 * c][i], acc[t][4 * c + 1][i], acc[t][4 * c + 2][i], acc[t][4 * c + 3][i]};
-            __syncthreads();
-            if (kw == 0)
-#pragma unroll
-                for (int t = 0; t < RT; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int c = 0; c < DT / 4; ++c) {
-                            const f32x4_t v = *reinterpret_cast<const f32x4_t*>(mine + 16 * t * PITCH + i * DT + 4 * c);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) acc[t][4 * c + e][i] += v[e];
-                        }
-            __syncthreads();
-        }
-    }
-
-    // O, sum and maximum of a row, 4 x DT values a elane, as the output
-    auto write = [&](int t, const f32x4_t (&v)[DT], float top, float sum) {
-        const int r = row0 + 16 * t + er16;
-        if (r >= all_rows) return;
-        const bool none = r >= rows || top == -__builtin_inff();
-        const float inv = none ? 0.0f : 1.0f / sum;
-        const int64_t at = out_row(r);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int c = 0; c < DT / 4; ++c) {
-                u32x2_t w = {0, 0};
-                if (!none)
-                    w = u32x2_t{f32x2_to_bf16x2(v[4 * c][i] * inv, v[4 * c + 1][i] * inv),
-                                f32x2_to_bf16x2(v[4 * c + 2][i] * inv, v[4 * c + 3][i] * inv)};
-                *reinterpret_cast<u32x2_t*>(a.o + at * D + (4 * eg + i) * DT + 4 * c) = w;
-            }
-        if (eg == 0) a.lse[at] = none ? -__builtin_inff() : (top + __builtin_amdgcn_logf(sum)) * kLn2;
-    };
-    if (kw != 0) continue;
-    if (whole) {
-#pragma unroll
-        for (int t = 0; t < RT; ++t) write(t, acc[t], m[t], l[t]);
-        continue;
-    }
-    // A run has one part of a request that goes on from the run before (the first
-    // of its two places) and one of a request that begins in it (the second).
-    float* part = a.parts + (((int64_t)run_head * a.row_blocks + rb) * 2 + (lo > 0 ? 0 : 1)) * PART;
-#pragma unroll
-    for (int t = 0; t < RT; ++t) {
-        const int r = wr * WROWS + 16 * t + er16;
+        l[t] = sum_of_groups(l[t]);
+        if (eg == 0) sm_ml[wave][16 * t + er16] = f32x2_t{m[t], l[t]};
+        const float f = __builtin_amdgcn_ldexpf(1.0f, max(unit - kTop, -1000));
+        float* mine = sm_o[wave] + (16 * t + er16) * PITCH + 4 * eg * DT;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int c = 0; c < DT / 4; ++c)
-                *reinterpret_cast<f32x4_t*>(part + r * D + (4 * eg + i) * DT + 4 * c) =
-                    f32x4_t{acc[t][4 * c][i], acc[t][4 * c + 1][i], acc[t][4 * c + 2][i], acc[t][4 * c + 3][i]};
-        if (eg == 0) *reinterpret_cast<f32x2_t*>(part + ROWS * D + 2 * r) = f32x2_t{m[t], l[t]};
+                *reinterpret_cast<f32x4_t*>(mine + i * DT + 4 * c) =
+                    f32x4_t{acc[t][4 * c][i] * f, acc[t][4 * c + 1][i] * f, acc[t][4 * c + 2][i] * f, acc[t][4 * c + 3][i] * f};
     }
+    __syncthreads();
+    // A run has one part of a request that goes on from the run before (the first
+    // of its two places) and one of a request that begins in it (the second).
+    float* part = a.parts + (((int64_t)run_head * a.row_blocks + rb) * 2 + (lo > 0 ? 0 : 1)) * PART;
+    for (int i = fresh(threadIdx.x); i < ROWS * D / 4; i += kWaves * 64) {
+        const int r = i / (D / 4), d = i % (D / 4) * 4;
+        float top = -__builtin_inff(), sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) top = __builtin_fmaxf(top, sm_ml[w][r].x);
+        f32x4_t v = {0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            const f32x2_t ml = sm_ml[w][r];
+            const float f = ml.x == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(ml.x - top);
+            sum += f * ml.y;
+            v += f * *reinterpret_cast<const f32x4_t*>(sm_o[w] + r * PITCH + d);
+        }
+        if (!whole) {
+            *reinterpret_cast<f32x4_t*>(part + r * D + d) = v;
+            if (d == 0) *reinterpret_cast<f32x2_t*>(part + ROWS * D + 2 * r) = f32x2_t{top, sum};
+        } else if (row0 + r < all_rows) {
+            const bool none = row0 + r >= rows || top == -__builtin_inff();
+            const float inv = none ? 0.0f : 1.0f / sum;
+            const int64_t at = out_row(row0 + r);
+            u32x2_t w = {0, 0};
+            if (!none) w = u32x2_t{f32x2_to_bf16x2(v.x * inv, v.y * inv), f32x2_to_bf16x2(v.z * inv, v.w * inv)};
+            *reinterpret_cast<u32x2_t*>(a.o + at * D + d) = w;
+            if (d == 0) a.lse[at] = none ? -__builtin_inff() : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+        }
+    }
+    __syncthreads();                      // before the next request's
     }
 }
 
@@ -597,47 +557,43 @@ __global__ __launch_bounds__(256) void tree_attn_join_kernel(AttnArgs a, int row
 
 // What a call of these sizes launches.
 struct Shape {
-    int row_tiles, row_waves;             // of a wave, of a workgroup
-    int row_blocks, runs;
+    int row_tiles, row_blocks, runs;
 
-    int rows() const { return 16 * row_tiles * row_waves; }
+    int rows() const { return 16 * row_tiles; }
 };
 
-// Rows: 16 a wave up to 16 (and for D = 256, whose O fills the registers), else
-// 32; as many waves over the rows as there are.  Runs: two workgroups a CU of
-// 256 (one for D = 256); no run is shorter than one step a wave.  Three a CU fit
-// for one row tile, but more parts to join and more places read at once cost 3 to
-// 10%.  From the sizes alone: lengths are on the device.
+// Rows of a workgroup: 16 where there are no more (and for D = 256, whose O fills
+// the registers), else 32.
+// Runs: two workgroups a CU of 256, one for D = 256 (its registers; two that
+// follow one another cost 4 to 18%); no run is shorter than one step a wave.
+// Three fit for D = 64, but more runs are more parts to join and more places
+// read at once: the third is taken where 32 rows compute long, 16 steps a wave
+// (16 requests of 20 tokens over 8000: 56 us against 63; 7 of 24 over 3001: 25.9
+// against 24.4).  Runs in excess of what is resident would follow the others: one
+// request of 40 tokens over 20000, D = 128, takes 40 us in 480 workgroups, 52 in
+// 560.  From the sizes alone: lengths are on the device.
 Shape shape_of(int64_t B, int64_t N, int64_t Hq, int64_t H, int64_t D, int64_t max_pages, int64_t page_size) {
     const int64_t rows = N * (Hq / H);
     Shape s;
     s.row_tiles = rows <= 16 || D == 256 ? 1 : 2;
-    const int64_t waves = (rows + 16 * s.row_tiles - 1) / (16 * s.row_tiles);
-    s.row_waves = waves <= 1 ? 1 : waves <= 2 ? 2 : 4;
     s.row_blocks = (int)((rows + s.rows() - 1) / s.rows());
     const int64_t groups = H * s.row_blocks, steps = B * ((max_pages * page_size + kStep - 1) / kStep);
-    const int64_t wanted = D == 256 ? 256 : 512;
-    s.runs = (int)std::max<int64_t>(1, std::min((wanted + groups - 1) / groups, steps * s.row_waves / kWaves));
+    const bool third = D == 64 && s.row_tiles == 2 && steps * groups >= 768 * 16 * kWaves;
+    const int64_t wanted = D == 256 ? 256 : third ? 768 : 512;
+    s.runs = (int)std::max<int64_t>(1, std::min(wanted / groups, steps / kWaves));
     return s;
-}
-
-template <int D, int RT>
-hipError_t launch(const AttnArgs& a, int row_waves, hipStream_t stream) {
-    const int64_t groups = ((int64_t)a.runs * a.H + 7) / 8 * 8;
-    const dim3 grid((unsigned)(groups * a.row_blocks)), block(kWaves * 64);
-    if constexpr (RT == 2 || D == 256) {      // else 16 rows are one wave's
-        if (row_waves == 2) hipLaunchKernelGGL((tree_attn_kernel<D, RT, 2>), grid, block, 0, stream, a);
-        if (row_waves == 4) hipLaunchKernelGGL((tree_attn_kernel<D, RT, 4>), grid, block, 0, stream, a);
-    }
-    if (row_waves == 1) hipLaunchKernelGGL((tree_attn_kernel<D, RT, 1>), grid, block, 0, stream, a);
-    return hipGetLastError();
 }
 
 template <int D>
 hipError_t launch(const AttnArgs& a, const Shape& s, hipStream_t stream) {
-    hipError_t e;
-    if (D <= 128 && s.row_tiles == 2) e = launch<D, D <= 128 ? 2 : 1>(a, s.row_waves, stream);
-    else e = launch<D, 1>(a, s.row_waves, stream);
+    const int64_t groups = ((int64_t)a.runs * a.H + 7) / 8 * 8;
+    const dim3 grid((unsigned)(groups * a.row_blocks)), block(kWaves * 64);
+    if (s.row_tiles == 1) {
+        hipLaunchKernelGGL((tree_attn_kernel<D, 1>), grid, block, 0, stream, a);
+    } else if constexpr (D <= 128) {
+        hipLaunchKernelGGL((tree_attn_kernel<D, 2>), grid, block, 0, stream, a);
+    }
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.runs == 1) return e;
     // few rows have many parts each: a workgroup a row, else a thread for each four values
     const int64_t rows = (int64_t)a.B * a.H * a.N * a.G, per = 256 / (D / 4);

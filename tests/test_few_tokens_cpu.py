@@ -14,7 +14,7 @@ from tests import few_tokens as ft
 from tests.test_resource_gate import HIPCC, kernel_reports
 
 A = [ctypes.c_void_p(0x10000000 * (i + 1)) for i in range(14)]    # far apart, never dereferenced
-BAD = ctypes.c_void_p(0x10008)
+BAD = ctypes.c_void_p(0x10002)
 BIG = 1 << 40
 INVALID = dg.DG_ERR_INVALID_ARG
 NO_DEVICE = (dg.DG_ERR_HIP, dg.DG_ERR_UNSUPPORTED, dg.DG_OK)
@@ -159,7 +159,7 @@ def test_binding_rejects_host_tensors():
 # ---- the compiled kernels ---------------------------------------------------------------------------
 
 @pytest.mark.skipif(not os.path.exists(HIPCC), reason="hipcc not available")
-@pytest.mark.parametrize("src,least", [("kv_cache_kernel.hip", 12), ("tree_attn_kernel.hip", 17), ("moe_few_kernel.hip", 12)])
+@pytest.mark.parametrize("src,least", [("kv_cache_kernel.hip", 12), ("tree_attn_kernel.hip", 11), ("moe_few_kernel.hip", 12)])
 def test_no_vgpr_spill_no_scratch(src, least):
     reports = kernel_reports(src)
     assert len(reports) >= least, sorted(reports)
