@@ -6,26 +6,31 @@
 // operand), bf16 x, and ids outside [0, E) taking no part.
 //
 // Bound: the weights of the experts that are reached are read once from HBM;
-// everything else is small beside them.  So the weights go from HBM straight
-// into registers in the layout of the MFMA's row operand (lane l: 16 bytes of
-// row l & 15), are widened to bf16 there (exact) and multiplied by the tokens
-// as columns, and no barrier stands between a weight's load and its use.  The
+// everything else is small beside them.  So a wave fetches them in whole cache
+// lines into registers, a block ahead, and passes them through its own piece of
+// LDS, without a barrier, into the layout of the MFMA's row operand; they are
+// widened to bf16 there (exact) and multiplied by the tokens as columns.  The
 // product of a 128-K block is scaled and added to the fp32 accumulator, as in
 // the GEMMs.
-//  * Up: a workgroup takes 16 gate rows and the 16 up rows beside them of one
+//  * Up: a workgroup takes 16 or 32 gate rows and the up rows beside them of one
 //    reached expert; its waves deal the K blocks among themselves and meet in
 //    LDS, where silu and the product are taken in fp32.  h is stored as the
 //    sum of bf16 parts, each the truncated rest of the one before: two parts
 //    (2^-16 of h) where y is bf16, three (all of fp32's bits) where it is
 //    fp32, so that the second product can use the matrix unit without
 //    rounding h.
-//  * Down: a workgroup takes 16 rows of y for up to 64 tokens over all reached
-//    experts, so the sum over experts needs no atomics: its waves take equal
-//    runs of (expert, K block), add each expert's weighted product to their
-//    own fp32 slab in LDS, and the slabs are summed in order.
+//  * Down: a workgroup takes some rows of y for up to 64 tokens over the reached
+//    experts, or a share of them; each expert's weighted product is added to an
+//    fp32 slab in LDS.  The sums over experts need no atomics: slabs and shares
+//    are added in order, the shares by the one that arrives last.
 // The first kernel's workgroups find the reached experts from the ids by
 // themselves (a bitmap in LDS) and leave each expert's tokens and weights in
 // the workspace for the second.
+//
+// Measured, times of a whole layer with the weights' bytes over them: 1 token of
+// 6 in 32 experts, 4096 x 2048: 37 us, 4.1 TB/s (each kernel's start and end are
+// a third of it); 13 tokens: 134 us, 5.5 TB/s; 64 of 8 in 64 experts, 7168 x
+// 2048, fp32: 536 us, 5.3 TB/s.  A plain read of as many bytes reaches 6.2.
 #include "fp8_values.h"
 #include "serve_internal.h"
 
@@ -37,7 +42,6 @@ namespace {
 
 constexpr int kBlk = 128;
 constexpr int kUpWaves = 4, kDownWaves = 4;
-constexpr int kMaxShares = 8;           // XCDs
 constexpr int kTile = 16;               // rows and tokens of a matrix tile
 constexpr int kGroup = 64;              // tokens of a pass
 
@@ -250,11 +254,6 @@ __device__ __forceinline__ void products(const uint8_t* (&w)[NW], uint32_t w_off
     }
 }
 
-// Tiles of weight rows a workgroup takes for up to MOST tiles of columns: with
-// more columns to fetch for a weight, more weights for a column, while the
-// registers hold them.
-template <int MOST>
-constexpr int kRowTiles = MOST == 2 ? 2 : 1;
 // 16 * RT gate rows and the up rows beside them for the tokens list[first ...]
 // of an expert, MT tiles of them at most.
 template <int PARTS, int RT, int MT, int DEPTH>
@@ -319,9 +318,9 @@ __device__ __forceinline__ void up_pass(const MoeArgs& a, int e, int i0, int fir
     __syncthreads();
 }
 
-template <int PARTS, int MOST>
+template <int PARTS, int MOST, int RT>
 __global__ __launch_bounds__(kUpWaves * 64, 2) void moe_up_kernel(MoeArgs a) {
-    constexpr int RT = kRowTiles<MOST>, DEPTH = kUpDepth<MOST>;
+    constexpr int DEPTH = kUpDepth<MOST>;
     __shared__ uint32_t bitmap[kMoeMaxExperts / 32];
     __shared__ int list[kMoeMaxTokens];               // the rows of h of its tokens
     // the waves' stages, then their sums
@@ -408,47 +407,69 @@ __global__ __launch_bounds__(kUpWaves * 64, 2) void moe_up_kernel(MoeArgs a) {
     if (e < 0) return;                                // uniform
     const int count = found[1], i0 = tile * kTile * RT;
     for (int first = 0; first < count; first += 16 * MOST) {
-        const int left = count - first;
-        if (MOST == 1 || left <= 16)
-            up_pass<PARTS, RT, 1, DEPTH>(a, e, i0, first, count, list, sm, wave, lane);
-        else if (MOST == 2 || left <= 32)
-            up_pass<PARTS, RT, MOST == 1 ? 1 : 2, DEPTH>(a, e, i0, first, count, list, sm, wave, lane);
-        else
-            up_pass<PARTS, RT, MOST, DEPTH>(a, e, i0, first, count, list, sm, wave, lane);
+        if (count - first <= 16) up_pass<PARTS, RT, 1, DEPTH>(a, e, i0, first, count, list, sm, wave, lane);
+        else up_pass<PARTS, RT, MOST, DEPTH>(a, e, i0, first, count, list, sm, wave, lane);
     }
 }
 
 // Tokens whose parts fit MOST column tiles, and the tokens of a workgroup.
 template <int PARTS, int MOST>
 constexpr int kPass = 16 * MOST / PARTS;
+constexpr int kWideTiles = 2, kWideColumns = 2;     // where the waves share the columns
 template <int MOST>
 constexpr int kDownTokens = MOST == 1 ? 16 : kGroup;
 
-// 16 * RT rows of y for the workgroup's tokens.  The work is a list of passes,
-// an expert and up to kPass of its tokens each, of I / 128 K blocks; the waves
-// take equal runs of the list's blocks.  A pass's columns are its tokens' first
-// parts, then their second ones, ...  A wave's loads run kDownDepth blocks ahead of
-// its products and over the ends of passes, so HBM's latency is met once.
-template <int PARTS, int MOST>
-__global__ __launch_bounds__(kDownWaves * 64) void moe_down_kernel(MoeArgs a) {
-    constexpr int RT = kRowTiles<MOST>, ROWS = RT * kTile, MT = MOST;
-    constexpr int TOKENS = kDownTokens<MOST>, PASS = kPass<PARTS, MOST>;
-    // a pass: expert | first of `entries` << 10 | tokens << 20
-    static_assert(kMoeMaxExperts <= 1024 && kGroup * kMoeMaxTopk <= 1024 && PASS < 2048, "a pass fits a word");
-    __shared__ __attribute__((aligned(16))) float slabs[kDownWaves][TOKENS * ROWS];
-    __shared__ u32x4_t stages[kDownWaves][Block<RT, MT>::STAGE];
-    __shared__ Entry entries[TOKENS * kMoeMaxTopk];
-    __shared__ uint32_t passes[TOKENS * kMoeMaxTopk];
-    __shared__ int totals[kDownWaves];
-    const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int z = blockIdx.x % a.shares, tile = blockIdx.x / a.shares;
-    const int n0 = tile * ROWS, token0 = blockIdx.y * TOKENS;
-    const int tokens = min(a.T - token0, TOKENS);
-    float* slab = slabs[wave];
-    for (int i = lane; i < TOKENS * ROWS; i += 64) slab[i] = 0.0f;
+// y of a workgroup's TOKENS x ROWS tile from its sums, sum(i) the values 2 i and
+// 2 i + 1 of them, and those of the other shares, in order.
+template <int PARTS, int TOKENS, int ROWS, typename F>
+__device__ __forceinline__ void finish(const MoeArgs& a, int z, int tile, int tokens, int token0, int n0,
+                                       int* meet, F sum) {
+    auto put_y = [&](int i, float v0, float v1) {
+        const int64_t at = (int64_t)(token0 + 2 * i / ROWS) * a.H + n0 + 2 * i % ROWS;
+        if constexpr (PARTS == 3) *reinterpret_cast<f32x2_t*>(static_cast<float*>(a.y) + at) = f32x2_t{v0, v1};
+        else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.y) + at) = f32x2_to_bf16x2(v0, v1);
+    };
+    // [tile][group][share][token][rows]
+    const int64_t home = ((int64_t)tile * gridDim.y + blockIdx.y) * a.shares;
+    uint64_t* parts = reinterpret_cast<uint64_t*>(a.parts + home * (TOKENS * ROWS));
+    for (int i = threadIdx.x; i < tokens * ROWS / 2; i += kDownWaves * 64) {
+        const f32x2_t v = sum(i);
+        if (a.shares == 1) put_y(i, v.x, v.y);
+        else
+            __hip_atomic_store(parts + z * (TOKENS * ROWS / 2) + i, __builtin_bit_cast(uint64_t, v), __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
+    }
+    if (a.shares == 1) return;
+    // The share that arrives last adds them up.  Its count is taken after every
+    // wave's device-coherent stores have completed, and the parts are read with
+    // device-coherent loads after it (the GEMMs' split-K order).
+    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+    int* arrived = a.arrived + tile * gridDim.y + blockIdx.y;
+    if (threadIdx.x == 0) *meet = __hip_atomic_fetch_add(arrived, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (*meet != a.shares - 1) return;
+    for (int i = threadIdx.x; i < tokens * ROWS / 2; i += kDownWaves * 64) {
+        f32x2_t v = {0.0f, 0.0f};
+        for (int k0 = 0; k0 < a.shares; k0 += 8) {
+            uint64_t part[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                part[k] = __hip_atomic_load(parts + min(k0 + k, a.shares - 1) * (TOKENS * ROWS / 2) + i,
+                                            __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (k0 + k < a.shares) v += __builtin_bit_cast(f32x2_t, part[k]);
+        }
+        put_y(i, v.x, v.y);
+    }
+}
 
-    // the list of passes: a thread an expert, its place by a prefix sum
+// A workgroup's tokens of `entries` and its list of passes, a thread an expert, its
+// place by a prefix sum; returns their number.
+template <int PASS>
+__device__ __forceinline__ int list_passes(const MoeArgs& a, int token0, int tokens, Entry* entries,
+                                           uint32_t* passes, int* totals) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     for (int i = threadIdx.x; i < tokens * a.topk; i += kDownWaves * 64) entries[i] = a.entries[token0 * a.topk + i];
     int pass_count = 0;
     const int reached = *a.reached_count;
@@ -475,7 +496,34 @@ __global__ __launch_bounds__(kDownWaves * 64) void moe_down_kernel(MoeArgs a) {
             passes[at + i] = r.expert | (r.first + i * PASS) << 10 | min(PASS, r.count - i * PASS) << 20;
         __syncthreads();
     }
+    return __builtin_amdgcn_readfirstlane(pass_count);
+}
 
+// 16 * RT rows of y for the workgroup's tokens.  The work is a list of passes,
+// an expert and up to kPass of its tokens each, of I / 128 K blocks; the waves
+// take equal runs of the list's blocks.  A pass's columns are its tokens' first
+// parts, then their second ones, ...  A wave's loads run kDownDepth blocks ahead of
+// its products and over the ends of passes, so HBM's latency is met once.
+template <int PARTS, int MOST, int RT>
+__global__ __launch_bounds__(kDownWaves * 64) void moe_down_kernel(MoeArgs a) {
+    constexpr int ROWS = RT * kTile, MT = MOST;
+    constexpr int TOKENS = kDownTokens<MOST>, PASS = kPass<PARTS, MOST>;
+    // a pass: expert | first of `entries` << 10 | tokens << 20
+    static_assert(kMoeMaxExperts <= 1024 && kGroup * kMoeMaxTopk <= 1024 && PASS < 2048, "a pass fits a word");
+    __shared__ __attribute__((aligned(16))) float slabs[kDownWaves][TOKENS * ROWS];
+    __shared__ u32x4_t stages[kDownWaves][Block<RT, MT>::STAGE];
+    __shared__ Entry entries[TOKENS * kMoeMaxTopk];
+    __shared__ uint32_t passes[TOKENS * kMoeMaxTopk];
+    __shared__ int totals[kDownWaves];
+    const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int z = blockIdx.x % a.shares, tile = blockIdx.x / a.shares;
+    const int n0 = tile * ROWS, token0 = blockIdx.y * TOKENS;
+    const int tokens = min(a.T - token0, TOKENS);
+    float* slab = slabs[wave];
+    for (int i = lane; i < TOKENS * ROWS; i += 64) slab[i] = 0.0f;
+
+    const int pass_count = list_passes<PASS>(a, token0, tokens, entries, passes, totals);
     const int KB = a.I / kBlk;
     const int64_t blocks = (int64_t)pass_count * KB;
     const int share = z * kDownWaves + wave, all = a.shares * kDownWaves;
@@ -577,82 +625,199 @@ __global__ __launch_bounds__(kDownWaves * 64) void moe_down_kernel(MoeArgs a) {
         });
     }
     __syncthreads();
-    // two values a thread: the waves' slabs in order, then the shares in order
-    auto put_y = [&](int i, float v0, float v1) {
-        const int64_t at = (int64_t)(token0 + 2 * i / ROWS) * a.H + n0 + 2 * i % ROWS;
-        if constexpr (PARTS == 3) *reinterpret_cast<f32x2_t*>(static_cast<float*>(a.y) + at) = f32x2_t{v0, v1};
-        else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.y) + at) = f32x2_to_bf16x2(v0, v1);
-    };
-    // [tile][group][share][token][rows]
-    const int64_t home = ((int64_t)tile * gridDim.y + blockIdx.y) * a.shares;
-    uint64_t* parts = reinterpret_cast<uint64_t*>(a.parts + home * (TOKENS * ROWS));
-    for (int i = threadIdx.x; i < tokens * ROWS / 2; i += kDownWaves * 64) {
+    // the waves' slabs in order
+    finish<PARTS, TOKENS, ROWS>(a, z, tile, tokens, token0, n0, &totals[0], [&](int i) {
         f32x2_t v = {0.0f, 0.0f};
 #pragma unroll
         for (int k = 0; k < kDownWaves; ++k) v += *reinterpret_cast<const f32x2_t*>(slabs[k] + 2 * i);
-        if (a.shares == 1) put_y(i, v.x, v.y);
-        else
-            __hip_atomic_store(parts + z * (TOKENS * ROWS / 2) + i, __builtin_bit_cast(uint64_t, v), __ATOMIC_RELAXED,
-                               __HIP_MEMORY_SCOPE_AGENT);
-    }
-    if (a.shares == 1) return;
-    // The share that arrives last adds them up.  Its count is taken after every
-    // wave's device-coherent stores have completed, and the parts are read with
-    // device-coherent loads after it (the GEMMs' split-K order).
-    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-    int* arrived = a.arrived + tile * gridDim.y + blockIdx.y;
-    if (threadIdx.x == 0)
-        totals[0] = __hip_atomic_fetch_add(arrived, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        return v;
+    });
+}
+
+// The same where columns are many.  The workgroup's waves stand side by side over
+// 4 x 16 x RT rows of y and go through the same blocks, so that a column is
+// fetched once for all of them (each wave fetches a quarter) and meets them in
+// LDS, in two places in turn: one barrier a block.  What a wave has on its way is
+// then mostly weights.
+template <int PARTS>
+__global__ __launch_bounds__(kDownWaves * 64, 2) void moe_down_wide_kernel(MoeArgs a) {
+    constexpr int RT = kWideTiles, MT = kWideColumns, WROWS = RT * kTile, ROWS = kDownWaves * WROWS, PITCH = ROWS + 4;
+    constexpr int TOKENS = kGroup, PASS = kPass<PARTS, MT>, DEPTH = kDownDepth;
+    static_assert(kMoeMaxExperts <= 1024 && kGroup * kMoeMaxTopk <= 1024 && PASS < 2048, "a pass fits a word");
+    __shared__ __attribute__((aligned(16))) float slab[TOKENS * PITCH];
+    __shared__ u32x4_t weights[kDownWaves][RT * 128], columns[2][MT * 256];
+    __shared__ Entry entries[TOKENS * kMoeMaxTopk];
+    __shared__ uint32_t passes[TOKENS * kMoeMaxTopk];
+    __shared__ int totals[kDownWaves];
+    const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int z = blockIdx.x % a.shares, tile = blockIdx.x / a.shares;
+    const int n0 = tile * ROWS, row0 = n0 + wave * WROWS, token0 = blockIdx.y * TOKENS;
+    const int tokens = min(a.T - token0, TOKENS);
+    for (int i = threadIdx.x; i < TOKENS * PITCH; i += kDownWaves * 64) slab[i] = 0.0f;
+    const int pass_count = list_passes<PASS>(a, token0, tokens, entries, passes, totals);
     __syncthreads();
-    if (totals[0] != a.shares - 1) return;
-    for (int i = threadIdx.x; i < tokens * ROWS / 2; i += kDownWaves * 64) {
-        uint64_t part[kMaxShares];
+
+    const int KB = a.I / kBlk;
+    const int64_t blocks = (int64_t)pass_count * KB;
+    const int64_t u0 = blocks * z / a.shares;
+    const int count = (int)(blocks * (z + 1) / a.shares - u0);
+    const uint32_t w_off = (lane >> 3) * a.I + 16 * (lane & 7);
+    u32x4_t* stage = weights[wave];
+    const int put = lane ^ (lane >> 3);                                  // line l >> 3, chunk l & 7
+    const int line = r16 * 8, turn = lane & 7;
+    if (count > 0) {
+        // the loads' place
+        int lp = (int)(u0 / KB), lk = (int)(u0 - (int64_t)lp * KB);
+        const uint8_t* w;
+        const float* s;
+        // The wave's MT of the block's 4 MT column fetches, of 8 lines each:
+        // number q = wave * MT + i is lines 8 (q % 2) ... of tile q / 2 % MT, half q / 2 / MT.
+        uint32_t col[MT];
+        auto aim = [&]() {
+            const int pass = __builtin_amdgcn_readfirstlane(passes[lp]);
+            const int e = pass & 1023, first = pass >> 10 & 1023, n = pass >> 20;
+            w = a.w2 + ((int64_t)e * a.H + row0) * a.I;
+            s = a.s2 + ((int64_t)e * (a.H / kBlk) + row0 / kBlk) * KB;
 #pragma unroll
-        for (int k = 0; k < kMaxShares; ++k)
-            part[k] = __hip_atomic_load(parts + min(k, a.shares - 1) * (TOKENS * ROWS / 2) + i, __ATOMIC_RELAXED,
-                                        __HIP_MEMORY_SCOPE_AGENT);
-        f32x2_t v = {0.0f, 0.0f};
+            for (int i = 0; i < MT; ++i) {
+                const int q = wave * MT + i;
+                // columns past the last repeat the first one; their sums are not used
+                const int c = 16 * (q / 2 % MT) + 8 * (q % 2) + (lane >> 3), p = c / n;
+                const int pair = entries[first + (p < PARTS ? c - p * n : 0)].pair;
+                col[i] = 2u * (((uint32_t)(p < PARTS ? p : 0) * a.T * a.topk + pair) * (uint32_t)a.I +
+                               64 * (q / 2 / MT) + 8 * (lane & 7));
+            }
+        };
+        u32x4_t rw[DEPTH][RT][2], rx[DEPTH][MT];
+        float scale[DEPTH];
+        auto load = [&](int d) {
 #pragma unroll
-        for (int k = 0; k < kMaxShares; ++k)
-            if (k < a.shares) v += __builtin_bit_cast(f32x2_t, part[k]);
-        put_y(i, v.x, v.y);
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    rw[d][r][i] = *reinterpret_cast<const u32x4_t*>(
+                        w + ((int64_t)(r * kTile + 8 * i) * a.I + lk * kBlk) + w_off);
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+                rx[d][i] = *reinterpret_cast<const u32x4_t*>(reinterpret_cast<const char*>(a.h + lk * kBlk) + col[i]);
+            scale[d] = s[lk];
+            if (lk + 1 < KB) ++lk;
+            else if (lp + 1 < pass_count) {            // else there is nothing more to fetch
+                ++lp;
+                lk = 0;
+                aim();
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        // the products' place
+        int up = lp, uk = lk;
+        f32x4_t acc[RT][MT];
+        // the weighted sums to the slab; a token is in an expert's list once, so no
+        // two lanes of a part meet
+        auto flush = [&]() {
+            const int pass = __builtin_amdgcn_readfirstlane(passes[up]);
+            const int first = pass >> 10 & 1023, n = pass >> 20;
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                const int c = 16 * t + r16, part = c / n;
+                const Entry en = entries[first + (part < PARTS ? c - part * n : 0)];
+                float* at = slab + (en.pair / a.topk - token0) * PITCH + wave * WROWS + 4 * g;
+#pragma unroll
+                for (int q = 0; q < PARTS; ++q) {
+                    if (part == q)
+#pragma unroll
+                        for (int r = 0; r < RT; ++r)
+                            *reinterpret_cast<f32x4_t*>(at + r * kTile) += acc[r][t] * en.weight;
+                    wave_lds_order();
+                }
+            }
+        };
+        aim();
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) load(d);       // past the last block the last one again, or more
+        clear(acc);
+        in_flight<DEPTH>(count, [&](int d, int i, auto more) {
+            u32x4_t* xs = columns[i & 1];
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) stage[r * 128 + k * 64 + put] = rw[d][r][k];
+#pragma unroll
+            for (int k = 0; k < MT; ++k) xs[(wave * MT + k) * 64 + put] = rx[d][k];
+            const float sc = scale[d];
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (more) load(d);
+            // Every wave's columns are there; those of the other place, which the
+            // next block's go to, were read before the barrier behind this one.
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            f32x4_t p[RT][MT];
+            clear(p);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                u32x4_t v[RT];
+#pragma unroll
+                for (int r = 0; r < RT; ++r) v[r] = stage[r * 128 + line + ((4 * h + g) ^ turn)];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    bf16x8_t f[MT];
+#pragma unroll
+                    for (int t = 0; t < MT; ++t)
+                        f[t] = __builtin_bit_cast(bf16x8_t, xs[(h * MT + t) * 128 + line + ((2 * g + c) ^ turn)]);
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) {
+                        const bf16x8_t m = c ? e4m3x8_to_bf16x8(v[r].z, v[r].w) : e4m3x8_to_bf16x8(v[r].x, v[r].y);
+#pragma unroll
+                        for (int t = 0; t < MT; ++t) p[r][t] = mfma_bf16(m, f[t], p[r][t]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < RT; ++r) promote(p[r], sc, acc[r]);
+            if (++uk == KB || i + 1 == count) {
+                flush();
+                clear(acc);
+                uk = 0;
+                ++up;
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        });
     }
+    __syncthreads();
+    finish<PARTS, TOKENS, ROWS>(a, z, tile, tokens, token0, n0, &totals[0], [&](int i) {
+        return *reinterpret_cast<const f32x2_t*>(slab + 2 * i / ROWS * PITCH + 2 * i % ROWS);
+    });
 }
+// The second kernel of a call: `shares` workgroups for a tile of `rows` rows and
+// `tokens` tokens.  One column tile where no expert can have more; its workgroups
+// are small, and 1024 are wanted, else the 512 that are resident: a few more
+// follow the others (13 tokens of 6 in 32 experts, 7168 x 2048: 275 us in 672,
+// 252 in 448).  A share has 8 blocks of work to be worth its place in the join.
+// 32 rows for two column tiles fetch a column half as often, but where that
+// leaves half the chip idle 16 do better, in either kernel (64 of 2 in 8, 1024 x
+// 512: 16.4 us against 20.0; 17 of 2 in 4, 512 x 512: 12.2 against 14.5).
+// With waves that share the columns, a tile has four times the rows, and takes
+// four times the shares to fill the chip, up to 16: from 40 tiles on, where 12
+// do, that gains (64 of 8 in 64 experts, 7168 x 2048, fp32: 536 us against 612;
+// 128 of 8 in 128, 4096 x 1536: 533 against 628), below it loses (48 of 4 in 32,
+// 2048 x 1024: 65 against 54; 32 tiles: 0 to 2%).
+struct Down {
+    bool wide;
+    int most, rows, tokens, shares;
+};
 
-template <int PARTS, int MOST>
-hipError_t launch_up(const MoeArgs& a, hipStream_t stream) {
-    hipLaunchKernelGGL((moe_up_kernel<PARTS, MOST>),
-                       dim3((unsigned)((int64_t)a.slots * (a.I / (kRowTiles<MOST> * kTile)))), dim3(kUpWaves * 64), 0,
-                       stream, a);
-    return hipGetLastError();
-}
-
-template <int PARTS, int MOST>
-hipError_t launch_down(const MoeArgs& a, hipStream_t stream) {
-    constexpr int TOKENS = kDownTokens<MOST>;
-    hipLaunchKernelGGL((moe_down_kernel<PARTS, MOST>),
-                       dim3((unsigned)(a.H / (kRowTiles<MOST> * kTile) * a.shares), (unsigned)((a.T + TOKENS - 1) / TOKENS)),
-                       dim3(kDownWaves * 64), 0, stream, a);
-    return hipGetLastError();
-}
-
-// Column tiles of a pass: one where no expert can have more, two where an
-// expert has 12 columns or fewer on average (most of them then fit one), four
-// else.  A pass more reads the weights again, from the caches.
-int up_tiles(int64_t T, int64_t topk, int64_t E) {
-    return T <= 16 ? 1 : T <= 32 || T * topk <= 12 * E ? 2 : 4;
-}
-
-int down_tiles(int64_t T, int64_t topk, int64_t E, int parts) {
-    return T * parts <= 16 ? 1 : T * parts <= 32 || T * topk * parts <= 24 * E ? 2 : 4;
-}
-
-// Workgroups that share a tile's passes: what makes 512 of them (1024 of those
-// with one row tile), while a wave has two blocks.
-int down_shares(int64_t T, int64_t topk, int64_t E, int64_t H, int64_t I, int row_tiles) {
-    const int64_t blocks = std::min(E, T * topk) * (I / kBlk), tiles = H / (kTile * row_tiles);
-    const int64_t wanted = ((row_tiles == 1 ? 1024 : 512) + tiles - 1) / tiles;
-    return (int)std::max<int64_t>(1, std::min({(int64_t)kMaxShares, wanted, blocks / (2 * kDownWaves)}));
+Down down_of(int64_t T, int64_t topk, int64_t E, int64_t H, int64_t I, int parts) {
+    const int64_t blocks = std::min(E, T * topk) * (I / kBlk);
+    Down d;
+    d.most = T * parts <= 16 ? 1 : 2;
+    d.tokens = d.most == 1 ? kDownTokens<1> : kDownTokens<2>;
+    const int64_t groups = (T + d.tokens - 1) / d.tokens, wide_rows = kDownWaves * kTile * kWideTiles;
+    d.wide = d.most == 2 && H / wide_rows * groups >= 40;
+    const bool narrow = H / kTile * groups * (blocks / 8) < 1024;
+    d.rows = (int)(d.wide ? wide_rows : kTile * (d.most == 1 || narrow ? 1 : 2));
+    const int64_t wanted = (d.most == 1 ? 1024 : 512) / (H / d.rows * groups);
+    d.shares = (int)std::max<int64_t>(1, std::min({(int64_t)(d.wide ? 16 : 8), wanted, blocks / 8}));
+    return d;
 }
 
 constexpr int64_t align16(int64_t n) { return (n + 15) / 16 * 16; }
@@ -661,9 +826,9 @@ constexpr int64_t align16(int64_t n) { return (n + 15) / 16 * 16; }
 int64_t lay_out(MoeArgs& a, int parts, char* base) {
     const int64_t T = a.T, groups = (T + kGroup - 1) / kGroup, pairs = T * a.topk;
     a.slots = std::min(a.E, a.T * a.topk);
-    const int most = down_tiles(T, a.topk, a.E, parts), row_tiles = most == 2 ? kRowTiles<2> : 1;
-    a.shares = down_shares(T, a.topk, a.E, a.H, a.I, row_tiles);
-    a.counters = (int)(a.H / (kTile * row_tiles) * groups);
+    const Down d = down_of(T, a.topk, a.E, a.H, a.I, parts);
+    a.shares = d.shares;
+    a.counters = (int)(a.H / d.rows * groups);
     int64_t n = 0;
     auto piece = [&](int64_t bytes) {
         char* at = base + n;
@@ -676,22 +841,31 @@ int64_t lay_out(MoeArgs& a, int parts, char* base) {
     a.arrived = reinterpret_cast<int32_t*>(piece(4ll * a.counters));
     a.h = reinterpret_cast<uint16_t*>(piece(parts * pairs * a.I * 2));
     a.parts = reinterpret_cast<float*>(
-        piece(a.shares == 1 ? 0 : 4ll * a.shares * groups * (most == 1 ? 16 : kGroup) * a.H));
+        piece(a.shares == 1 ? 0 : 4ll * a.shares * groups * d.tokens * a.H));
     return n;
 }
 
 template <int PARTS>
 hipError_t launch(const MoeArgs& a, hipStream_t stream) {
-    hipError_t e;
-    const int up = up_tiles(a.T, a.topk, a.E);
-    if (up == 1) e = launch_up<PARTS, 1>(a, stream);
-    else if (up == 2) e = launch_up<PARTS, 2>(a, stream);
-    else e = launch_up<PARTS, 4>(a, stream);
+    // column tiles of a pass: one where no expert can have more, else two, with
+    // passes that read the weights again from the caches (four lose 4% of the
+    // layer for 64 tokens of 8 in 64 experts and 16% for 256 of 8 in 64)
+    const int64_t up_tiles = (int64_t)a.slots * (a.I / kTile);
+    const bool narrow = a.T > 16 && up_tiles < 1024;
+    const dim3 up_grid((unsigned)(a.T <= 16 || narrow ? up_tiles : up_tiles / 2)), up_block(kUpWaves * 64);
+    if (a.T <= 16) hipLaunchKernelGGL((moe_up_kernel<PARTS, 1, 1>), up_grid, up_block, 0, stream, a);
+    else if (narrow) hipLaunchKernelGGL((moe_up_kernel<PARTS, 2, 1>), up_grid, up_block, 0, stream, a);
+    else hipLaunchKernelGGL((moe_up_kernel<PARTS, 2, 2>), up_grid, up_block, 0, stream, a);
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int down = down_tiles(a.T, a.topk, a.E, PARTS);
-    if (down == 1) return launch_down<PARTS, 1>(a, stream);
-    if (down == 2) return launch_down<PARTS, 2>(a, stream);
-    return launch_down<PARTS, 4>(a, stream);
+    const Down d = down_of(a.T, a.topk, a.E, a.H, a.I, PARTS);
+    const dim3 grid((unsigned)(a.H / d.rows * d.shares), (unsigned)((a.T + d.tokens - 1) / d.tokens));
+    const dim3 block(kDownWaves * 64);
+    if (d.wide) hipLaunchKernelGGL((moe_down_wide_kernel<PARTS>), grid, block, 0, stream, a);
+    else if (d.most == 1) hipLaunchKernelGGL((moe_down_kernel<PARTS, 1, 1>), grid, block, 0, stream, a);
+    else if (d.rows == kTile) hipLaunchKernelGGL((moe_down_kernel<PARTS, 2, 1>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((moe_down_kernel<PARTS, 2, 2>), grid, block, 0, stream, a);
+    return hipGetLastError();
 }
 
 }  // namespace

@@ -377,6 +377,21 @@ def test_moe(T, E, k, H, I, dtype):
     moe_case(T, E, k, H, I, routed(T, E, k), dtype, T + E)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,E,k,H,I", [(256, 8, 2, 1280, 256), (130, 20, 3, 1792, 128), (17, 4, 2, 5120, 128), (64, 6, 4, 5248, 384),
+                                       (9, 5, 1, 5120, 640), (200, 3, 1, 1408, 1024)])
+def test_moe_many_rows_of_y(T, E, k, H, I, dtype):
+    """Sizes whose second product is taken by waves that share the columns."""
+    announce(f"moe many rows T={T} E={E} k={k} H={H} I={I} {dtype}")
+    moe_case(T, E, k, H, I, routed(T, E, k, 0.1), dtype, T + E)
+    moe_case(T, E, k, H, I, lambda rng: rng.choice([-1, 1, 2], (T, k)), dtype, T)
+    if T == 17:
+        moe_case(T, E, k, H, I, lambda rng: np.full((T, k), -1), dtype, T)
+        args, y = moe_case(T, E, k, H, I, lambda rng: np.where(np.arange(T)[:, None] == 3, [1, 0], [-1, -1]), dtype, T)
+        for _ in range(3):
+            assert same_bits(dg.fp8_moe_few_tokens(*args, dtype=TYPES[dtype]), y)
+
+
 @pytest.mark.parametrize("T", [1, 3, 12, 40, 100])
 def test_moe_dropped_slots(T):
     announce(f"moe dropped slots T={T}")
