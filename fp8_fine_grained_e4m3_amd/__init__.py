@@ -13,6 +13,13 @@ forms the scales may instead be packed UE8M0 words (int32, four power-of-two
 exponents per word, the README's newer-path format): the dtype of the scale
 tensors picks the C entry point.  The caller allocates the output and passes
 it in.
+
+For steps of a few tokens there are the paged FP8 key/value cache
+(make_fp8_kv_cache, fp8_kv_cache_write, fp8_kv_cache_read), attention of drafted
+trees or single tokens over it (fp8_tree_attention) and a whole
+mixture-of-experts layer (fp8_moe_few_tokens).  These allocate what they return
+unless it is passed in, and take their workspace from torch's allocator unless
+one is given (make_fp8_*_workspace).
 """
 from __future__ import annotations
 

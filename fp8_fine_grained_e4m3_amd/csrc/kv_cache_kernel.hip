@@ -15,7 +15,8 @@
 // values share a launch (gridDim.y = 2), which halves the launches of a decode
 // step.  Read rows are stored past the caches (40000 tokens of 8 heads of 128
 // values as bf16, 249 MB: 47 us, 5.2 TB/s, against 64 us with plain stores);
-// written codes are not, the attention that follows reads them.
+// written codes are not, the attention that follows reads them.  16384 tokens of
+// that shape are written in 23 us, 4.4 TB/s of the 101 MB that pass.
 #include "fp8_values.h"
 #include "serve_internal.h"
 
