@@ -102,7 +102,7 @@ __device__ __forceinline__ float of_quad(float v) {
 }
 
 // Inclusive sum of v over the wave's lanes up to each.
-__device__ __forceinline__ int sum_up_to_lane(int v) {
+__device__ __forceinline__ uint32_t sum_up_to_lane(uint32_t v) {
     v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);   // row_shr:1
     v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);   // row_shr:2
     v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);   // row_shr:4

@@ -470,13 +470,17 @@ template <int PASS>
 __device__ __forceinline__ int list_passes(const MoeArgs& a, int token0, int tokens, Entry* entries,
                                            uint32_t* passes, int* totals) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // all loads on their way together: a thread's experts before their number is there
+    auto load = [&](int nth) { return a.reached[blockIdx.y * a.slots + min(nth, a.slots - 1)]; };
+    Reached next = load(threadIdx.x);
+    const int reached = *a.reached_count;
     for (int i = threadIdx.x; i < tokens * a.topk; i += kDownWaves * 64) entries[i] = a.entries[token0 * a.topk + i];
     int pass_count = 0;
-    const int reached = *a.reached_count;
     for (int base = 0; base < reached; base += kDownWaves * 64) {
         const int nth = base + (int)threadIdx.x;
-        Reached r{0, 0, 0};
-        if (nth < reached) r = a.reached[blockIdx.y * a.slots + nth];
+        Reached r = next;
+        if (nth >= reached) r.count = 0;
+        next = load(nth + kDownWaves * 64);
         const int n = (r.count + PASS - 1) / PASS;
         int before = n;                                // inclusive prefix in the wave
 #pragma unroll

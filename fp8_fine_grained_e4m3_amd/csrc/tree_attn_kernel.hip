@@ -151,10 +151,10 @@ __global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : D == 128 ? 2 : 3) void 
 
     // this run's steps of all requests', and the request that they start in
     int64_t total = 0;
-    int upto = 0;                         // of the lane's request and those before it of its 64
+    uint32_t upto = 0;                    // of the lane's request and those before it of its 64, 2^31 at most
     for (int base = 0; base < a.B; base += 64) {
         upto = sum_up_to_lane(steps_of_lane(a, base + lane, row0));
-        total += __builtin_amdgcn_readlane(upto, 63);
+        total += (uint32_t)__builtin_amdgcn_readlane(upto, 63);
     }
     const int64_t runs = max((int64_t)1, min((int64_t)a.runs, total / kWaves));
     if (run >= runs) return;
@@ -163,16 +163,16 @@ __global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : D == 128 ? 2 : 3) void 
     int b = a.B;
     for (int base = 0; base < a.B; base += 64) {
         if (a.B > 64) upto = sum_up_to_lane(steps_of_lane(a, base + lane, row0));
-        const int before = __shfl_up(upto, 1);
-        const int64_t from = start + (lane > 0 ? before : 0);
+        const uint32_t before = __shfl_up(upto, 1);
+        const int64_t from = start + (lane > 0 ? before : 0u);
         const uint64_t hit = __ballot(base + lane < a.B && (start + upto > s0 || from >= s0));
         if (hit != 0) {
             const int at = __builtin_ctzll(hit);
             b = base + at;
-            if (at > 0) start += __builtin_amdgcn_readlane(upto, at - 1);
+            if (at > 0) start += (uint32_t)__builtin_amdgcn_readlane(upto, at - 1);
             break;
         }
-        start += __builtin_amdgcn_readlane(upto, 63);
+        start += (uint32_t)__builtin_amdgcn_readlane(upto, 63);
     }
 
     for (; b < a.B && (start < s1 || (run == runs - 1 && start == total)); ++b) {
