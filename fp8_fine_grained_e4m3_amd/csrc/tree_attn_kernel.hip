@@ -40,11 +40,12 @@
 // to join through memory (one request of 40 tokens over 20000: 55 us against 40).
 // With many rows the VALU (widening keys and values, exponentials) is the bound.
 //
-// Requests differ in length, so the steps of all of them, end to end, are cut
-// into equal runs, one a workgroup for each key head: a workgroup goes through
-// the requests that its run touches.  Where a run ends inside a request, its O,
-// maximum and sum go to the workspace, and a second kernel joins a request's
-// parts in order, a thread for four values of a row.  (Joined by the last
+// Short requests have a workgroup each, for a key head and a row block.  Long ones
+// differ in length, so the steps of all of them, end to end, are cut into equal
+// runs, and the workgroup of a run goes through the requests that it touches.
+// Where a run ends inside a request, its O, maximum and sum go to the workspace,
+// and a second kernel joins a request's parts in order, a thread for four values
+// of a row.  (Joined by the last
 // workgroup to arrive instead, a long request's parts pass through one CU: 344 us
 // for two trees of 16 over 100001 tokens.)
 #include "fp8_values.h"
@@ -81,6 +82,7 @@ struct AttnArgs {
     float scale;
     int B, N, H, G, num_pages, page_shift, max_pages, mask_words;
     int runs, row_blocks;
+    bool whole;                           // a run is a request
 };
 
 template <int D>
@@ -129,15 +131,15 @@ __device__ __forceinline__ int steps_of_lane(const AttnArgs& a, int b, int first
     return b < a.B ? request_of(a, a.ctx[b], a.tree ? a.tree[b] : a.N, first_row).steps : 0;
 }
 
-// RT: row tiles, of each of a workgroup's waves the same.
-template <int D, int RT>
-__global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : D == 128 ? 2 : 3) void tree_attn_kernel(AttnArgs a) {
+// RT: row tiles, of each of a workgroup's W waves the same.
+template <int D, int RT, int W>
+__global__ __launch_bounds__(W * 64, W == 8 ? 2 : D == 256 ? 1 : D == 128 ? 2 : 3) void tree_attn_kernel(AttnArgs a) {
     constexpr int DT = D / 16;            // 16-row tiles of O^T
     constexpr int ROWS = 16 * RT;
     constexpr int PITCH = D + 4;          // of a row of O in LDS
     constexpr int PART = ROWS * (D + 2);  // floats of a part
-    __shared__ __attribute__((aligned(16))) float sm_o[kWaves][ROWS * PITCH];
-    __shared__ f32x2_t sm_ml[kWaves][ROWS];
+    __shared__ __attribute__((aligned(16))) float sm_o[W][ROWS * PITCH];
+    __shared__ f32x2_t sm_ml[W][ROWS];
     const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // The row blocks of a run follow one another on one XCD (workgroups go to the
@@ -149,46 +151,51 @@ __global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : D == 128 ? 2 : 3) void 
     const int row0 = rb * ROWS;
     const int all_rows = a.N * a.G, Hq = a.H * a.G;
 
-    // this run's steps of all requests', and the request that they start in
-    int64_t total = 0;
-    uint32_t upto = 0;                    // of the lane's request and those before it of its 64, 2^31 at most
-    for (int base = 0; base < a.B; base += 64) {
-        upto = sum_up_to_lane(steps_of_lane(a, base + lane, row0));
-        total += (uint32_t)__builtin_amdgcn_readlane(upto, 63);
-    }
-    const int64_t runs = max((int64_t)1, min((int64_t)a.runs, total / kWaves));
-    if (run >= runs) return;
-    const int64_t s0 = total * run / runs, s1 = total * (run + 1) / runs;
-    int64_t start = 0;                    // of request b
-    int b = a.B;
-    for (int base = 0; base < a.B; base += 64) {
-        if (a.B > 64) upto = sum_up_to_lane(steps_of_lane(a, base + lane, row0));
-        const uint32_t before = __shfl_up(upto, 1);
-        const int64_t from = start + (lane > 0 ? before : 0u);
-        const uint64_t hit = __ballot(base + lane < a.B && (start + upto > s0 || from >= s0));
-        if (hit != 0) {
-            const int at = __builtin_ctzll(hit);
-            b = base + at;
-            if (at > 0) start += (uint32_t)__builtin_amdgcn_readlane(upto, at - 1);
-            break;
+    int b = run, end = a.B;
+    int64_t s0 = 0, s1 = 1ll << 62, start = 0, total = 0, runs = 1;     // start: of request b
+    if (a.whole) {
+        end = run + 1;
+    } else {
+        // this run's steps of all requests', and the request that they start in
+        uint32_t upto = 0;                // of the lane's request and those before it of its 64, 2^31 at most
+        for (int base = 0; base < a.B; base += 64) {
+            upto = sum_up_to_lane(steps_of_lane(a, base + lane, row0));
+            total += (uint32_t)__builtin_amdgcn_readlane(upto, 63);
         }
-        start += (uint32_t)__builtin_amdgcn_readlane(upto, 63);
+        runs = max((int64_t)1, min((int64_t)a.runs, total / W));
+        if (run >= runs) return;
+        s0 = total * run / runs;
+        s1 = total * (run + 1) / runs;
+        b = a.B;
+        for (int base = 0; base < a.B; base += 64) {
+            if (a.B > 64) upto = sum_up_to_lane(steps_of_lane(a, base + lane, row0));
+            const uint32_t before = __shfl_up(upto, 1);
+            const int64_t from = start + (lane > 0 ? before : 0u);
+            const uint64_t hit = __ballot(base + lane < a.B && (start + upto > s0 || from >= s0));
+            if (hit != 0) {
+                const int at = __builtin_ctzll(hit);
+                b = base + at;
+                if (at > 0) start += (uint32_t)__builtin_amdgcn_readlane(upto, at - 1);
+                break;
+            }
+            start += (uint32_t)__builtin_amdgcn_readlane(upto, 63);
+        }
     }
 
-    for (; b < a.B && (start < s1 || (run == runs - 1 && start == total)); ++b) {
+    for (; b < end && (start < s1 || (run == runs - 1 && start == total)); ++b) {
     const Request rq = request(a, b, row0);
     const int ctx = rq.ctx, L = rq.L, rows = rq.n * a.G;
     const int lo = (int)max(s0 - start, (int64_t)0), hi = (int)min(s1 - start, (int64_t)rq.steps);
     start += rq.steps;
     auto out_row = [&](int r) { return ((int64_t)b * a.N + r / a.G) * Hq + h * a.G + r % a.G; };
     const bool whole = lo == 0 && hi == rq.steps;
-    if (lo == 0 && threadIdx.x == 0 && a.runs > 1) {
+    if (lo == 0 && threadIdx.x == 0 && !a.whole && a.runs > 1) {
         // the last run that starts at or before the request's last step
         const int64_t last = whole ? run - 1 : (start * runs + total - 1) / total - 1;
         a.split[((int64_t)b * a.H + h) * a.row_blocks + rb] = make_int2(run, (int)last);
     }
     if (rq.steps == 0) {                  // no row of the block sees anything
-        for (int i = threadIdx.x; i < ROWS * D / 8; i += kWaves * 64) {
+        for (int i = threadIdx.x; i < ROWS * D / 8; i += W * 64) {
             const int r = row0 + i / (D / 8);
             if (r >= all_rows) break;
             const int64_t at = out_row(r);
@@ -271,19 +278,19 @@ __global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : D == 128 ? 2 : 3) void 
         }
     };
     const int s_last = hi - 1;
-    int pages = ask(min(lo + wave, s_last)), pages_next = ask(min(lo + wave + kWaves, s_last));
+    int pages = ask(min(lo + wave, s_last)), pages_next = ask(min(lo + wave + W, s_last));
     Place at = place(min(lo + wave, s_last), pages);
-    pages = ask(min(lo + wave + 2 * kWaves, s_last));
+    pages = ask(min(lo + wave + 2 * W, s_last));
     fetch_k(at, 0);
     fetch_k(at, 1);
     __builtin_amdgcn_sched_barrier(0);
     fetch_v(at);
     __builtin_amdgcn_sched_barrier(0);
-    for (int s = lo + wave; s < hi; s += kWaves) {
+    for (int s = lo + wave; s < hi; s += W) {
         const int j0 = s * kStep;
-        const Place next = place(min(s + kWaves, s_last), pages_next);
+        const Place next = place(min(s + W, s_last), pages_next);
         pages_next = pages;
-        pages = ask(min(s + 3 * kWaves, s_last));
+        pages = ask(min(s + 3 * W, s_last));
         __builtin_amdgcn_sched_barrier(0);
         const bool all = j0 + kStep <= ctx && at.live[0] && at.live[1];   // uniform: no mask here
         float sc[RT][2][4];
@@ -455,14 +462,14 @@ __global__ __launch_bounds__(kWaves * 64, D == 256 ? 1 : D == 128 ? 2 : 3) void 
     // A run has one part of a request that goes on from the run before (the first
     // of its two places) and one of a request that begins in it (the second).
     float* part = a.parts + (((int64_t)run_head * a.row_blocks + rb) * 2 + (lo > 0 ? 0 : 1)) * PART;
-    for (int i = fresh(threadIdx.x); i < ROWS * D / 4; i += kWaves * 64) {
+    for (int i = fresh(threadIdx.x); i < ROWS * D / 4; i += W * 64) {
         const int r = i / (D / 4), d = i % (D / 4) * 4;
         float top = -__builtin_inff(), sum = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) top = __builtin_fmaxf(top, sm_ml[w][r].x);
+        for (int w = 0; w < W; ++w) top = __builtin_fmaxf(top, sm_ml[w][r].x);
         f32x4_t v = {0, 0, 0, 0};
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
+        for (int w = 0; w < W; ++w) {
             const f32x2_t ml = sm_ml[w][r];
             const float f = ml.x == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(ml.x - top);
             sum += f * ml.y;
@@ -557,13 +564,22 @@ __global__ __launch_bounds__(256) void tree_attn_join_kernel(AttnArgs a, int row
 
 // What a call of these sizes launches.
 struct Shape {
-    int row_tiles, row_blocks, runs;
+    int row_tiles, row_blocks, runs, waves;
+    bool whole;
 
     int rows() const { return 16 * row_tiles; }
 };
 
 // Rows of a workgroup: 16 where there are no more (and for D = 256, whose O fills
 // the registers), else 32.
+// Whole requests, a workgroup each and no second kernel, where that is soon done
+// whatever the lengths turn out to be: up to 1024 positions, or up to 2048 and
+// 4096 where requests and heads make 128 and 256 workgroups.  Two row tiles have
+// eight waves then.  In graphs, whole against split: 16 requests of 60, 5.5 us
+// against 16.4; 64 of 1000, 20.9 against 28.8; 64 of 4000, 74.7 against 87; one of
+// 500, 8.0 against 10.1; trees of 24 over 1000 in 7, 12.1 against 18.7; but one of
+// 2000, 17.1 against 11.3, and of 1000 with D = 256, 15.5 against 11.9.  (One of
+// 1000, D = 128: 11.0 against 10.6, and a launch of 2.4 us less for the host.)
 // Runs: two workgroups a CU of 256, one for D = 256 (its registers; two that
 // follow one another cost 4 to 18%); no run is shorter than one step a wave.
 // Three fit for D = 64, but more runs are more parts to join and more places
@@ -577,7 +593,11 @@ Shape shape_of(int64_t B, int64_t N, int64_t Hq, int64_t H, int64_t D, int64_t m
     Shape s;
     s.row_tiles = rows <= 16 || D == 256 ? 1 : 2;
     s.row_blocks = (int)((rows + s.rows() - 1) / s.rows());
-    const int64_t groups = H * s.row_blocks, steps = B * ((max_pages * page_size + kStep - 1) / kStep);
+    const int64_t groups = H * s.row_blocks, most = (max_pages * page_size + kStep - 1) / kStep, steps = B * most;
+    s.whole = most <= (D == 256 ? 16 : 32) || (most <= 64 && B * groups >= 128) || (most <= 128 && B * groups >= 256);
+    s.waves = s.whole && s.row_tiles == 2 ? 8 : kWaves;
+    s.runs = (int)B;
+    if (s.whole) return s;
     const bool third = D == 64 && s.row_tiles == 2 && steps * groups >= 768 * 16 * kWaves;
     const int64_t wanted = D == 256 ? 256 : third ? 768 : 512;
     s.runs = (int)std::max<int64_t>(1, std::min(wanted / groups, steps / kWaves));
@@ -587,14 +607,15 @@ Shape shape_of(int64_t B, int64_t N, int64_t Hq, int64_t H, int64_t D, int64_t m
 template <int D>
 hipError_t launch(const AttnArgs& a, const Shape& s, hipStream_t stream) {
     const int64_t groups = ((int64_t)a.runs * a.H + 7) / 8 * 8;
-    const dim3 grid((unsigned)(groups * a.row_blocks)), block(kWaves * 64);
+    const dim3 grid((unsigned)(groups * a.row_blocks)), block(s.waves * 64);
     if (s.row_tiles == 1) {
-        hipLaunchKernelGGL((tree_attn_kernel<D, 1>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((tree_attn_kernel<D, 1, kWaves>), grid, block, 0, stream, a);
     } else if constexpr (D <= 128) {
-        hipLaunchKernelGGL((tree_attn_kernel<D, 2>), grid, block, 0, stream, a);
+        if (s.waves == 8) hipLaunchKernelGGL((tree_attn_kernel<D, 2, 8>), grid, block, 0, stream, a);
+        else hipLaunchKernelGGL((tree_attn_kernel<D, 2, kWaves>), grid, block, 0, stream, a);
     }
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || a.runs == 1) return e;
+    if (e != hipSuccess || a.whole || a.runs == 1) return e;
     // few rows have many parts each: a workgroup a row, else a thread for each four values
     const int64_t rows = (int64_t)a.B * a.H * a.N * a.G, per = 256 / (D / 4);
     if (rows <= 4096)
@@ -612,7 +633,7 @@ int64_t split_bytes(int64_t B, int64_t H, const Shape& s) { return (B * H * s.ro
 int64_t tree_attn_workspace_bytes(int64_t B, int64_t N, int64_t Hq, int64_t H, int64_t D,
                                   int64_t max_pages, int64_t page_size) {
     const Shape s = shape_of(B, N, Hq, H, D, max_pages, page_size);
-    if (s.runs == 1) return 0;            // no request is split
+    if (s.whole || s.runs == 1) return 0;      // no request is split
     return split_bytes(B, H, s) + 2ll * s.runs * H * s.row_blocks * s.rows() * (D + 2) * 4;
 }
 
@@ -627,7 +648,7 @@ hipError_t launch_tree_attn(const TreeAttnProblem& p, hipStream_t stream) {
     a.num_pages = (int)p.cache.num_pages; a.max_pages = (int)p.max_pages;
     a.page_shift = __builtin_ctzll((unsigned long long)p.cache.page_size);
     a.mask_words = (int)((p.N + 63) / 64);
-    a.runs = s.runs; a.row_blocks = s.row_blocks;
+    a.runs = s.runs; a.row_blocks = s.row_blocks; a.whole = s.whole;
     a.split = static_cast<int2*>(p.workspace);
     a.parts = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + split_bytes(p.B, p.cache.H, s));
     switch (p.cache.D) {

@@ -152,8 +152,9 @@ def test_cache_larger_than_32_bit_offsets():
 
 # ---- attention -----------------------------------------------------------------------------------------
 
-def attention_case(B, N, H, G, D, page, ctx, lens, mask, seed, scale=None, hide=(), q_scale=1.0):
-    """A random case run on the GPU, with 0x7F codes and NaN scales wherever no one may look."""
+def attention_case(B, N, H, G, D, page, ctx, lens, mask, seed, scale=None, hide=(), q_scale=1.0, room=0):
+    """A random case run on the GPU, with 0x7F codes and NaN scales wherever no one may look.
+    room: positions that the table has beyond the longest request (with many, requests are split)."""
     rng = np.random.default_rng(seed)
     ctx, lens = np.asarray(ctx, np.int32), np.asarray(lens, np.int32)
     MP = max(1, -(-int((np.clip(ctx, 0, None) + np.clip(lens, 0, N)).max()) // page)) + 1
@@ -169,6 +170,7 @@ def attention_case(B, N, H, G, D, page, ctx, lens, mask, seed, scale=None, hide=
         sf.transpose(0, 2, 1)[~live] = np.nan
     for b, p, value in hide:
         table[b, p] = value
+    table = np.concatenate([table, np.full((B, room // page), -7, np.int32)], 1)
     q = torch.from_numpy((q_scale * rng.standard_normal((B, N, H * G, D))).astype(np.float32)).bfloat16()
     scale = D ** -0.5 if scale is None else scale
     words = None if mask is None else dev(ft.pack_mask(mask))
@@ -255,7 +257,22 @@ def test_scores_far_apart():
         check_attention(got, want)
 
 
-@pytest.mark.parametrize("B,N,G,ctx", [(1, 1, 4, 5000), (3, 1, 8, 2500), (70, 1, 2, 60), (2, 12, 8, 1500)])
+@pytest.mark.parametrize("N,G,D", [(1, 4, 64), (1, 3, 128), (1, 16, 256), (3, 4, 128), (16, 2, 256), (17, 4, 128), (24, 8, 64),
+                                   (65, 2, 64), (130, 1, 128)])
+def test_short_requests_in_a_long_table(N, G, D):
+    """Split over workgroups by the table's size, with lengths around tiles and steps, trees, hidden
+    pages and rows that see nothing."""
+    announce(f"split short N={N} G={G} D={D}")
+    rng = np.random.default_rng(N)
+    ctx, lens = [100, 0, 37, 5, 31, 32, 33, 0, 601, 16], [N, N - 1, max(N // 2, 1), 0, N, N, 1, N, N, N]
+    mask = np.stack([ft.random_tree(rng, N) for _ in ctx])
+    mask[2, 0] = mask[7, N // 2] = False
+    got, want = attention_case(10, N, 2, G, D, 16, ctx, lens, mask, N, hide=((0, 1, -1), (8, 3, 1 << 30), (4, 0, -9)), room=5000)
+    assert np.isneginf(want[1]).any()
+    check_attention(got, want)
+
+
+@pytest.mark.parametrize("B,N,G,ctx", [(70, 1, 2, 1500), (1, 1, 4, 5000), (3, 1, 8, 2500), (70, 1, 2, 60), (2, 12, 8, 1500)])
 def test_requests_split_over_workgroups(B, N, G, ctx):
     announce(f"split B={B} N={N} G={G} ctx={ctx}")
     rng = np.random.default_rng(B)
@@ -299,9 +316,10 @@ def test_unseen_tokens_do_not_touch_others():
         dg.fp8_kv_cache_write(k, v, cache, slot)
 
 
-def test_strided_queries_given_outputs_and_workspaces():
-    announce("strides, out=, workspace")
-    args = random_call()
+@pytest.mark.parametrize("ctx", [300, 5000])
+def test_strided_queries_given_outputs_and_workspaces(ctx):
+    announce(f"strides, out=, workspace, {ctx}")
+    args = random_call(ctx=ctx)
     q = args[0]
     o, lse = dg.fp8_tree_attention(*args)
     wide = torch.full((5, 9, 12, 128), float("nan"), device="cuda").bfloat16()
@@ -332,7 +350,7 @@ def test_attention_binding_rejects():
     with pytest.raises(dg.DGError, match="multiple of H"):
         dg.fp8_tree_attention(q[:, :, :7].contiguous(), cache, table, ctx, lens)
     with pytest.raises(dg.DGError, match="needed"):
-        dg.fp8_tree_attention(q, cache, table, ctx, lens, workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
+        dg.fp8_tree_attention(q, cache, table.repeat(1, 20), ctx, lens, workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(TypeError, match="uint8"):
         dg.fp8_tree_attention(q, cache, table, ctx, lens, workspace=torch.zeros(16, device="cuda"))
 
@@ -474,10 +492,10 @@ def step(state):
     dg.fp8_moe_few_tokens(s["x"], s["w1"], s["w2"], s["ids"], s["wt"], out=s["y"], workspace=s["ws_m"])
 
 
-def decode_state(seed=0):
+def decode_state(seed=0, ctx=700):
     torch.manual_seed(seed)
     rng = np.random.default_rng(seed)
-    q, cache, table, ctx, lens = random_call(seed=seed, ctx=700)
+    q, cache, table, ctx, lens = random_call(seed=seed, ctx=ctx)
     s = dict(q=q, cache=cache, table=table, ctx=ctx, lens=lens)
     s["k"], s["v"] = torch.randn(2, 30, 2, 128, device="cuda").bfloat16()
     s["slots"] = dev(rng.permutation(cache[0][0].shape[0] * 16)[:30].astype(np.int32))
@@ -498,9 +516,10 @@ def outputs(s):
     return [*s["o"], *s["rows"], s["y"]]
 
 
-def test_a_step_is_bitwise_repeatable_and_capturable():
-    announce("graph replays")
-    s = decode_state()
+@pytest.mark.parametrize("most", [700, 5000])
+def test_a_step_is_bitwise_repeatable_and_capturable(most):
+    announce(f"graph replays, {most}")
+    s = decode_state(ctx=most)
     changes = [(s["ctx"].clone(), s["lens"].clone(), s["ids"].clone()),
                ((s["ctx"] // 3), (9 - s["lens"]).int(), s["ids"].flip(0).contiguous()),
                (torch.zeros_like(s["ctx"]), torch.zeros_like(s["lens"]), torch.full_like(s["ids"], -1))]
@@ -529,7 +548,7 @@ def test_a_step_is_bitwise_repeatable_and_capturable():
 
 def test_on_another_stream():
     announce("another stream")
-    s = decode_state(1)
+    s = decode_state(1, ctx=5000)
     step(s)
     want = [t.clone() for t in outputs(s)]
     for t in outputs(s):
