@@ -573,19 +573,20 @@ struct Shape {
 // Rows of a workgroup: 16 where there are no more (and for D = 256, whose O fills
 // the registers), else 32.
 // Whole requests, a workgroup each and no second kernel, where that is soon done
-// whatever the lengths turn out to be: up to 1024 positions, or up to 2048 and
-// 4096 where requests and heads make 128 and 256 workgroups.  Two row tiles have
-// eight waves then.  In graphs, whole against split: 16 requests of 60, 5.5 us
-// against 16.4; 64 of 1000, 20.9 against 28.8; 64 of 4000, 74.7 against 87; one of
-// 500, 8.0 against 10.1; trees of 24 over 1000 in 7, 12.1 against 18.7; but one of
-// 2000, 17.1 against 11.3, and of 1000 with D = 256, 15.5 against 11.9.  (One of
-// 1000, D = 128: 11.0 against 10.6, and a launch of 2.4 us less for the host.)
+// whatever the lengths turn out to be: up to 1024 positions, or up to 2048 where
+// requests and heads make 128 workgroups, up to 4096 where they make 256 or have
+// two row tiles, and with those eight waves.  In graphs, whole against split: 16
+// requests of 60, 5.5 us against 16.4; 64 of 1000, 20.9 against 28.8; 64 of 4000,
+// 76 against 87; one of 500, 8.0 against 10.1; 7 trees of 24 over 3001, 20.9
+// against 24.0; but one of 2000, 17.1 against 11.3, and of 1000 with D = 256, 15.5
+// against 11.9.  (One of 1000, D = 128: 11.0 against 10.6, and a launch of 2.4 us
+// less for the host.)
 // Runs: two workgroups a CU of 256, one for D = 256 (its registers; two that
 // follow one another cost 4 to 18%); no run is shorter than one step a wave.
 // Three fit for D = 64, but more runs are more parts to join and more places
 // read at once: the third is taken where 32 rows compute long, 16 steps a wave
-// (16 requests of 20 tokens over 8000: 56 us against 63; 7 of 24 over 3001: 25.9
-// against 24.4).  Runs in excess of what is resident would follow the others: one
+// (16 requests of 20 tokens over 8000: 56 us against 63; with 5 steps a wave, 7 of
+// 24 over 3001: 25.9 against 24.4).  Runs in excess of what is resident would follow the others: one
 // request of 40 tokens over 20000, D = 128, takes 40 us in 480 workgroups, 52 in
 // 560.  From the sizes alone: lengths are on the device.
 Shape shape_of(int64_t B, int64_t N, int64_t Hq, int64_t H, int64_t D, int64_t max_pages, int64_t page_size) {
@@ -594,7 +595,8 @@ Shape shape_of(int64_t B, int64_t N, int64_t Hq, int64_t H, int64_t D, int64_t m
     s.row_tiles = rows <= 16 || D == 256 ? 1 : 2;
     s.row_blocks = (int)((rows + s.rows() - 1) / s.rows());
     const int64_t groups = H * s.row_blocks, most = (max_pages * page_size + kStep - 1) / kStep, steps = B * most;
-    s.whole = most <= (D == 256 ? 16 : 32) || (most <= 64 && B * groups >= 128) || (most <= 128 && B * groups >= 256);
+    s.whole = most <= (D == 256 ? 16 : 32) || (most <= (s.row_tiles == 2 ? 128 : 64) && B * groups >= 128) ||
+              (most <= 128 && B * groups >= 256);
     s.waves = s.whole && s.row_tiles == 2 ? 8 : kWaves;
     s.runs = (int)B;
     if (s.whole) return s;
