@@ -653,12 +653,13 @@ def _same_device(first: torch.Tensor, *others):
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _call(fn: str, device: int, *args):
     """An entry point on the device's current stream."""
     f = getattr(load_library(), fn)
-    if torch.cuda.current_device() == device:
+    if _current_device() == device:
         status = f(*args, _raw_stream(device))
     else:
         with torch.cuda.device(device):
@@ -705,7 +706,7 @@ def fp8_kv_cache_read(cache, slots: torch.Tensor, dtype: torch.dtype = torch.bfl
     if out is None:
         if dtype not in _ROW_TYPES:
             raise TypeError(f"dtype must be bfloat16 or float32, got {dtype}")
-        k = torch.empty((T, H, D), dtype=dtype, device=kc.device)
+        k = kc.new_empty((T, H, D), dtype=dtype)
         v = torch.empty_like(k)
     else:
         k, v = _dev(out[0], "out k"), _dev(out[1], "out v")
@@ -795,8 +796,8 @@ def fp8_tree_attention(q: torch.Tensor, cache, page_table: torch.Tensor, context
                 raise ValueError(f"tree_mask {tuple(tree_mask.shape)} must be {mask_shape}")
         _same_device(kc, q, table, ctx, tree_lens, tree_mask)
     if out is None:
-        o = torch.empty((B, N, Hq, D), dtype=_BF16, device=on)
-        lse = torch.empty((B, N, Hq), dtype=_F32, device=on)
+        o = torch.empty_like(q) if q.is_contiguous() else q.new_empty(q.shape)
+        lse = q.new_empty((B, N, Hq), dtype=_F32)
     else:
         o, lse = _dev(out[0], "out"), _f32(out[1], "lse")
         if o.dtype != torch.bfloat16:
@@ -868,7 +869,7 @@ def fp8_moe_few_tokens(x: torch.Tensor, w1: Tuple[torch.Tensor, torch.Tensor],
     if out is None:
         if dtype not in _ROW_TYPES:
             raise TypeError(f"dtype must be bfloat16 or float32, got {dtype}")
-        out = torch.empty((T, H), dtype=dtype, device=on)
+        out = torch.empty_like(x) if dtype is _BF16 else x.new_empty((T, H), dtype=dtype)
     else:
         out = _dev(out, "out")
         if out.dtype not in _ROW_TYPES:

@@ -595,8 +595,10 @@ Shape shape_of(int64_t B, int64_t N, int64_t Hq, int64_t H, int64_t D, int64_t m
     s.row_tiles = rows <= 16 || D == 256 ? 1 : 2;
     s.row_blocks = (int)((rows + s.rows() - 1) / s.rows());
     const int64_t groups = H * s.row_blocks, most = (max_pages * page_size + kStep - 1) / kStep, steps = B * most;
-    s.whole = most <= (D == 256 ? 16 : 32) || (most <= (s.row_tiles == 2 ? 128 : 64) && B * groups >= 128) ||
-              (most <= 128 && B * groups >= 256);
+    const int64_t workgroups = B * groups;
+    s.whole = most <= (D == 256 ? 16 : 32) || (most <= (s.row_tiles == 2 ? 128 : 64) && workgroups >= 128) ||
+              (most <= 128 && workgroups >= 256);
+    if (workgroups > (1 << 20)) s.whole = false;       // a grid has fewer than 2^32 threads
     s.waves = s.whole && s.row_tiles == 2 ? 8 : kWaves;
     s.runs = (int)B;
     if (s.whole) return s;
