@@ -133,7 +133,7 @@ __device__ __forceinline__ int steps_of_lane(const AttnArgs& a, int b, int first
 
 // RT: row tiles, of each of a workgroup's W waves the same.
 template <int D, int RT, int W>
-__global__ __launch_bounds__(W * 64, W == 8 ? 2 : D == 256 ? 1 : D == 128 ? 2 : 3) void tree_attn_kernel(AttnArgs a) {
+__global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) void tree_attn_kernel(AttnArgs a) {
     constexpr int DT = D / 16;            // 16-row tiles of O^T
     constexpr int ROWS = 16 * RT;
     constexpr int PITCH = D + 4;          // of a row of O in LDS
@@ -575,7 +575,11 @@ struct Shape {
 // Whole requests, a workgroup each and no second kernel, where that is soon done
 // whatever the lengths turn out to be: up to 1024 positions, or up to 2048 where
 // requests and heads make 128 workgroups, up to 4096 where they make 256 or have
-// two row tiles, and with those eight waves.  In graphs, whole against split: 16
+// two row tiles.  Their waves are as many as are resident with all the others, up
+// to eight for two row tiles and four else, but at most 16 steps fall to one (60
+// trees of 24 over 221: 45 us with one wave, 60 with four, 100 with eight; 16 of 64
+// over 300: 22 with two, 28 with four, 43 with eight; 8 of 16 over 1000: 17 with
+// eight, 19 with four, 27 with two).  In graphs, whole against split: 16
 // requests of 60, 5.5 us against 16.4; 64 of 1000, 20.9 against 28.8; 64 of 4000,
 // 76 against 87; one of 500, 8.0 against 10.1; 7 trees of 24 over 3001, 20.9
 // against 24.0; but one of 2000, 17.1 against 11.3, and of 1000 with D = 256, 15.5
@@ -586,9 +590,9 @@ struct Shape {
 // Three fit for D = 64, but more runs are more parts to join and more places
 // read at once: the third is taken where 32 rows compute long, 16 steps a wave
 // (16 requests of 20 tokens over 8000: 56 us against 63; with 5 steps a wave, 7 of
-// 24 over 3001: 25.9 against 24.4).  Runs in excess of what is resident would follow the others: one
-// request of 40 tokens over 20000, D = 128, takes 40 us in 480 workgroups, 52 in
-// 560.  From the sizes alone: lengths are on the device.
+// 24 over 3001: 25.9 against 24.4).  Runs in excess of what is resident would
+// follow the others: one request of 40 tokens over 20000, D = 128, takes 40 us in
+// 480 workgroups, 52 in 560.  From the sizes alone: lengths are on the device.
 Shape shape_of(int64_t B, int64_t N, int64_t Hq, int64_t H, int64_t D, int64_t max_pages, int64_t page_size) {
     const int64_t rows = N * (Hq / H);
     Shape s;
@@ -599,7 +603,12 @@ Shape shape_of(int64_t B, int64_t N, int64_t Hq, int64_t H, int64_t D, int64_t m
     s.whole = most <= (D == 256 ? 16 : 32) || (most <= (s.row_tiles == 2 ? 128 : 64) && workgroups >= 128) ||
               (most <= 128 && workgroups >= 256);
     if (workgroups > (1 << 20)) s.whole = false;       // a grid has fewer than 2^32 threads
-    s.waves = s.whole && s.row_tiles == 2 ? 8 : kWaves;
+    s.waves = kWaves;
+    if (s.whole) {
+        const int64_t resident = 1024 * (D == 256 ? 1 : D == 128 ? 2 : 3);
+        s.waves = s.row_tiles == 2 ? 8 : 4;
+        while (s.waves > 1 && workgroups * s.waves > resident && 2 * most <= 16 * s.waves) s.waves /= 2;
+    }
     s.runs = (int)B;
     if (s.whole) return s;
     const bool third = D == 64 && s.row_tiles == 2 && steps * groups >= 768 * 16 * kWaves;
@@ -608,15 +617,22 @@ Shape shape_of(int64_t B, int64_t N, int64_t Hq, int64_t H, int64_t D, int64_t m
     return s;
 }
 
+template <int D, int RT>
+void launch_waves(const AttnArgs& a, int waves, dim3 grid, hipStream_t stream) {
+    if (waves == 1) hipLaunchKernelGGL((tree_attn_kernel<D, RT, 1>), grid, dim3(64), 0, stream, a);
+    else if (waves == 2) hipLaunchKernelGGL((tree_attn_kernel<D, RT, 2>), grid, dim3(128), 0, stream, a);
+    else if (waves == 4) hipLaunchKernelGGL((tree_attn_kernel<D, RT, 4>), grid, dim3(256), 0, stream, a);
+    else if constexpr (RT == 2) hipLaunchKernelGGL((tree_attn_kernel<D, RT, 8>), grid, dim3(512), 0, stream, a);
+}
+
 template <int D>
 hipError_t launch(const AttnArgs& a, const Shape& s, hipStream_t stream) {
     const int64_t groups = ((int64_t)a.runs * a.H + 7) / 8 * 8;
-    const dim3 grid((unsigned)(groups * a.row_blocks)), block(s.waves * 64);
+    const dim3 grid((unsigned)(groups * a.row_blocks));
     if (s.row_tiles == 1) {
-        hipLaunchKernelGGL((tree_attn_kernel<D, 1, kWaves>), grid, block, 0, stream, a);
+        launch_waves<D, 1>(a, s.waves, grid, stream);
     } else if constexpr (D <= 128) {
-        if (s.waves == 8) hipLaunchKernelGGL((tree_attn_kernel<D, 2, 8>), grid, block, 0, stream, a);
-        else hipLaunchKernelGGL((tree_attn_kernel<D, 2, kWaves>), grid, block, 0, stream, a);
+        launch_waves<D, 2>(a, s.waves, grid, stream);
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.whole || a.runs == 1) return e;

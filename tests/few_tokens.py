@@ -89,7 +89,11 @@ def attention(q, cache, table, ctx, lens, mask, scale, page):
                     lse[b, i, h * G + g] = m + np.log(z)
                     # the sums run over len(w) terms, of the weights and of the values
                     rel = 2 * es + (len(w) + 64) * EPS + 2.0 ** -20
-                    bo[b, i, h * G + g] = (np.abs(p) @ np.abs(val) / z * (2.0 ** -11 + 2 * rel)
+                    # a weight times its value's scale is kept to 11 bits, and to 2^-35 of the
+                    # largest weight (1) times the largest scale, whichever is more
+                    code = np.abs(e4m3(vc[at[w], h, w % page])).sum(0)
+                    least = 2.0 ** -35 * float(vs[at[w], h, w % page].max()) * code / z
+                    bo[b, i, h * G + g] = (np.abs(p) @ np.abs(val) / z * (2.0 ** -11 + 2 * rel) + least
                                            + 2.0 ** -8 * np.abs(o[b, i, h * G + g]) + 1e-37)
                     bl[b, i, h * G + g] = rel + 2.0 ** -20 + 4 * EPS * abs(m)
     return o, lse, bo, bl

@@ -282,6 +282,18 @@ def test_requests_split_over_workgroups(B, N, G, ctx):
     check_attention(got, want)
 
 
+@pytest.mark.parametrize("B,N,H,G,D", [(400, 1, 2, 4, 64), (800, 1, 2, 1, 64), (300, 1, 2, 3, 128), (600, 1, 2, 1, 128), (150, 1, 2, 4, 256),
+                                       (600, 1, 1, 2, 256), (250, 9, 2, 2, 64), (400, 5, 2, 4, 64), (800, 9, 2, 2, 64), (160, 5, 2, 4, 128),
+                                       (270, 9, 2, 2, 128), (1030, 5, 1, 4, 128)])
+def test_many_short_requests(B, N, H, G, D):
+    """More workgroups than are resident with many waves each."""
+    announce(f"many short B={B} N={N} H={H} G={G} D={D}")
+    rng = np.random.default_rng(B)
+    mask = np.stack([ft.random_tree(rng, N) for _ in range(B)]) if N > 1 else None
+    got, want = attention_case(B, N, H, G, D, 16, rng.integers(0, 120, B), rng.integers(0, N + 1, B), mask, B)
+    check_attention(got, want)
+
+
 def random_call(B=5, N=9, H=2, G=4, D=128, page=16, ctx=300, seed=0):
     rng = np.random.default_rng(seed)
     MP = -(-(ctx + N) // page)
