@@ -33,8 +33,8 @@
 //    maximum follows, with the exchange and the scaling of O that this takes, only
 //    where one passes it by 2^4 or more: in nearly every step it does not.  P's
 //    range leaves those 4 powers of two free.
-// A workgroup has 16 or 32 rows, and its four waves share their steps and add up
-// in LDS.  More rows than that are further workgroups beside it, which find the
+// A workgroup has 16 or 32 rows, and its waves share their steps and add up in
+// LDS.  More rows than that are further workgroups beside it, which find the
 // keys in the XCD's cache: all of 128 rows' waves in one workgroup, each with 32
 // of them and all steps, leave less to join within it but four times the parts
 // to join through memory (one request of 40 tokens over 20000: 55 us against 40).
@@ -45,9 +45,12 @@
 // runs, and the workgroup of a run goes through the requests that it touches.
 // Where a run ends inside a request, its O, maximum and sum go to the workspace,
 // and a second kernel joins a request's parts in order, a thread for four values
-// of a row.  (Joined by the last
-// workgroup to arrive instead, a long request's parts pass through one CU: 344 us
-// for two trees of 16 over 100001 tokens.)
+// of a row.  (Joined by the last workgroup to arrive instead, a long request's
+// parts pass through one CU: 344 us against 174 for two trees of 16 over 100001
+// tokens, both as they were then.)
+// Measured: 32 single tokens over 8192, 32 / 8 heads of 128, 89 us, 4.7 TB/s; two
+// trees of 16 over 100001, 64 / 8 heads of 128, 141 us, 2.2 TB/s and 0.56 PFLOP/s
+// with the VALU 57% and the matrix unit 22% busy; 7 trees of 24 over 3001, 21 us.
 #include "fp8_values.h"
 #include "serve_internal.h"
 
@@ -57,7 +60,7 @@
 namespace dg {
 namespace {
 
-constexpr int kWaves = 4;
+constexpr int kWaves = 4;                 // of a workgroup where requests are split
 constexpr int kStep = 32;                 // keys of a wave's step
 constexpr int kTop = 11;                  // P of a value with the largest scale is below 2^(kTop + kLazy)
 constexpr float kLazy = 4.0f;             // how far, in powers of two, scores pass m before m follows
@@ -443,7 +446,7 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
     }
 
     // The waves put down their O and meet: a thread then adds up four values of a
-    // row, wave by wave, relative to the largest of the four maxima.
+    // row, wave by wave, relative to the largest of their maxima.
     const int elane = fresh(lane), er16 = elane & 15, eg = elane >> 4;
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
