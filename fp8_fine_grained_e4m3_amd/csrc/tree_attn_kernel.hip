@@ -40,12 +40,13 @@
 // to join through memory (one request of 40 tokens over 20000: 55 us against 40).
 // With many rows the VALU (widening keys and values, exponentials) is the bound.
 //
-// Short requests have a workgroup each, for a key head and a row block.  Long ones
-// differ in length, so the steps of all of them, end to end, are cut into equal
-// runs, and the workgroup of a run goes through the requests that it touches.
-// Where a run ends inside a request, its O, maximum and sum go to the workspace,
-// and a second kernel joins a request's parts in order, a thread for four values
-// of a row.  (Joined by the last workgroup to arrive instead, a long request's
+// Short requests have a workgroup each, for a key head and a row block, as the
+// table's size or, in a long table, their lengths tell.  Long ones differ in
+// length, so the steps of all of them, end to end, are cut into equal runs, and the
+// workgroup of a run goes through the requests that it touches.  Where a run ends
+// inside a request, its O, maximum and sum go to the workspace, and a second kernel
+// joins a request's parts in order, a thread for four values of a row.
+// (Joined by the last workgroup to arrive instead, a long request's
 // parts pass through one CU: 344 us against 174 for two trees of 16 over 100001
 // tokens, both as they were then.)
 // Measured: 32 single tokens over 8192, 32 / 8 heads of 128, 89 us, 4.7 TB/s; two
@@ -62,6 +63,13 @@ namespace {
 
 constexpr int kWaves = 4;                 // of a workgroup where requests are split
 constexpr int kStep = 32;                 // keys of a wave's step
+// Several requests that turn out to be short, though their table is long, stay
+// whole and are dealt to the runs in turn: where none has more than kBrief steps,
+// or kFew and there are as many requests as runs.  Borders between requests in a
+// run, and parts to join, cost more than equal runs gain (64 requests of 20 to 700
+// tokens: 16.5 us against 25.8; 7 trees of 24 over 500 to 760, 12.7 against 18.6;
+// 128 of 500 to 2000, 70 against 79; alone, 760: 11.3 against 10.0).
+constexpr int kBrief = 24, kFew = 64;
 constexpr int kTop = 11;                  // P of a value with the largest scale is below 2^(kTop + kLazy)
 constexpr float kLazy = 4.0f;             // how far, in powers of two, scores pass m before m follows
 constexpr float kLog2e = 1.4426950408889634f;
@@ -154,38 +162,46 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
     const int row0 = rb * ROWS;
     const int all_rows = a.N * a.G, Hq = a.H * a.G;
 
-    int b = run, end = a.B;
+    int b = run, stride = 1, end = a.B;
     int64_t s0 = 0, s1 = 1ll << 62, start = 0, total = 0, runs = 1;     // start: of request b
     if (a.whole) {
         end = run + 1;
     } else {
         // this run's steps of all requests', and the request that they start in
         uint32_t upto = 0;                // of the lane's request and those before it of its 64, 2^31 at most
+        bool brief = a.B > 1, few = a.B >= a.runs;
         for (int base = 0; base < a.B; base += 64) {
-            upto = sum_up_to_lane(steps_of_lane(a, base + lane, row0));
+            const int own = steps_of_lane(a, base + lane, row0);
+            brief = brief && !__any(own > kBrief);
+            few = few && !__any(own > kFew);
+            upto = sum_up_to_lane(own);
             total += (uint32_t)__builtin_amdgcn_readlane(upto, 63);
         }
-        runs = max((int64_t)1, min((int64_t)a.runs, total / W));
-        if (run >= runs) return;
-        s0 = total * run / runs;
-        s1 = total * (run + 1) / runs;
-        b = a.B;
-        for (int base = 0; base < a.B; base += 64) {
-            if (a.B > 64) upto = sum_up_to_lane(steps_of_lane(a, base + lane, row0));
-            const uint32_t before = __shfl_up(upto, 1);
-            const int64_t from = start + (lane > 0 ? before : 0u);
-            const uint64_t hit = __ballot(base + lane < a.B && (start + upto > s0 || from >= s0));
-            if (hit != 0) {
-                const int at = __builtin_ctzll(hit);
-                b = base + at;
-                if (at > 0) start += (uint32_t)__builtin_amdgcn_readlane(upto, at - 1);
-                break;
+        if (brief || few) {
+            stride = a.runs;
+        } else {
+            runs = max((int64_t)1, min((int64_t)a.runs, total / W));
+            if (run >= runs) return;
+            s0 = total * run / runs;
+            s1 = total * (run + 1) / runs;
+            b = a.B;
+            for (int base = 0; base < a.B; base += 64) {
+                if (a.B > 64) upto = sum_up_to_lane(steps_of_lane(a, base + lane, row0));
+                const uint32_t before = __shfl_up(upto, 1);
+                const int64_t from = start + (lane > 0 ? before : 0u);
+                const uint64_t hit = __ballot(base + lane < a.B && (start + upto > s0 || from >= s0));
+                if (hit != 0) {
+                    const int at = __builtin_ctzll(hit);
+                    b = base + at;
+                    if (at > 0) start += (uint32_t)__builtin_amdgcn_readlane(upto, at - 1);
+                    break;
+                }
+                start += (uint32_t)__builtin_amdgcn_readlane(upto, 63);
             }
-            start += (uint32_t)__builtin_amdgcn_readlane(upto, 63);
         }
     }
 
-    for (; b < end && (start < s1 || (run == runs - 1 && start == total)); ++b) {
+    for (; b < end && (start < s1 || (run == runs - 1 && start == total)); b += stride) {
     const Request rq = request(a, b, row0);
     const int ctx = rq.ctx, L = rq.L, rows = rq.n * a.G;
     const int lo = (int)max(s0 - start, (int64_t)0), hi = (int)min(s1 - start, (int64_t)rq.steps);

@@ -272,6 +272,19 @@ def test_short_requests_in_a_long_table(N, G, D):
     check_attention(got, want)
 
 
+@pytest.mark.parametrize("B,N,H,G,D,most", [(5, 7, 2, 4, 128, 700), (300, 1, 8, 1, 64, 100), (70, 3, 8, 2, 128, 900), (40, 2, 16, 1, 256, 300),
+                                            (9, 20, 1, 2, 64, 760), (66, 1, 16, 1, 128, 2040)])
+def test_whole_requests_in_a_long_table(B, N, H, G, D, most):
+    """Short or many requests, which stay whole whatever the table's size."""
+    announce(f"whole in a long table B={B} N={N} H={H} G={G} D={D}")
+    rng = np.random.default_rng(B)
+    mask = np.stack([ft.random_tree(rng, N) for _ in range(B)])
+    ctx, lens = rng.integers(0, most + 1, B), rng.integers(0, N + 1, B)
+    ctx[0], ctx[B // 2], lens[0] = most - N, 0, N
+    got, want = attention_case(B, N, H, G, D, 16, ctx, lens, mask, B, room=5000)
+    check_attention(got, want)
+
+
 @pytest.mark.parametrize("B,N,G,ctx", [(70, 1, 2, 1500), (1, 1, 4, 5000), (3, 1, 8, 2500), (70, 1, 2, 60), (2, 12, 8, 1500)])
 def test_requests_split_over_workgroups(B, N, G, ctx):
     announce(f"split B={B} N={N} G={G} ctx={ctx}")
