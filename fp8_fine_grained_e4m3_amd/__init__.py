@@ -768,7 +768,9 @@ def fp8_tree_attention(q: torch.Tensor, cache, page_table: torch.Tensor, context
     if q.dim() != 4 or q.shape[3] != D:
         raise ValueError(f"q {tuple(q.shape)} must be [B, N, Hq, {D}]")
     B, N, Hq, _ = q.shape
-    stride = _rows(q, "q") if N > 1 or B <= 1 else q.stride(0)
+    stride = _rows(q, "q")
+    if N == 1 and B > 1:                          # a token a request: requests are the rows
+        stride = q.stride(0)
     mask_shape = (B, N, (N + 63) // 64)
     if not (q.dtype is _BF16 and table.dtype is _I32 and ctx.dtype is _I32 and table.dim() == 2
             and table.shape[0] == B and ctx.shape == (B,) and table.is_contiguous() and ctx.is_contiguous()
