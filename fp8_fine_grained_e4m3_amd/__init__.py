@@ -775,7 +775,7 @@ def fp8_tree_attention(q: torch.Tensor, cache, page_table: torch.Tensor, context
     if not (q.dtype is _BF16 and table.dtype is _I32 and ctx.dtype is _I32 and table.dim() == 2
             and table.shape[0] == B and ctx.shape == (B,) and table.is_contiguous() and ctx.is_contiguous()
             and q.get_device() == on and table.get_device() == on and ctx.get_device() == on
-            and (B <= 1 or q.stride(0) == N * stride)
+            and (B <= 1 or N == 0 or q.stride(0) == N * stride)
             and (tree_lens is None or (tree_lens.dtype is _I32 and tree_lens.shape == (B,)
                                        and tree_lens.is_contiguous() and tree_lens.get_device() == on))
             and (tree_mask is None or (tree_mask.dtype is _I64 and tree_mask.shape == mask_shape
@@ -783,7 +783,7 @@ def fp8_tree_attention(q: torch.Tensor, cache, page_table: torch.Tensor, context
         if q.dtype != torch.bfloat16:
             raise TypeError(f"q must be bfloat16, got {q.dtype}")
         _rows(q, "q")
-        if B > 1 and q.stride(0) != N * stride:
+        if B > 1 and N > 0 and q.stride(0) != N * stride:
             raise ValueError(f"q: tokens must be evenly spaced over requests, strides are {q.stride()}")
         _i32(table, "page_table"), _i32(ctx, "context_lens")
         if table.dim() != 2 or table.shape[0] != B or tuple(ctx.shape) != (B,):

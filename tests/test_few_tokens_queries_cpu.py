@@ -72,3 +72,13 @@ def test_queries_of_wider_rows_pass_their_stride(attend, name, make, stride):
     calls, (o, lse) = attend(q, H=1)
     assert len(calls) == 1 and calls[0][1] == stride
     assert o.shape == q.shape and lse.shape == q.shape[:3] and o.is_contiguous()
+
+
+@pytest.mark.parametrize("q", [rows(4, 0, 8, 128), rows(4, 3, 8, 128)[:, 3:], rows(1, 0, 8, 128), rows(0, 0, 8, 128),
+                               rows(0, 3, 8, 128), rows(4, 3, 0, 128)], ids=lambda q: str(tuple(q.shape)))
+def test_queries_of_nothing(attend, q):
+    """No requests, tokens or heads are no work and no error, as in the C call."""
+    calls, (o, lse) = attend(q)
+    assert len(calls) == 1 and o.shape == q.shape and lse.shape == q.shape[:3]
+    stride = calls[0][1]
+    assert stride >= q.shape[2] * 128 and stride % 8 == 0
