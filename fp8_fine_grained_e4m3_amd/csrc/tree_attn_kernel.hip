@@ -5,7 +5,8 @@
 // mask has, at positions c + j.  With one token this is decode attention.
 //   S_j = scale * ks_j * (q . kc_j)      kc, vc e4m3 codes, ks, vs their scales
 //   o   = sum_j p_j vs_j vc_j,  p = softmax(S),  lse = ln sum_j exp S_j
-// A row that sees nothing has o = 0 and lse = -inf.
+// A row that sees nothing has o = 0 and lse = -inf: its sum is 0, where what is seen
+// leaves 1 or more, or NaN.  (The maximum does not tell: it passes over NaN.)
 //
 // The rows of one key head are its n tokens times the G query heads that share
 // it (row = token * G + head), so a key or value is fetched once for all.
@@ -498,7 +499,7 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
             *reinterpret_cast<f32x4_t*>(part + r * D + d) = v;
             if (d == 0) *reinterpret_cast<f32x2_t*>(part + ROWS * D + 2 * r) = f32x2_t{top, sum};
         } else if (row0 + r < all_rows) {
-            const bool none = row0 + r >= rows || top == -__builtin_inff();
+            const bool none = row0 + r >= rows || sum == 0.0f;      // a sum of NaN is none of it
             const float inv = none ? 0.0f : 1.0f / sum;
             const int64_t at = out_row(row0 + r);
             u32x2_t w = {0, 0};
@@ -536,9 +537,10 @@ __global__ __launch_bounds__(256) void tree_attn_join_kernel(AttnArgs a, int row
     const int ml = rows_of_block * D + 2 * in_block, o = in_block * D + d;
     float top = -__builtin_inff(), sum = 0.0f;
     f32x4_t v = {0, 0, 0, 0};
-    // adds a partial sum with its maximum; a part that saw nothing has none
+    // adds a partial sum with its maximum; a part that saw nothing has the sum 0 (one
+    // that saw nothing but NaN has the maximum -inf too, but the sum NaN)
     auto add = [&](float m, float l, f32x4_t w) {
-        if (m == -__builtin_inff()) return;
+        if (l == 0.0f) return;
         const float t = __builtin_fmaxf(top, m);
         const float f = __builtin_amdgcn_exp2f(top - t), g = __builtin_amdgcn_exp2f(m - t);
         top = t;
@@ -572,7 +574,7 @@ __global__ __launch_bounds__(256) void tree_attn_join_kernel(AttnArgs a, int row
             add(sm_ml[from][0], sm_ml[from][1], sm_v[from]);
         }
     }
-    const bool none = r >= n * a.G || top == -__builtin_inff();
+    const bool none = r >= n * a.G || sum == 0.0f;
     const float inv = none ? 0.0f : 1.0f / sum;
     const int64_t to = ((int64_t)b * a.N + r / a.G) * a.H * a.G + h * a.G + r % a.G;
     u32x2_t w = {0, 0};

@@ -58,3 +58,69 @@ def test_single_tokens_of_wider_rows(room):
                 torch.zeros(5, 1, 16, 128, device="cuda").bfloat16()[:, :, ::2]):
         with pytest.raises(ValueError, match="dense"):
             dg.fp8_tree_attention(bad, cache, table, ctx)
+
+
+# ---- values that are not finite -----------------------------------------------------------------------
+
+SHAPES = [(1, 4, 64), (1, 3, 128), (1, 16, 256), (3, 4, 128), (24, 8, 64), (17, 4, 128)]     # N, G, D
+
+
+@pytest.mark.parametrize("N,G,D", SHAPES)
+@pytest.mark.parametrize("ctx,room", [(1, 0), (40, 0), (300, 5000), (5000, 0)])
+def test_queries_with_nan_give_nan(N, G, D, ctx, room):
+    """Rows of NaN queries are NaN where they see anything, 0 and -inf where not; the others keep
+    their bits."""
+    announce(f"NaN queries N={N} G={G} D={D} ctx={ctx} room={room}")
+    q, cache, table = call_of(3, N, 2, G, D, ctx=ctx, room=room)
+    ctxs, lens = ints(ctx, 0, ctx // 2 + 1), ints(N, N, max(N - 1, 1))
+    mask = np.stack([ft.chain(N)] * 3)
+    mask[1, 0] = False                                # sees nothing
+    words = dev(ft.pack_mask(mask))
+    o, lse = dg.fp8_tree_attention(q, cache, table, ctxs, lens, words)
+    bad = torch.zeros(3, N, 2 * G, dtype=torch.bool, device="cuda")
+    bad[0, 0, 0] = bad[1, 0] = bad[1, -1, 1] = bad[2, -1, -1] = bad[2, 0, G] = True
+    x = q.clone()
+    x[bad] = torch.where(torch.arange(D, device="cuda") == D - 5, float("nan"), x[bad])
+    ob, lb = dg.fp8_tree_attention(x, cache, table, ctxs, lens, words)
+    sees = lse > -float("inf")
+    assert not sees[1, 0].any() and sees[0].all() and sees[2, 0].all()
+    assert ob[bad & sees].isnan().all() and lb[bad & sees].isnan().all()
+    keep = ~(bad & sees)
+    assert same_bits(ob[keep], o[keep]) and same_bits(lb[keep], lse[keep])
+
+
+@pytest.mark.parametrize("N,G,D", SHAPES)
+@pytest.mark.parametrize("ctx,room,first,last", [(1, 0, 0, 1), (40, 0, 0, 40), (300, 5000, 0, 300), (300, 5000, 299, 300),
+                                                 (5000, 0, 0, 5000), (5000, 0, 0, 4000), (5000, 0, 1000, 5000), (5000, 0, 0, 1)])
+def test_cached_rows_of_nan_reach_every_row(N, G, D, ctx, room, first, last):
+    """Keys or values of NaN in positions [first, last), alone or among others, whole or a split
+    request's parts."""
+    announce(f"NaN rows of the cache N={N} G={G} D={D} ctx={ctx} room={room} {first}:{last}")
+    q, cache, table = call_of(2, N, 2, G, D, ctx=ctx, room=room)
+    ctxs, lens = ints(ctx, ctx), ints(N, N)
+    mask = dev(ft.pack_mask(np.zeros((2, N, N), bool)))     # the context alone
+    o, lse = dg.fp8_tree_attention(q, cache, table, ctxs, lens, mask)
+    at = torch.arange(first, last, device="cuda")
+    slots = (table[0, at // 16] * 16 + at % 16).int()
+    k, v = dg.fp8_kv_cache_read(cache, slots, dtype=torch.float32)
+    spoilt = torch.full_like(k, 2.0)
+    spoilt[:, 1, 7] = float("nan")                    # key head 1 of request 0
+    for keys, values in ((spoilt, v), (k, spoilt)):
+        dg.fp8_kv_cache_write(keys, values, cache, slots)
+        ob, lb = dg.fp8_tree_attention(q, cache, table, ctxs, lens, mask)
+        assert ob[0, :, G:].isnan().all() and not ob[0, :, :G].isnan().any()
+        assert lb[0, :, G:].isnan().all() if keys is spoilt else not lb.isnan().any()
+        assert same_bits(ob[1], o[1]) and same_bits(lb[1], lse[1])
+
+
+def test_parts_of_nan_are_joined():
+    """However many of a split request's first keys are NaN, whole parts of it among them."""
+    announce("NaN parts")
+    q, cache, table = call_of(1, 1, 1, 4, 128, ctx=5000)
+    scales = cache[0][1].clone()
+    for last in range(32, 1400, 32):
+        at = torch.arange(last, device="cuda")
+        cache[0][1].copy_(scales)
+        cache[0][1][table[0, at // 16].long(), 0, at % 16] = float("nan")
+        o, lse = dg.fp8_tree_attention(q, cache, table, ints(5000))
+        assert o.isnan().all() and lse.isnan().all(), last
