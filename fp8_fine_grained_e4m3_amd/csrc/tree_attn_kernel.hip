@@ -306,6 +306,20 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
     __builtin_amdgcn_sched_barrier(0);
     fetch_v(at);
     __builtin_amdgcn_sched_barrier(0);
+    // A query row with an infinity becomes one of NaN, which its softmax is: scores that
+    // are all -infinity would look like those of hidden keys.  0 * q sums to 0 or to NaN.
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        f32x4_t zero = {0, 0, 0, 0};
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) zero = mfma_bf16(bf16x8_t(0.0f), qf[t][c], zero);
+        const bool finite = zero.x == 0.0f;
+        if (!__all(finite)) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c)
+                if (!finite) qf[t][c] = bf16x8_t(__builtin_nanf(""));
+        }
+    }
     for (int s = lo + wave; s < hi; s += W) {
         const int j0 = s * kStep;
         const Place next = place(min(s + W, s_last), pages_next);

@@ -488,8 +488,8 @@ dg_status dg_fp8_kv_cache_read(const uint8_t* k_codes, const float* k_sf,
  * each j < n whose bit is set in its mask.  With N = 1 this is decode attention.
  *   S_p = scale * (q . k_p),  o = sum_p softmax(S)_p v_p,  lse = ln sum_p exp S_p
  * A token that sees nothing, and every token i >= n, gets o = 0, lse = -inf.  A
- * NaN in a token's query or in a key that it sees makes its o and lse NaN, one in
- * a value its o.
+ * NaN or an infinity in a token's query makes its o and lse NaN, and so does a
+ * NaN in a key that it sees; one in a value its o.
  *   q            [B, N, Hq, D]  bf16, q_stride elements from token to token
  *                               (a multiple of 8, request to request N times
  *                               that); Hq % H == 0, query head hq reads key

@@ -124,3 +124,30 @@ def test_parts_of_nan_are_joined():
         cache[0][1][table[0, at // 16].long(), 0, at % 16] = float("nan")
         o, lse = dg.fp8_tree_attention(q, cache, table, ints(5000))
         assert o.isnan().all() and lse.isnan().all(), last
+
+
+@pytest.mark.parametrize("N,G,D", SHAPES)
+@pytest.mark.parametrize("ctx,room", [(1, 0), (40, 0), (300, 5000), (5000, 0)])
+def test_queries_with_infinities_give_nan(N, G, D, ctx, room):
+    """Scores of infinity less infinity: NaN where the row sees anything, also where all its scores
+    are -infinity, 0 and -inf where it sees nothing."""
+    announce(f"infinite queries N={N} G={G} D={D} ctx={ctx} room={room}")
+    q, cache, table = call_of(2, N, 2, G, D, ctx=ctx, room=room)
+    (kc, ks), _ = cache
+    kc[..., D - 9] = 0x38                             # 1 in every key, so that scores have one sign
+    ctxs, lens = ints(ctx, 0), ints(N, N)
+    mask = np.stack([ft.chain(N)] * 2)
+    mask[1, 0] = False
+    words = dev(ft.pack_mask(mask))
+    o, lse = dg.fp8_tree_attention(q, cache, table, ctxs, lens, words)
+    bad = torch.zeros(2, N, 2 * G, dtype=torch.bool, device="cuda")
+    bad[0, 0, 0] = bad[0, -1, G] = bad[1, 0] = bad[1, -1, -1] = True
+    for value in (-float("inf"), float("inf")):
+        x = q.clone()
+        x[bad] = torch.where(torch.arange(D, device="cuda") == D - 9, value, x[bad])
+        ob, lb = dg.fp8_tree_attention(x, cache, table, ctxs, lens, words)
+        sees = lse > -float("inf")
+        assert sees[0].all() and not sees[1, 0].any()
+        assert ob[bad & sees].isnan().all() and lb[bad & sees].isnan().all()
+        keep = ~(bad & sees)
+        assert same_bits(ob[keep], o[keep]) and same_bits(lb[keep], lse[keep])
