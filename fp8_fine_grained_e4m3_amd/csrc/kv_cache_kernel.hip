@@ -71,8 +71,12 @@ __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
 // x / s, correctly rounded, given y = 1 / s correctly rounded: each correction adds
 // the exact remainder x - q s times y, the first leaves q within a unit in the
 // last place, and from such a q a correction with a correctly rounded reciprocal
-// gives the rounded quotient (Markstein).  s is normal; quotients too small for
-// the remainder to be exact are far below half the smallest code.
+// gives the rounded quotient (Markstein).  The remainder is a multiple of the last
+// places of q and s multiplied, and exact where that is a number of fp32: from
+// s = 2^-92 on for q >= 2^-11.  (Less than that is below half the smallest code, with
+// an exact remainder or not.)
+constexpr float kLeastScale = 0x1p-92f;
+
 __device__ __forceinline__ float quotient(float x, float s, float y) {
 #pragma clang fp contract(off)
     float q = x * y;
@@ -110,11 +114,11 @@ __global__ __launch_bounds__(kThreads) void kv_cache_write_kernel(CopyArgs a) {
     float s = __uint_as_float(m) / kMaxE4m3;
     if (s == 0.0f) s = 1.0f;
     const float y = 1.0f / s;
-    const bool normal = s >= 1.17549435e-38f;     // else 1 / s may be no number
+    const bool exact = s >= kLeastScale;
     float q[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        q[i] = normal ? quotient(x[i], s, y) : x[i] / s;
+        q[i] = exact ? quotient(x[i], s, y) : x[i] / s;
         q[i] = finite ? __builtin_fminf(__builtin_fmaxf(q[i], -kMaxE4m3), kMaxE4m3) : 0.0f;
     }
     if (slot < 0 || slot >= a.slot_count) return;

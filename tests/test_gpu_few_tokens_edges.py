@@ -151,3 +151,27 @@ def test_queries_with_infinities_give_nan(N, G, D, ctx, room):
         assert ob[bad & sees].isnan().all() and lb[bad & sees].isnan().all()
         keep = ~(bad & sees)
         assert same_bits(ob[keep], o[keep]) and same_bits(lb[keep], lse[keep])
+
+
+# ---- scales of any size ------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("low,high", [(-126, -118), (-118, -104), (-104, -88), (-88, -60), (60, 119)])
+def test_cache_quotients_at_any_scale(low, high):
+    """Quotients on and next to the midpoints of codes, for the smallest and largest scales of normal
+    numbers."""
+    announce(f"quotients at scales of 2^{low} to 2^{high}")
+    rng = np.random.default_rng(high + 200)
+    grid = ft.e4m3(np.arange(127, dtype=np.uint8))
+    mid = (grid[1:] + grid[:-1]) / 2
+    x = np.zeros((1024, 1, 256), np.float32)
+    for r in range(1024):
+        amax = np.float32(448 * np.exp2(rng.uniform(low, high)))
+        v = (mid * (amax / np.float32(448))).astype(np.float32)
+        near = np.concatenate([v, np.nextafter(v, np.float32(0 if r % 2 else np.inf))])
+        x[r, 0, :252], x[r, 0, 255] = near[:252] * rng.choice([-1, 1], 252), amax
+    cache = dg.make_fp8_kv_cache(64, 1, 16, 256)
+    dg.fp8_kv_cache_write(dev(x), dev(x), cache, torch.arange(1024, dtype=torch.int32, device="cuda"))
+    want, scale = ft.quantise_rows(x)
+    for codes, sf in cache:
+        np.testing.assert_array_equal(codes.cpu().numpy().reshape(1024, 1, 256), want)
+        np.testing.assert_array_equal(sf.cpu().numpy().reshape(1024, 1), scale)
