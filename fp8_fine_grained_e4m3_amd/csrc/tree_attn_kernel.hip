@@ -381,7 +381,7 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
         // Whether a score or a value's scale outgrows what O is relative to.  The
         // lanes look at their own; only then is the row's maximum exchanged.
         float mx[RT];
-        const float top = __builtin_fmaxf(x.vs[0], x.vs[1]);
+        const float top = __builtin_fmaxf(__builtin_fabsf(x.vs[0]), __builtin_fabsf(x.vs[1]));
         bool over = top > largest;
 #pragma unroll
         for (int t = 0; t < RT; ++t) {

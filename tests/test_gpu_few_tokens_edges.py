@@ -175,3 +175,34 @@ def test_cache_quotients_at_any_scale(low, high):
     for codes, sf in cache:
         np.testing.assert_array_equal(codes.cpu().numpy().reshape(1024, 1, 256), want)
         np.testing.assert_array_equal(sf.cpu().numpy().reshape(1024, 1), scale)
+
+
+def against_reference(q, cache, table, ctxs, lens, mask):
+    """The call's outputs, checked against the 64-bit result within its bound."""
+    B, N, _, D = q.shape
+    o, lse = dg.fp8_tree_attention(q, cache, table, ctxs, lens, dev(ft.pack_mask(mask)))
+    host = [(c.cpu().numpy(), s.cpu().numpy()) for c, s in cache]
+    ro, rl, bo, bl = ft.attention(q.float().cpu().numpy(), host, table.cpu().numpy(), ctxs.tolist(), lens.tolist(), mask,
+                                  D ** -0.5, cache[0][0].shape[2])
+    off = np.abs(o.double().cpu().numpy() - ro)
+    assert (off <= bo).all(), float((off / bo).max())
+    seen = np.isfinite(rl)
+    assert np.array_equal(np.isneginf(lse.cpu().numpy()), ~seen)
+    assert (np.abs(lse.double().cpu().numpy() - rl)[seen] <= bl[seen]).all()
+    return o, lse
+
+
+@pytest.mark.parametrize("N,G,D", SHAPES)
+@pytest.mark.parametrize("room", [0, 5000])
+def test_negative_value_scales(N, G, D, room):
+    """A cache of the caller's own may have them: all of a request's, or some."""
+    announce(f"negative value scales N={N} G={G} D={D} room={room}")
+    q, cache, table = call_of(2, N, 2, G, D, ctx=130, room=room)
+    mask = np.stack([ft.chain(N)] * 2)
+    args = ints(130, 61), ints(N, N), mask
+    _, lse = against_reference(q, cache, table, *args)
+    sf = cache[1][1]
+    sf.neg_()
+    assert same_bits(against_reference(q, cache, table, *args)[1], lse)
+    sf[:, :, ::3].neg_()
+    against_reference(q, cache, table, *args)
