@@ -27,8 +27,8 @@
 //  * P, times the values' scales, is rounded to fp16 for the second product (e4m3
 //    is exact in fp16 too): 11 bits, against bf16's 8, keep its rounding below
 //    the output's.  fp16 has few exponents, so P vs 2^(11 - x) is what is
-//    rounded, x the exponent of the largest scale that the wave has met: terms
-//    down to 2^-35 of the largest possible one count.  Maximum, sum and O are
+//    rounded, x the exponent of the largest scale that the row has seen in its wave:
+//    terms down to 2^-35 of the largest possible one count.  Maximum, sum and O are
 //    fp32.
 //  * Scores are checked against the running maximum in their own lanes, and the
 //    maximum follows, with the exchange and the scaling of O that this takes, only
@@ -204,7 +204,10 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
 
     for (; b < end && (start < s1 || (run == runs - 1 && start == total)); b += stride) {
     const Request rq = request(a, b, row0);
-    const int ctx = rq.ctx, L = rq.L, rows = rq.n * a.G;
+    const int ctx = rq.ctx, rows = rq.n * a.G;
+    // a token alone that does not see itself is as good as past the end
+    const bool blind = a.N == 1 && a.mask && !(uniform_input(reinterpret_cast<const int32_t*>(a.mask + b)) & 1);
+    const int L = blind ? min(ctx, rq.L) : rq.L;
     const int lo = (int)max(s0 - start, (int64_t)0), hi = (int)min(s1 - start, (int64_t)rq.steps);
     start += rq.steps;
     auto out_row = [&](int r) { return ((int64_t)b * a.N + r / a.G) * Hq + h * a.G + r % a.G; };
@@ -261,18 +264,23 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
         }
         return w;
     };
-    f32x4_t acc[RT][DT];                  // in units of 2^(unit - kTop)
+    f32x4_t acc[RT][DT];                  // in units of 2^(unit + more - kTop)
     float m[RT], base[RT], l[RT];         // base: m, or 0 while nothing was seen, so that exp2 stays 0
-    int unit = -1000;
+    // The exponent of the largest value scale that a row has seen is unit + more.  Rows
+    // have the same, and no more, until a masked step has one that not all of them see.
+    int unit = -1000, more[RT];
+    bool differ = false;
     float largest = 0.0f;                 // 2^unit
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
         m[t] = -__builtin_inff();
         base[t] = l[t] = 0.0f;
+        more[t] = 0;
 #pragma unroll
         for (int i = 0; i < DT; ++i) acc[t][i] = f32x4_t{0, 0, 0, 0};
     }
     const float c2 = a.scale * kLog2e;
+    const bool apart = a.N > 1;           // rows of several tokens: they may see different keys
     // The next step's keys are asked for when this step's are in the first
     // product, its values when they are in the second.  Neither is conditional
     // (past the last step the last one again), and they stay where they are
@@ -326,7 +334,7 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
         pages_next = pages;
         pages = ask(min(s + 3 * W, s_last));
         __builtin_amdgcn_sched_barrier(0);
-        const bool all = j0 + kStep <= ctx && at.live[0] && at.live[1];   // uniform: no mask here
+        const bool all = j0 + kStep <= ctx && at.live[0] && at.live[1] && !differ;   // uniform: no mask here
         float sc[RT][2][4];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -351,7 +359,7 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
             }
         }
         if (!all) {
-            const int g = fresh(lane) >> 4;
+            const int mlane = fresh(lane), g = mlane >> 4;
 #pragma unroll
             for (int t = 0; t < RT; ++t)
 #pragma unroll
@@ -361,7 +369,7 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
                         const int j = j0 + 16 * u + 4 * g + i;      // position
                         const int d = j - ctx;                      // number in the tree
                         bool seen = at.live[u] && j < L;
-                        if (seen && d >= 0)
+                        if (seen && d >= 0 && apart)
                             seen = a.mask ? (a.mask[((int64_t)b * a.N + tok[t]) * a.mask_words + (d >> 6)] >> (d & 63)) & 1
                                           : d <= tok[t];
                         if (!seen) sc[t][u][i] = -__builtin_inff();
@@ -369,10 +377,43 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
             // values past the end may hold anything: 0 * NaN must not reach O
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                if (!at.live[u] || j0 + 16 * u + 4 * g + (lane & 3) >= L) x.vs[u] = 0.0f;
+                if (!at.live[u] || j0 + 16 * u + 4 * g + (mlane & 3) >= L) x.vs[u] = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (!at.live[u] || j0 + 16 * u + 4 * g + i >= L) x.v[u][i] = typename VWord<D>::type(0);
+            }
+            // A row's scales are those of the keys that it sees: a large one that is hidden
+            // from it must not take the bits of its own.
+            if (apart) {
+                differ = false;
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                    float far = 0.0f;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const float v = __builtin_fabsf(x.vs[u]);
+                        const float vs[4] = {of_quad<0>(v), of_quad<1>(v), of_quad<2>(v), of_quad<3>(v)};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (sc[t][u][i] != -__builtin_inff()) far = __builtin_fmaxf(far, vs[i]);
+                    }
+                    const float now = __builtin_amdgcn_ldexpf(1.0f, unit + more[t]);
+                    if (__any(far > now)) {
+                        far = max_of_groups(far);
+                        const int add = far > now ? max(__builtin_amdgcn_frexp_expf(far) - unit - more[t], 0) : 0;
+                        const float shrink = __builtin_amdgcn_ldexpf(1.0f, max(-add, -1000));
+#pragma unroll
+                        for (int i = 0; i < DT; ++i) acc[t][i] *= shrink;
+                        more[t] += add;
+                    }
+                    differ |= __any(more[t] != __builtin_amdgcn_readfirstlane(more[0]));
+                }
+                if (!differ) {
+                    unit += __builtin_amdgcn_readfirstlane(more[0]);
+                    largest = __builtin_amdgcn_ldexpf(1.0f, unit);
+#pragma unroll
+                    for (int t = 0; t < RT; ++t) more[t] = 0;
+                }
             }
         }
         // A wave in its softmax goes before one in its products, which the matrix unit
@@ -381,7 +422,7 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
         // Whether a score or a value's scale outgrows what O is relative to.  The
         // lanes look at their own; only then is the row's maximum exchanged.
         float mx[RT];
-        const float top = __builtin_fmaxf(__builtin_fabsf(x.vs[0]), __builtin_fabsf(x.vs[1]));
+        const float top = all || !apart ? __builtin_fmaxf(__builtin_fabsf(x.vs[0]), __builtin_fabsf(x.vs[1])) : 0.0f;
         bool over = top > largest;
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
@@ -396,10 +437,10 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
             float far = __builtin_fmaxf(__builtin_fmaxf(of_quad<0>(top), of_quad<1>(top)),
                                         __builtin_fmaxf(of_quad<2>(top), of_quad<3>(top)));
             far = max_of_groups(__builtin_fmaxf(far, largest));
-            const int now = far > largest ? __builtin_amdgcn_readfirstlane(__builtin_amdgcn_frexp_expf(far)) : unit;
+            const int now = __builtin_amdgcn_readfirstlane(far > largest ? __builtin_amdgcn_frexp_expf(far) : unit);
             const float shrink = __builtin_amdgcn_ldexpf(1.0f, max(unit - now, -1000));
             unit = now;
-            if (far > largest) largest = __builtin_amdgcn_ldexpf(1.0f, now);
+            largest = __builtin_amdgcn_ldexpf(1.0f, now);
 #pragma unroll
             for (int t = 0; t < RT; ++t) {
                 mx[t] = __builtin_fmaxf(max_of_groups(mx[t]), m[t]);
@@ -411,14 +452,14 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
                 m[t] = mx[t];
             }
         }
-        float vscale[2][4];               // in units of the largest so far
+        float vs[2][4];                   // without a mask in units of the largest so far
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const float v = __builtin_amdgcn_ldexpf(x.vs[u], kTop - unit);
-            vscale[u][0] = of_quad<0>(v);
-            vscale[u][1] = of_quad<1>(v);
-            vscale[u][2] = of_quad<2>(v);
-            vscale[u][3] = of_quad<3>(v);
+            const float v = __builtin_amdgcn_ldexpf(x.vs[u], all ? kTop - unit : 0);
+            vs[u][0] = of_quad<0>(v);
+            vs[u][1] = of_quad<1>(v);
+            vs[u][2] = of_quad<2>(v);
+            vs[u][3] = of_quad<3>(v);
         }
         f16x8_t pf[RT];
         auto weigh = [&](auto some_hidden) {
@@ -431,9 +472,10 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
                     for (int i = 0; i < 4; ++i) {
                         const float e = __builtin_amdgcn_exp2f(sc[t][u][i] - base[t]);
                         l[t] += e;
-                        p[u][i] = e * vscale[u][i];
+                        if (!decltype(some_hidden)::value) p[u][i] = e * vs[u][i];
                         // a hidden key's weight is 0 whatever its value's scale
-                        if (decltype(some_hidden)::value && sc[t][u][i] == -__builtin_inff()) p[u][i] = 0.0f;
+                        else if (sc[t][u][i] == -__builtin_inff()) p[u][i] = 0.0f;
+                        else p[u][i] = e * __builtin_amdgcn_ldexpf(vs[u][i], kTop - unit - more[t]);
                     }
                 u32x4_t w;
 #pragma unroll
@@ -483,7 +525,7 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
     for (int t = 0; t < RT; ++t) {
         l[t] = sum_of_groups(l[t]);
         if (eg == 0) sm_ml[wave][16 * t + er16] = f32x2_t{m[t], l[t]};
-        const float f = __builtin_amdgcn_ldexpf(1.0f, max(unit - kTop, -1000));
+        const float f = __builtin_amdgcn_ldexpf(1.0f, max(unit + more[t] - kTop, -1000));
         float* mine = sm_o[wave] + (16 * t + er16) * PITCH + 4 * eg * DT;
 #pragma unroll
         for (int i = 0; i < 4; ++i)

@@ -505,8 +505,8 @@ dg_status dg_fp8_kv_cache_read(const uint8_t* k_codes, const float* k_sf,
  *   o            [B, N, Hq, D]  bf16, rounded once from fp32 sums.  A key's weight
  *                               times its value's scale is kept to 11 bits, and
  *                               to 2^-35 of the row's largest weight times the
- *                               request's largest value scale: what is less may
- *                               count as 0.
+ *                               largest value scale of what the row sees: what is
+ *                               less may count as 0.
  *   lse          [B, N, Hq]     fp32
  * Tree positions past max_pages * page_size are not seen.  Codes 0x7F and 0xFF
  * (NaN) are not allowed at positions below c + n; dg_fp8_kv_cache_write never

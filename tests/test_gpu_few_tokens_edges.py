@@ -206,3 +206,42 @@ def test_negative_value_scales(N, G, D, room):
     assert same_bits(against_reference(q, cache, table, *args)[1], lse)
     sf[:, :, ::3].neg_()
     against_reference(q, cache, table, *args)
+
+
+@pytest.mark.parametrize("N,G,D,ctx,room", [(6, 4, 64, 10, 0), (6, 4, 128, 3, 5000), (8, 2, 256, 0, 0), (24, 8, 64, 40, 0),
+                                            (40, 2, 128, 0, 5000), (130, 1, 128, 5, 0), (130, 1, 64, 700, 5000)])
+@pytest.mark.parametrize("factor", [2.0 ** 30, 2.0 ** 60, float("inf")])
+def test_large_values_of_unseen_tokens_do_not_touch_others(N, G, D, ctx, room, factor):
+    """A drafted token's values far larger than all others leave the rows that do not see it as they
+    were, bit for bit, and the others within their bound."""
+    announce(f"large unseen values N={N} G={G} D={D} ctx={ctx} room={room} {factor}")
+    q, cache, table = call_of(1, N, 2, G, D, ctx=ctx, room=room)
+    ctxs, lens = ints(ctx), ints(N)
+    mask = np.stack([ft.chain(N)])
+    mask[0, 1:, 0] = np.arange(1, N) % 3 == 0          # who sees token 0
+    mask[0, 3:, 2] = False                            # and token 2: itself alone
+    o, lse = against_reference(q, cache, table, ctxs, lens, mask)
+    for token in (0, 2):
+        at = ctx + token
+        cache[1][1][table[0, at // 16].long(), :, at % 16] *= factor
+    sees = torch.from_numpy(mask[0, :, 0] | mask[0, :, 2]).cuda()
+    if np.isfinite(factor):
+        ob, lb = against_reference(q, cache, table, ctxs, lens, mask)
+    else:
+        ob, lb = dg.fp8_tree_attention(q, cache, table, ctxs, lens, dev(ft.pack_mask(mask)))
+        assert not ob[0, sees].isfinite().any()
+    assert same_bits(ob[0, ~sees], o[0, ~sees]) and same_bits(lb, lse)
+
+
+@pytest.mark.parametrize("G,D,ctx,room", [(4, 64, 10, 0), (3, 128, 31, 5000), (16, 256, 32, 0), (8, 128, 300, 5000), (33, 64, 0, 0)])
+def test_a_single_token_that_does_not_see_itself(G, D, ctx, room):
+    announce(f"blind single tokens G={G} D={D} ctx={ctx} room={room}")
+    q, cache, table = call_of(2, 1, 2, G, D, ctx=ctx, room=room)
+    ctxs, lens, mask = ints(ctx, ctx), ints(1, 1), np.array([[[False]], [[True]]])
+    o, lse = against_reference(q, cache, table, ctxs, lens, mask)
+    for factor in (2.0 ** 60, float("inf"), float("nan")):
+        sf = cache[1][1].clone()
+        cache[1][1][table[0, ctx // 16].long(), :, ctx % 16] *= factor
+        ob, lb = dg.fp8_tree_attention(q, cache, table, ctxs, lens, dev(ft.pack_mask(mask)))
+        assert same_bits(ob, o) and same_bits(lb, lse)
+        cache[1][1].copy_(sf)
