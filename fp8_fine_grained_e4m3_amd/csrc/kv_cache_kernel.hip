@@ -33,7 +33,7 @@ struct CopyArgs {
     uint8_t* codes[2];
     float* sf[2];
     int64_t stride[2];
-    int64_t total;                  // T * H rows
+    int64_t total;                  // rows: tokens * H
     int64_t slot_count;             // num_pages * page_size
     int H, page_shift;
 };
@@ -163,7 +163,7 @@ __global__ __launch_bounds__(kThreads) void kv_cache_read_kernel(CopyArgs a) {
 }
 
 template <int D>
-hipError_t launch(const CopyArgs& a, bool f32, bool write, hipStream_t stream) {
+hipError_t launch_piece(const CopyArgs& a, bool f32, bool write, hipStream_t stream) {
     constexpr int64_t rows = kThreads / (D / kEpl);
     const dim3 grid((unsigned)((a.total + rows - 1) / rows), 2), block(kThreads);
     if (write) {
@@ -176,6 +176,21 @@ hipError_t launch(const CopyArgs& a, bool f32, bool write, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// A grid has fewer than 2^32 threads, so tokens beyond 2^31 threads' take further launches.
+template <int D>
+hipError_t launch(const CopyArgs& a, int64_t T, bool f32, bool write, hipStream_t stream) {
+    const int64_t piece = (1ll << 31) / (a.H * (D / kEpl));      // H is at most 65535
+    for (int64_t t = 0; t < T; t += piece) {
+        CopyArgs b = a;
+        b.slots = a.slots + t;
+        for (int i = 0; i < 2; ++i) b.rows[i] = static_cast<char*>(a.rows[i]) + t * a.stride[i] * (f32 ? 4 : 2);
+        b.total = (T - t < piece ? T - t : piece) * a.H;
+        const hipError_t e = launch_piece<D>(b, f32, write, stream);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
 hipError_t launch(const KvCopy& p, bool write, hipStream_t stream) {
     CopyArgs a;
     a.slots = p.slots;
@@ -183,14 +198,13 @@ hipError_t launch(const KvCopy& p, bool write, hipStream_t stream) {
     a.codes[0] = p.cache.k_codes; a.codes[1] = p.cache.v_codes;
     a.sf[0] = p.cache.k_sf; a.sf[1] = p.cache.v_sf;
     a.stride[0] = p.k_stride; a.stride[1] = p.v_stride;
-    a.total = p.T * p.cache.H;
     a.slot_count = p.cache.num_pages * p.cache.page_size;
     a.H = (int)p.cache.H;
     a.page_shift = __builtin_ctzll((unsigned long long)p.cache.page_size);
     switch (p.cache.D) {
-    case 64: return launch<64>(a, p.f32, write, stream);
-    case 128: return launch<128>(a, p.f32, write, stream);
-    case 256: return launch<256>(a, p.f32, write, stream);
+    case 64: return launch<64>(a, p.T, p.f32, write, stream);
+    case 128: return launch<128>(a, p.T, p.f32, write, stream);
+    case 256: return launch<256>(a, p.T, p.f32, write, stream);
     default: return hipErrorInvalidValue;
     }
 }

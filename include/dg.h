@@ -459,7 +459,7 @@ dg_status dg_fp8_mqa_logits(const uint8_t* q, const uint8_t* kv, const float* kv
  *   slots    [T]        int32; a slot outside [0, num_pages * page_size) marks
  *                       a token that is not stored.  A slot given twice in one
  *                       call leaves either token's values, in whole codes.
- * One kernel launch.
+ * One kernel launch for each 2^34 values of k.
  */
 dg_status dg_fp8_kv_cache_write(const void* k, const void* v, dg_dtype dtype,
                                 int64_t k_stride, int64_t v_stride, const int32_t* slots,
@@ -471,7 +471,7 @@ dg_status dg_fp8_kv_cache_write(const void* k, const void* v, dg_dtype dtype,
  * Reads T slots back: k[t, h, :] = code * sf in fp32, rounded once for
  * DG_BF16; a slot outside the cache gives zeros.
  *   k, v  [T, H, D] of dtype, dense.
- * One kernel launch.
+ * One kernel launch for each 2^34 values of k.
  */
 dg_status dg_fp8_kv_cache_read(const uint8_t* k_codes, const float* k_sf,
                                const uint8_t* v_codes, const float* v_sf, const int32_t* slots,

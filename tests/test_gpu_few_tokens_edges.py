@@ -188,7 +188,7 @@ def against_reference(q, cache, table, ctxs, lens, mask):
     assert (off <= bo).all(), float((off / bo).max())
     seen = np.isfinite(rl)
     assert np.array_equal(np.isneginf(lse.cpu().numpy()), ~seen)
-    assert (np.abs(lse.double().cpu().numpy() - rl)[seen] <= bl[seen]).all()
+    assert (np.abs(lse.double().cpu().numpy()[seen] - rl[seen]) <= bl[seen]).all()
     return o, lse
 
 
@@ -245,3 +245,33 @@ def test_a_single_token_that_does_not_see_itself(G, D, ctx, room):
         ob, lb = dg.fp8_tree_attention(q, cache, table, ctxs, lens, dev(ft.pack_mask(mask)))
         assert same_bits(ob, o) and same_bits(lb, lse)
         cache[1][1].copy_(sf)
+
+
+# ---- past a grid's limit ---------------------------------------------------------------------------------
+
+def test_cache_copies_of_more_than_2_to_the_32_threads():
+    """2^27 rows of 256 values and a few: 64 GiB of keys, of which a few tokens are stored."""
+    announce("cache copies past 2^32 threads")
+    D, T = 256, (1 << 27) + 5
+    if torch.cuda.mem_get_info()[0] < 150 << 30:
+        pytest.skip("too little memory")
+    at = torch.tensor([0, 1, 77, (1 << 26) - 1, 1 << 26, (1 << 26) + 1, (1 << 27) - 1, 1 << 27, T - 2, T - 1], device="cuda")
+    n = len(at)
+    few = torch.randn(n, 1, D, device="cuda").bfloat16()
+    k = torch.empty(T, 1, D, dtype=torch.bfloat16, device="cuda")
+    k[at] = few
+    slots = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    slots[at] = torch.arange(n, dtype=torch.int32, device="cuda") * 3
+    cache, want = dg.make_fp8_kv_cache(2, 1, 16, D), dg.make_fp8_kv_cache(2, 1, 16, D)
+    dg.fp8_kv_cache_write(k, k, cache, slots)
+    dg.fp8_kv_cache_write(few, few, want, slots[at])
+    for (codes, sf), (wc, ws) in zip(cache, want):
+        assert torch.equal(codes, wc) and torch.equal(sf, ws)
+    v = torch.empty_like(k)
+    near = torch.cat([at, torch.tensor([2, (1 << 26) + 2, T - 3], device="cuda")])
+    k[near], v[near] = 5.0, 5.0
+    dg.fp8_kv_cache_read(cache, slots, out=(k, v))
+    for rows in (k, v):
+        assert same_bits(rows[at], dg.fp8_kv_cache_read(want, slots[at])[0]) and not rows[near[n:]].any()
+    del k, v, rows, slots
+    torch.cuda.empty_cache()
