@@ -572,14 +572,14 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
 // them side by side, which go through the parts with a running maximum, four at
 // a time, and meet in LDS.
 template <int D, int SIDE>
-__global__ __launch_bounds__(256) void tree_attn_join_kernel(AttnArgs a, int rows_of_block) {
+__global__ __launch_bounds__(256) void tree_attn_join_kernel(AttnArgs a, int rows_of_block, int64_t first_row) {
     constexpr int TPR = D / 4, RPB = 256 / (TPR * SIDE);
     static_assert(SIDE == 1 || RPB == 1, "threads that meet return together");
     __shared__ f32x4_t sm_v[SIDE > 1 ? 256 : 1];
     __shared__ float sm_ml[SIDE > 1 ? 256 : 1][2];
     const int all_rows = a.N * a.G;
     const int side = threadIdx.x / TPR % SIDE, d = threadIdx.x % TPR * 4;
-    const int64_t id = (int64_t)blockIdx.x * RPB + threadIdx.x / (TPR * SIDE);   // (b, h, row)
+    const int64_t id = first_row + (int64_t)blockIdx.x * RPB + threadIdx.x / (TPR * SIDE);   // (b, h, row)
     if (id >= (int64_t)a.B * a.H * all_rows) return;
     const int64_t bh = id / all_rows;
     const int r = (int)(id - bh * all_rows), b = (int)(bh / a.H), h = (int)(bh - (int64_t)b * a.H);
@@ -715,12 +715,21 @@ hipError_t launch(const AttnArgs& a, const Shape& s, hipStream_t stream) {
     if (e != hipSuccess || a.whole || a.runs == 1) return e;
     // few rows have many parts each: a workgroup a row, else a thread for each four values
     const int64_t rows = (int64_t)a.B * a.H * a.N * a.G, per = 256 / (D / 4);
-    if (rows <= 4096)
-        hipLaunchKernelGGL((tree_attn_join_kernel<D, 1024 / D>), dim3((unsigned)rows), dim3(256), 0, stream, a, s.rows());
-    else
-        hipLaunchKernelGGL((tree_attn_join_kernel<D, 1>), dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0,
-                           stream, a, s.rows());
-    return hipGetLastError();
+    if (rows <= 4096) {
+        hipLaunchKernelGGL((tree_attn_join_kernel<D, 1024 / D>), dim3((unsigned)rows), dim3(256), 0, stream, a, s.rows(),
+                           (int64_t)0);
+        return hipGetLastError();
+    }
+    // a grid has fewer than 2^32 threads: rows beyond 2^31 threads' take further launches
+    const int64_t piece = (1ll << 31) / 256 * per;
+    for (int64_t row = 0; row < rows; row += piece) {
+        const int64_t n = std::min(piece, rows - row);
+        hipLaunchKernelGGL((tree_attn_join_kernel<D, 1>), dim3((unsigned)((n + per - 1) / per)), dim3(256), 0, stream, a,
+                           s.rows(), row);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 int64_t split_bytes(int64_t B, int64_t H, const Shape& s) { return (B * H * s.row_blocks * 8 + 15) / 16 * 16; }

@@ -515,7 +515,8 @@ dg_status dg_fp8_kv_cache_read(const uint8_t* k_codes, const float* k_sf,
  * workspace: dg_fp8_tree_attention_workspace_bytes of the same sizes (0 where no
  * request is ever split over workgroups), never initialised, not shared by calls
  * that may overlap.  How a request is split goes by the lengths of all of them;
- * the same inputs give the same bits.  One or two kernel launches.
+ * the same inputs give the same bits.  One or two kernel launches, and a further one
+ * for each 2^33 values of o beyond the first 2^33 where requests are split.
  */
 dg_status dg_fp8_tree_attention(const void* q, int64_t q_stride,
                                 const uint8_t* k_codes, const float* k_sf,

@@ -275,3 +275,24 @@ def test_cache_copies_of_more_than_2_to_the_32_threads():
         assert same_bits(rows[at], dg.fp8_kv_cache_read(want, slots[at])[0]) and not rows[near[n:]].any()
     del k, v, rows, slots
     torch.cuda.empty_cache()
+
+
+def test_joining_more_than_2_to_the_32_threads():
+    """32768 requests of 8192 query heads, D = 64: 2^34 values of o, two runs, so that the second
+    kernel looks at every row."""
+    announce("joined rows past 2^32 threads")
+    B, Hq, D, turn = 32768 + 16, 8192, 64, 16
+    if torch.cuda.mem_get_info()[0] < 90 << 30:
+        pytest.skip("too little memory")
+    small_q, cache, table = call_of(turn, 1, 1, Hq, D, ctx=16)
+    ctx = torch.arange(turn, dtype=torch.int32, device="cuda")
+    want, want_lse = dg.fp8_tree_attention(small_q, cache, table, ctx)
+    assert dg.get_fp8_tree_attention_workspace_bytes(B, 1, Hq, 1, D, 16, table.shape[1]) > 0
+    q = small_q.repeat(B // turn, 1, 1, 1)
+    o, lse = dg.fp8_tree_attention(q, cache, table.repeat(B // turn, 1), ctx.repeat(B // turn))
+    del q
+    o, lse = o.view(B // turn, turn, 1, Hq, D), lse.view(B // turn, turn, 1, Hq)
+    for i in range(B // turn):
+        assert torch.equal(o[i], want) and torch.equal(lse[i], want_lse), i
+    del o, lse
+    torch.cuda.empty_cache()
