@@ -671,8 +671,9 @@ def _call(fn: str, device: int, *args):
 def fp8_kv_cache_write(k: torch.Tensor, v: torch.Tensor, cache, slots: torch.Tensor):
     """Quantises k, v [T, H, D] (bf16 or fp32; tokens may be strided, as in a
     slice of a fused projection) into the cache's slots (int32 [T], page *
-    page_size + offset; a slot outside the cache stores nothing).  One fp32
-    scale per token and head.  Changes and returns the cache
+    page_size + offset; a slot outside the cache stores nothing, one given twice
+    is left with either token's codes and either one's scale).  One fp32 scale
+    per token and head.  Changes and returns the cache
     (make_fp8_kv_cache)."""
     kc, ks, vc, vs, (P, H, page, D), on = _cache(cache)
     T = slots.shape[0] if slots.dim() == 1 else -1

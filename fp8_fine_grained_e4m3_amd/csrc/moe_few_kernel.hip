@@ -29,7 +29,7 @@
 //
 // Measured, times of a whole layer with the weights' bytes over them: 1 token of
 // 6 in 32 experts, 4096 x 2048: 37 us, 4.1 TB/s (each kernel's start and end are
-// a third of it); 13 tokens: 134 us, 5.5 TB/s; 64 of 8 in 64 experts, 7168 x
+// a third of it); 13 tokens: 134 to 140 us, 5.2 to 5.5 TB/s; 64 of 8 in 64 experts, 7168 x
 // 2048, fp32: 536 us, 5.3 TB/s.  A plain read of as many bytes reaches 6.2.
 #include "fp8_values.h"
 #include "serve_internal.h"

@@ -50,9 +50,11 @@
 // (Joined by the last workgroup to arrive instead, a long request's
 // parts pass through one CU: 344 us against 174 for two trees of 16 over 100001
 // tokens, both as they were then.)
-// Measured: 32 single tokens over 8192, 32 / 8 heads of 128, 89 us, 4.7 TB/s; two
-// trees of 16 over 100001, 64 / 8 heads of 128, 141 us, 2.2 TB/s and 0.56 PFLOP/s
-// with the VALU 57% and the matrix unit 22% busy; 7 trees of 24 over 3001, 21 us.
+// Measured (a batch "of n over c" goes from n tokens and c positions down to half of
+// them): 32 single tokens over 8192, 32 / 8 heads of 128, 417 MB, 90 us, 4.6 TB/s;
+// two trees of 16 over 100001, 64 / 8 heads of 128, 317 MB and 66 GFLOP, 141 us,
+// 2.2 TB/s and 0.46 PFLOP/s with the VALU 47% and the matrix unit 20% busy; 7 trees
+// of 24 over 3001, the last of them idle, 21 us.
 #include "fp8_values.h"
 #include "serve_internal.h"
 
@@ -653,7 +655,8 @@ struct Shape {
 // whatever the lengths turn out to be: up to 1024 positions, or up to 2048 where
 // requests and heads make 128 workgroups, up to 4096 where they make 256 or have
 // two row tiles.  Their waves are as many as are resident with all the others, up
-// to eight for two row tiles and four else, but at most 16 steps fall to one (60
+// to eight for two row tiles and four else, and halved only where that leaves a wave
+// 16 steps at most (with all four, up to 32 fall to a wave of one row tile) (60
 // trees of 24 over 221: 45 us with one wave, 60 with four, 100 with eight; 16 of 64
 // over 300: 22 with two, 28 with four, 43 with eight; 8 of 16 over 1000: 17 with
 // eight, 19 with four, 27 with two).  In graphs, whole against split: 16

@@ -440,9 +440,10 @@ dg_status dg_fp8_mqa_logits(const uint8_t* q, const uint8_t* kv, const float* kv
  * The cache is paged.  For the keys and for the values:
  *   codes [num_pages, H, page_size, D]  e4m3
  *   sf    [num_pages, H, page_size]     fp32, one scale per token and head
- * with value = code * sf.  H is the number of key/value heads, D is 64, 128 or
- * 256, page_size a power of two from 16 to 4096, num_pages * page_size < 2^31.
- * A token's place is its slot, page * page_size + offset.
+ * with value = code * sf; dg_fp8_kv_cache_write makes scales that are positive or
+ * NaN, a caller's own may have either sign.  H is the number of key/value heads, D
+ * is 64, 128 or 256, page_size a power of two from 16 to 4096, num_pages *
+ * page_size < 2^31.  A token's place is its slot, page * page_size + offset.
  */
 
 /*
@@ -458,7 +459,8 @@ dg_status dg_fp8_mqa_logits(const uint8_t* q, const uint8_t* kv, const float* kv
  *                       16-byte multiples; heads and D dense
  *   slots    [T]        int32; a slot outside [0, num_pages * page_size) marks
  *                       a token that is not stored.  A slot given twice in one
- *                       call leaves either token's values, in whole codes.
+ *                       call is the caller's mistake: what it holds afterwards
+ *                       is either token's codes and either token's scale.
  * One kernel launch for each 2^34 values of k.
  */
 dg_status dg_fp8_kv_cache_write(const void* k, const void* v, dg_dtype dtype,
@@ -572,7 +574,9 @@ const char* dg_last_error(void);
  * (DeepGEMM Documentation, section 10: set/get the maximum SM count).
  * dg_get_num_cus() returns the current cap (the device's CU count by
  * default, 0 if no device is visible); dg_set_num_cus(n) accepts
- * 1 <= n <= device CU count, or 0 to restore the default.
+ * 1 <= n <= device CU count, or 0 to restore the default.  The casts, the
+ * indexer's logits and the few-token calls are not persistent: they launch
+ * what their sizes ask for, whatever the cap.
  */
 int dg_get_num_cus(void);
 dg_status dg_set_num_cus(int n);
