@@ -75,6 +75,9 @@ constexpr int kStep = 32;                 // keys of a wave's step
 constexpr int kBrief = 24, kFew = 64;
 constexpr int kTop = 11;                  // P of a value with the largest scale is below 2^(kTop + kLazy)
 constexpr float kLazy = 4.0f;             // how far, in powers of two, scores pass m before m follows
+// O is put down 2^kSpare too small: waves and parts, 8 x 768 at most, each with a sum
+// below 1, then add up without passing fp32's largest number, whatever the values.
+constexpr int kSpare = 13;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -526,15 +529,18 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
         l[t] = sum_of_groups(l[t]);
-        if (eg == 0) sm_ml[wave][16 * t + er16] = f32x2_t{m[t], l[t]};
-        const float f = __builtin_amdgcn_ldexpf(1.0f, max(unit + more[t] - kTop, -1000));
+        // the sum's power of two goes to the maximum
+        const int k = __builtin_amdgcn_frexp_expf(l[t]), shift = unit + more[t] - kTop - k - kSpare;
+        if (eg == 0) sm_ml[wave][16 * t + er16] = f32x2_t{m[t] + (float)k, __builtin_amdgcn_ldexpf(l[t], -k)};
         float* mine = sm_o[wave] + (16 * t + er16) * PITCH + 4 * eg * DT;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int c = 0; c < DT / 4; ++c)
                 *reinterpret_cast<f32x4_t*>(mine + i * DT + 4 * c) =
-                    f32x4_t{acc[t][4 * c][i] * f, acc[t][4 * c + 1][i] * f, acc[t][4 * c + 2][i] * f, acc[t][4 * c + 3][i] * f};
+                    f32x4_t{__builtin_amdgcn_ldexpf(acc[t][4 * c][i], shift), __builtin_amdgcn_ldexpf(acc[t][4 * c + 1][i], shift),
+                            __builtin_amdgcn_ldexpf(acc[t][4 * c + 2][i], shift),
+                            __builtin_amdgcn_ldexpf(acc[t][4 * c + 3][i], shift)};
     }
     __syncthreads();
     // A run has one part of a request that goes on from the run before (the first
@@ -558,7 +564,7 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
             if (d == 0) *reinterpret_cast<f32x2_t*>(part + ROWS * D + 2 * r) = f32x2_t{top, sum};
         } else if (row0 + r < all_rows) {
             const bool none = row0 + r >= rows || sum == 0.0f;      // a sum of NaN is none of it
-            const float inv = none ? 0.0f : 1.0f / sum;
+            const float inv = none ? 0.0f : (1 << kSpare) / sum;
             const int64_t at = out_row(row0 + r);
             u32x2_t w = {0, 0};
             if (!none) w = u32x2_t{f32x2_to_bf16x2(v.x * inv, v.y * inv), f32x2_to_bf16x2(v.z * inv, v.w * inv)};
@@ -633,7 +639,7 @@ __global__ __launch_bounds__(256) void tree_attn_join_kernel(AttnArgs a, int row
         }
     }
     const bool none = r >= n * a.G || sum == 0.0f;
-    const float inv = none ? 0.0f : 1.0f / sum;
+    const float inv = none ? 0.0f : (1 << kSpare) / sum;
     const int64_t to = ((int64_t)b * a.N + r / a.G) * a.H * a.G + h * a.G + r % a.G;
     u32x2_t w = {0, 0};
     if (!none) w = u32x2_t{f32x2_to_bf16x2(v.x * inv, v.y * inv), f32x2_to_bf16x2(v.z * inv, v.w * inv)};

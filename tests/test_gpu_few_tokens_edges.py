@@ -247,6 +247,30 @@ def test_a_single_token_that_does_not_see_itself(G, D, ctx, room):
         cache[1][1].copy_(sf)
 
 
+@pytest.mark.parametrize("N,G,D", SHAPES)
+@pytest.mark.parametrize("ctx,room", [(40, 0), (300, 5000), (5000, 0)])
+@pytest.mark.parametrize("power", [-118, -60, 60, 118])
+def test_values_of_any_size(N, G, D, ctx, room, power):
+    """Values multiplied by a power of two multiply o by it, up to the largest numbers of bf16 and
+    down to the smallest normal ones."""
+    announce(f"values of 2^{power} N={N} G={G} D={D} ctx={ctx} room={room}")
+    q, cache, table = call_of(2, N, 2, G, D, ctx=ctx, room=room)
+    q = q * 2.0 ** -6                                 # weights that are nearly even
+    ctxs, lens = ints(ctx, ctx // 3), ints(N, N)
+    o, lse = dg.fp8_tree_attention(q, cache, table, ctxs, lens)
+    sf = cache[1][1]
+    assert 448 * sf.max() < 2.0 ** 9                  # so that no value passes 2^127
+    sf.copy_(torch.from_numpy(np.ldexp(sf.cpu().numpy(), power)))
+    ob, lb = dg.fp8_tree_attention(q, cache, table, ctxs, lens)
+    want = np.ldexp(o.double().cpu().numpy(), power)
+    got = ob.double().cpu().numpy()
+    # Sums are put down 2^13 too small, over a sum of weights of 1/2 or more: below the normal
+    # numbers of fp32 each of some (16 + 3 * 80 parts) roundings is 2^-150 * 2^14 of o, and then
+    # bf16 may round to the other side.  Otherwise nothing is lost.
+    off = 0.0 if power > -64 else 2.0 ** -128 + 2.0 ** -7 * np.abs(want)
+    assert same_bits(lb, lse) and (np.abs(got - want) <= off).all()
+
+
 # ---- past a grid's limit ---------------------------------------------------------------------------------
 
 def test_cache_copies_of_more_than_2_to_the_32_threads():
