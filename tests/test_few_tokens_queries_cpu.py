@@ -63,7 +63,7 @@ def test_queries_that_are_not_dense_are_refused(attend, B, N, name, make):
     ("dense", lambda: rows(4, 1, 8, 128), 1024),
     ("heads of a wider row", lambda: rows(4, 12, 128)[:, 2:10].unsqueeze(1), 1536),
     ("heads of a wider row, by token", lambda: rows(4, 1, 12, 128)[:, :, 2:10], 1536),
-    ("the last of each request's tokens", lambda: rows(4, 3, 8, 128)[:, 2:], 3072),
+    ("the last of each request's tokens", lambda: rows(4, 5, 8, 128)[:, 4:], 5120),
     ("one head", lambda: rows(4, 1, 4, 128)[:, :, 1:2], 512),
     ("tokens of a wider row", lambda: rows(4, 3, 12, 128)[:, :, 2:10], 1536),
     ("one request", lambda: rows(1, 3, 12, 128)[:, :, 2:10], 1536)])
@@ -74,7 +74,7 @@ def test_queries_of_wider_rows_pass_their_stride(attend, name, make, stride):
     assert o.shape == q.shape and lse.shape == q.shape[:3] and o.is_contiguous()
 
 
-@pytest.mark.parametrize("q", [rows(4, 0, 8, 128), rows(4, 3, 8, 128)[:, 3:], rows(1, 0, 8, 128), rows(0, 0, 8, 128),
+@pytest.mark.parametrize("q", [rows(4, 0, 8, 128), rows(4, 5, 8, 128)[:, 5:], rows(1, 0, 8, 128), rows(0, 0, 8, 128),
                                rows(0, 3, 8, 128), rows(4, 3, 0, 128)], ids=lambda q: str(tuple(q.shape)))
 def test_queries_of_nothing(attend, q):
     """No requests, tokens or heads are no work and no error, as in the C call."""
