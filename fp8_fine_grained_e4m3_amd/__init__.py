@@ -68,6 +68,7 @@ EXPORTED = (
     "dg_fp8_tree_attention_workspace_bytes",
     "dg_fp8_moe_few_tokens",
     "dg_fp8_moe_few_tokens_workspace_bytes",
+    "dg_kv_cache_plan",
 )
 DG_CAST_POW2_SCALE = 1
 
@@ -135,6 +136,8 @@ def load_library(path: Optional[str] = None):
                  "dg_m_grouped_fp8_gemm_nt_masked_ue8m0", "dg_pack_ue8m0_scales"):
         getattr(lib, name).restype = I
     F = ctypes.c_float
+    lib.dg_kv_cache_plan.argtypes = [P] * 9 + [I64, I64, I, I64, I64, I64, P]
+    lib.dg_kv_cache_plan.restype = I
     lib.dg_fp8_kv_cache_write.argtypes = [P, P, I, I64, I64, P, P, P, P, P, I64, I64, I64, I64, I64, P]
     lib.dg_fp8_kv_cache_read.argtypes = [P, P, P, P, P, P, P, I, I64, I64, I64, I64, I64, P]
     lib.dg_fp8_tree_attention.argtypes = [P, I64, P, P, P, P, P, P, P, P, P, P, F, I64, I64, I64, I64,
@@ -719,6 +722,62 @@ def fp8_kv_cache_read(cache, slots: torch.Tensor, dtype: torch.dtype = torch.bfl
     _call("dg_fp8_kv_cache_read", on, kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), slots.data_ptr(),
           k.data_ptr(), v.data_ptr(), _ROW_TYPES[k.dtype], T, H, D, P, page)
     return k, v
+
+
+def make_kv_page_pool(num_pages: int, device=None):
+    """A pool in which all of a cache's pages are free: (pages int32 [num_pages], a
+    ring, state int32 [2]: the place of the first free page, and how many are free)."""
+    device = torch.cuda.current_device() if device is None else device
+    return (torch.arange(num_pages, dtype=torch.int32, device=device),
+            torch.tensor([0, num_pages], dtype=torch.int32, device=device))
+
+
+def kv_cache_plan(page_table: torch.Tensor, context_lens: torch.Tensor, add_lens: torch.Tensor, pool, page_size: int,
+                  rows: int, padded: bool = False, out=None):
+    """Gives requests their pages and new tokens their slots.  Request b of
+    context_lens[b] tokens (int32 [B]) gets add_lens[b] more (int32 [B]); where that
+    is negative it loses tokens at its end.  pool = (pages, state), as
+    make_kv_page_pool makes it.  New pages go from the pool into page_table (int32
+    [B, max_pages]), pages behind a new end back into it; both are changed in place.
+    Returns (slots, positions, lens, state): int32 [B, rows] where padded, else
+    [rows], the requests' tokens end to end (rows without a token, and tokens of
+    requests that the pool or the table has no room for, have the slot -1); the lengths
+    afterwards, int32 [B] (as before where there was no room); the pool's state
+    afterwards, int32 [2].  out: these four, to be filled, other tensors than the
+    arguments."""
+    pages, state = pool
+    table, ctx, add = page_table, context_lens, add_lens
+    if table.dim() != 2 or pages.dim() != 1:
+        raise ValueError(f"page_table {tuple(table.shape)} and the pool's pages {tuple(pages.shape)} must be "
+                         "[B, max_pages] and [num_pages]")
+    (B, most), P, on = table.shape, pages.shape[0], table.get_device()
+    if not (table.dtype is _I32 and ctx.dtype is _I32 and add.dtype is _I32 and pages.dtype is _I32 and state.dtype is _I32
+            and ctx.shape == (B,) and add.shape == (B,) and state.shape == (2,) and on >= 0
+            and table.is_contiguous() and ctx.is_contiguous() and add.is_contiguous() and pages.is_contiguous()
+            and state.is_contiguous() and ctx.get_device() == on and add.get_device() == on
+            and pages.get_device() == on and state.get_device() == on):
+        _i32(table, "page_table"), _i32(ctx, "context_lens"), _i32(add, "add_lens"), _i32(pages, "pool pages")
+        _i32(state, "pool state")
+        if tuple(ctx.shape) != (B,) or tuple(add.shape) != (B,) or tuple(state.shape) != (2,):
+            raise ValueError(f"context_lens {tuple(ctx.shape)} and add_lens {tuple(add.shape)} must be [{B}], the "
+                             f"pool's state {tuple(state.shape)} [2]")
+        _same_device(table, ctx, add, pages, state)
+    shape = (B, rows) if padded else (rows,)
+    if out is None:
+        if rows < 0:
+            raise ValueError(f"rows={rows} must not be negative")
+        slots, positions = table.new_empty(shape), table.new_empty(shape)
+        lens, new_state = table.new_empty(B), table.new_empty(2)
+    else:
+        slots, positions, lens, new_state = (_i32(t, f"out {name}") for t, name in zip(out, ("slots", "positions", "lens", "state")))
+        if tuple(slots.shape) != shape or tuple(positions.shape) != shape or tuple(lens.shape) != (B,) or tuple(new_state.shape) != (2,):
+            raise ValueError(f"out shapes {tuple(slots.shape)} {tuple(positions.shape)} {tuple(lens.shape)} "
+                             f"{tuple(new_state.shape)}, want {shape} {shape} {(B,)} {(2,)}")
+        _same_device(table, slots, positions, lens, new_state)
+    _call("dg_kv_cache_plan", on, table.data_ptr(), ctx.data_ptr(), add.data_ptr(), pages.data_ptr(), state.data_ptr(),
+          slots.data_ptr(), positions.data_ptr(), lens.data_ptr(), new_state.data_ptr(), B, rows, int(padded), most, P,
+          page_size)
+    return slots, positions, lens, new_state
 
 
 def _workspace(given: Optional[torch.Tensor], on: int, need) -> Tuple[torch.Tensor, int, int]:

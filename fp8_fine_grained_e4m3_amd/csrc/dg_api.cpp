@@ -734,6 +734,57 @@ dg_status dg_fp8_kv_cache_read(const uint8_t* k_codes, const float* k_sf, const 
     return kv_cache_copy(p, dtype, false, stream);
 }
 
+dg_status dg_kv_cache_plan(int32_t* page_table, const int32_t* context_lens, const int32_t* add_lens,
+                           int32_t* pool_pages, const int32_t* pool_state, int32_t* slots,
+                           int32_t* positions, int32_t* new_lens, int32_t* new_state, int64_t B,
+                           int64_t rows, int padded, int64_t max_pages, int64_t num_pages,
+                           int64_t page_size, void* stream) {
+    REQUIRE(B >= 0 && rows >= 0, "negative size (B=%lld rows=%lld)", (long long)B, (long long)rows);
+    REQUIRE(padded == 0 || padded == 1, "padded must be 0 or 1");
+    REQUIRE(cache_page_ok(page_size), "page_size=%lld must be a power of two from 16 to 4096", (long long)page_size);
+    REQUIRE(num_pages >= 1 && num_pages <= INT_MAX / page_size,
+            "num_pages=%lld: num_pages * page_size must be from page_size to 2^31", (long long)num_pages);
+    REQUIRE(max_pages >= 1 && max_pages <= (1LL << 30) / page_size,
+            "max_pages=%lld: max_pages * page_size must be from page_size to 2^30", (long long)max_pages);
+    REQUIRE(B <= 65536, "B=%lld must be at most 65536", (long long)B);
+    REQUIRE(rows <= INT_MAX && (!padded || B == 0 || rows <= INT_MAX / B), "rows=%lld: too many rows", (long long)rows);
+    const int64_t all = padded ? B * rows : rows;
+    if (B > 0) {
+        REQUIRE_PTR(page_table, 4);
+        REQUIRE_PTR(context_lens, 4);
+        REQUIRE_PTR(add_lens, 4);
+        REQUIRE_PTR(new_lens, 4);
+    }
+    REQUIRE_PTR(pool_pages, 4);
+    REQUIRE_PTR(pool_state, 4);
+    REQUIRE_PTR(new_state, 4);
+    if (all > 0) {
+        REQUIRE_PTR(slots, 4);
+        REQUIRE_PTR(positions, 4);
+    }
+    const struct { const void* p; int64_t n; bool written; } buffers[] = {
+        {page_table, B * max_pages, true}, {pool_pages, num_pages, true}, {slots, all, true}, {positions, all, true},
+        {new_lens, B, true}, {new_state, 2, true}, {context_lens, B, false}, {add_lens, B, false}, {pool_state, 2, false}};
+    for (size_t i = 0; i < sizeof buffers / sizeof buffers[0]; ++i)
+        for (size_t j = 0; j < i; ++j)
+            REQUIRE(buffers[i].n == 0 || buffers[j].n == 0 || !buffers[j].written ||
+                        disjoint(buffers[i].p, buffers[i].n * 4, buffers[j].p, buffers[j].n * 4),
+                    "what the call writes overlaps something else");
+    dg::KvPlan p{};
+    p.page_table = page_table; p.context_lens = context_lens; p.add_lens = add_lens;
+    p.pool_pages = pool_pages; p.pool_state = pool_state;
+    p.slots = slots; p.positions = positions; p.new_lens = new_lens; p.new_state = new_state;
+    p.B = B; p.rows = rows; p.padded = padded != 0;
+    p.max_pages = max_pages; p.num_pages = num_pages; p.page_size = page_size;
+    int dev = 0;
+    DeviceInfo info;
+    dg_status st = current_device(dev, info);
+    if (st != DG_OK) return st;
+    hipError_t e = dg::launch_kv_cache_plan(p, reinterpret_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(DG_ERR_HIP, "kernel launch: %s", hipGetErrorString(e));
+    return ok();
+}
+
 // What the sizes of a tree attention call have to be; "" where they are right.
 static const char* tree_attn_sizes_wrong(int64_t B, int64_t N, int64_t Hq, int64_t H, int64_t D,
                                          int64_t page_size, int64_t max_pages) {

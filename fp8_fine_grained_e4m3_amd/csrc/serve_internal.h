@@ -1,6 +1,6 @@
 // Internal interface between the C-ABI layer (dg_api.cpp) and the kernels of
-// the few-token operators: the FP8 key/value cache, tree attention over it and
-// the few-token mixture-of-experts layer.
+// the few-token operators: the FP8 key/value cache, tree attention over it, the
+// few-token mixture-of-experts layer, and the plan of a cache's pages and slots.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -31,6 +31,22 @@ struct KvCopy {
 };
 hipError_t launch_kv_cache_write(const KvCopy& p, hipStream_t stream);
 hipError_t launch_kv_cache_read(const KvCopy& p, hipStream_t stream);
+
+// Pages and slots from request lengths (dg_kv_cache_plan).
+struct KvPlan {
+    int32_t* page_table;           // [B, max_pages]
+    const int32_t* context_lens;   // [B]
+    const int32_t* add_lens;       // [B]
+    int32_t* pool_pages;           // [num_pages], a ring
+    const int32_t* pool_state;     // [2]: first free page's place, free pages
+    int32_t* slots;                // [rows], or [B, rows] where padded
+    int32_t* positions;
+    int32_t* new_lens;             // [B]
+    int32_t* new_state;            // [2]
+    int64_t B, rows, max_pages, num_pages, page_size;
+    bool padded;
+};
+hipError_t launch_kv_cache_plan(const KvPlan& p, hipStream_t stream);
 
 struct TreeAttnProblem {
     KvCache cache;

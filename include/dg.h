@@ -482,6 +482,45 @@ dg_status dg_fp8_kv_cache_read(const uint8_t* k_codes, const float* k_sf,
                                int64_t page_size, void* stream);
 
 /*
+ * Gives the requests of a batch their pages and their new tokens their slots, on
+ * the device, from the requests' lengths.  Free pages are a ring: pool_pages
+ * [num_pages], of which pool_state[1] = n pages from place pool_state[0] = head on
+ * (modulo num_pages) are free.  Request b holds the first ceil(c / page_size) pages
+ * of its row of the table for its c = context_lens[b] tokens; its length becomes
+ * max(c + add_lens[b], 0).
+ *   - A request that grows gets the pages that it lacks from the ring, first ones
+ *     first, requests in order; they are written behind its pages in the table.
+ *     Once the pages do not suffice for a request, it and all later ones that lack
+ *     a page are not served.  Nor is one whose length would pass max_pages *
+ *     page_size, or (padded) whose new tokens pass `rows`; these take no page.  A
+ *     request that is not served keeps its length, and its tokens have no slots.
+ *   - A request that shrinks (drafts that were not accepted; -c when it is done)
+ *     gives the pages behind its new end back, to the ring's end, requests in
+ *     order; they can be taken by later calls.  Its table row stays as it is.
+ *   page_table    [B, max_pages] int32, changed in place
+ *   context_lens  [B]            clamped to [0, max_pages * page_size]
+ *   add_lens      [B]            new tokens, or (negative) dropped ones
+ *   pool_pages    [num_pages]    changed in place
+ *   pool_state    [2]            head taken modulo num_pages, n clamped to [0, num_pages]
+ *   slots, positions  padded == 1: [B, rows], token i of request b in row i;
+ *                 padded == 0: [rows], the requests' tokens end to end (those past
+ *                 rows are left out).  A token's position is c + i.  Its slot is -1
+ *                 where its request is not served or the page not in [0, num_pages).
+ *                 Rows without a token have the slot -1 and the position 0.
+ *   new_lens      [B]            the lengths afterwards
+ *   new_state     [2]            the ring's state afterwards
+ * context_lens and pool_state are not changed (attention of the same step needs the
+ * former).  What is written must not overlap anything else.
+ * Rules: B <= 65536, page_size and num_pages as for the cache, max_pages *
+ * page_size <= 2^30, fewer than 2^31 rows in all.  One kernel launch, no workspace.
+ */
+dg_status dg_kv_cache_plan(int32_t* page_table, const int32_t* context_lens, const int32_t* add_lens,
+                           int32_t* pool_pages, const int32_t* pool_state, int32_t* slots,
+                           int32_t* positions, int32_t* new_lens, int32_t* new_state, int64_t B,
+                           int64_t rows, int padded, int64_t max_pages, int64_t num_pages,
+                           int64_t page_size, void* stream);
+
+/*
  * Attention of the drafted tokens of B requests over the cache.  Request b has
  * c = context_lens[b] tokens in the cache and a tree of n = tree_lens[b] <= N
  * drafted tokens, whose keys and values are in the cache too, tree token j at
