@@ -69,6 +69,9 @@ EXPORTED = (
     "dg_fp8_moe_few_tokens",
     "dg_fp8_moe_few_tokens_workspace_bytes",
     "dg_kv_cache_plan",
+    "dg_qk_norm_rope",
+    "dg_qk_norm_rope_backward",
+    "dg_qk_norm_rope_backward_workspace_bytes",
 )
 DG_CAST_POW2_SCALE = 1
 
@@ -136,6 +139,13 @@ def load_library(path: Optional[str] = None):
                  "dg_m_grouped_fp8_gemm_nt_masked_ue8m0", "dg_pack_ue8m0_scales"):
         getattr(lib, name).restype = I
     F = ctypes.c_float
+    lib.dg_qk_norm_rope.argtypes = [P, P, I, I64, I64, P, P, I, P, P, P, P, I64, I64, F, I, I64, I64, I64, I64, I64, P]
+    lib.dg_qk_norm_rope.restype = I
+    lib.dg_qk_norm_rope_backward.argtypes = ([P, P, P, P, I, I64, I64, I64, I64, P, P, I, P, P, P, P, I64, I64, P, P, F, I]
+                                             + [I64] * 5 + [P, I64, P])
+    lib.dg_qk_norm_rope_backward.restype = I
+    lib.dg_qk_norm_rope_backward_workspace_bytes.argtypes = [I64] * 4
+    lib.dg_qk_norm_rope_backward_workspace_bytes.restype = I64
     lib.dg_kv_cache_plan.argtypes = [P] * 9 + [I64, I64, I, I64, I64, I64, P]
     lib.dg_kv_cache_plan.restype = I
     lib.dg_fp8_kv_cache_write.argtypes = [P, P, I, I64, I64, P, P, P, P, P, I64, I64, I64, I64, I64, P]
@@ -790,6 +800,115 @@ def _workspace(given: Optional[torch.Tensor], on: int, need) -> Tuple[torch.Tens
             raise TypeError("workspace must be uint8")
         raise ValueError(f"workspace must be contiguous and on device {on}, is on {_dev(given, 'workspace').device}")
     return given, given.data_ptr(), given.numel()
+
+
+def _check_rows(given, like, weights, positions, inv_freq, on):
+    """What is wrong with the arguments of a norm and rotation: rows of both tensors,
+    weights, positions and frequencies."""
+    (q, k), dtype = like, like[0].dtype
+    if dtype not in _ROW_TYPES or any(t.dtype != dtype for t, _, _ in given):
+        raise TypeError(f"{', '.join(name for _, _, name in given)} must all be bfloat16 or float32, got "
+                        f"{[t.dtype for t, _, _ in given]}")
+    for t, shape, name in given:
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"shape mismatch: {name} {tuple(t.shape)} must be {tuple(shape)}")
+        _rows(t, name)
+    for w, name in zip(weights, ("q_weight", "k_weight")):
+        if w is not None:
+            if w.dtype not in _ROW_TYPES:
+                raise TypeError(f"{name} must be bfloat16 or float32, got {w.dtype}")
+            if tuple(_dev(w, name).shape) != (q.shape[2],):
+                raise ValueError(f"{name} {tuple(w.shape)} must be [{q.shape[2]}]")
+    if weights[0] is not None and weights[1] is not None and weights[0].dtype != weights[1].dtype:
+        raise TypeError(f"q_weight and k_weight must be of one type, got {weights[0].dtype} and {weights[1].dtype}")
+    if tuple(_i32(positions, "positions").shape) != (q.shape[0],):
+        raise ValueError(f"positions {tuple(positions.shape)} must be [{q.shape[0]}]")
+    if _f32(inv_freq, "inv_freq").dim() != 1:
+        raise ValueError(f"inv_freq {tuple(inv_freq.shape)} must be [R / 2]")
+    _same_device(q, k, *(t for t, _, _ in given), *weights, positions, inv_freq)
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tensor], k_weight: Optional[torch.Tensor],
+                 positions: torch.Tensor, inv_freq: torch.Tensor, eps: float = 1e-6, interleaved: bool = False,
+                 out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None):
+    """RMS norms of each head of q [T, Hq, D] and k [T, H, D] (bf16 or fp32; tokens may
+    be strided, as in slices of a fused projection) with weights [D] (bf16 or fp32;
+    None: ones), then the rotation of the first R = 2 * len(inv_freq) values by
+    positions (int32 [T]) times inv_freq (fp32 [R / 2], R a multiple of 16): values i and
+    i + R / 2 are a pair, or 2 i and 2 i + 1 where interleaved.  Returns (q, k) like
+    those given but dense, or fills out, which may be q and k themselves."""
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} must be [T, heads, D]")
+    (T, Hq, D), H, on = q.shape, k.shape[1], q.get_device()
+    given = [(q, (T, Hq, D), "q"), (k, (T, H, D), "k")]
+    if out is not None:
+        given += [(out[0], (T, Hq, D), "out q"), (out[1], (T, H, D), "out k")]
+    wq, wk = q_weight, k_weight
+    w = wq if wq is not None else wk
+    if not (on >= 0 and q.dtype in _ROW_TYPES and positions.dtype is _I32 and positions.shape == (T,)
+            and inv_freq.dtype is _F32 and inv_freq.dim() == 1 and positions.is_contiguous() and inv_freq.is_contiguous()
+            and positions.get_device() == on and inv_freq.get_device() == on
+            and all(t.dtype is q.dtype and t.shape == shape and t.get_device() == on for t, shape, _ in given)
+            and all(x is None or (x.dtype is w.dtype and x.dtype in _ROW_TYPES and x.shape == (D,) and x.is_contiguous()
+                                  and x.get_device() == on) for x in (wq, wk))):
+        _check_rows(given, (q, k), (wq, wk), positions, inv_freq, on)
+    oq, ok = (q.new_empty((T, Hq, D)), k.new_empty((T, H, D))) if out is None else out
+    _call("dg_qk_norm_rope", on, q.data_ptr(), k.data_ptr(), _ROW_TYPES[q.dtype], _rows(q, "q"), _rows(k, "k"),
+          0 if wq is None else wq.data_ptr(), 0 if wk is None else wk.data_ptr(), DG_F32 if w is None else _ROW_TYPES[w.dtype],
+          positions.data_ptr(), inv_freq.data_ptr(), oq.data_ptr(), ok.data_ptr(), _rows(oq, "out q"), _rows(ok, "out k"),
+          eps, int(interleaved), T, Hq, H, D, 2 * inv_freq.shape[0])
+    return oq, ok
+
+
+def get_qk_norm_rope_backward_workspace_bytes(T: int, Hq: int, H: int, D: int) -> int:
+    """Workspace bytes that the gradients of a norm and rotation of these sizes need."""
+    return int(load_library().dg_qk_norm_rope_backward_workspace_bytes(T, Hq, H, D))
+
+
+def make_qk_norm_rope_backward_workspace(q: torch.Tensor, k: torch.Tensor) -> torch.Tensor:
+    """A workspace for qk_norm_rope_backward calls with arguments of these shapes.
+    Stream-ordered calls may share it."""
+    need = get_qk_norm_rope_backward_workspace_bytes(q.shape[0], q.shape[1], k.shape[1], q.shape[2])
+    return torch.empty(need, dtype=torch.uint8, device=q.device)
+
+
+def qk_norm_rope_backward(dq: torch.Tensor, dk: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
+                          q_weight: Optional[torch.Tensor], k_weight: Optional[torch.Tensor], positions: torch.Tensor,
+                          inv_freq: torch.Tensor, eps: float = 1e-6, interleaved: bool = False,
+                          out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
+                          workspace: Optional[torch.Tensor] = None):
+    """The gradients of qk_norm_rope from those of its outputs, dq and dk, and its
+    inputs: (dq_in, dk_in, dq_weight, dk_weight), the first two like q and k but dense
+    (or out, other tensors than the arguments), the last two fp32 [D] (None where the
+    weight is).  workspace: a uint8 buffer (make_qk_norm_rope_backward_workspace); when
+    None, one is allocated for the call."""
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} must be [T, heads, D]")
+    (T, Hq, D), H, on = q.shape, k.shape[1], q.get_device()
+    given = [(q, (T, Hq, D), "q"), (k, (T, H, D), "k"), (dq, (T, Hq, D), "dq"), (dk, (T, H, D), "dk")]
+    if out is not None:
+        given += [(out[0], (T, Hq, D), "out q"), (out[1], (T, H, D), "out k")]
+    wq, wk = q_weight, k_weight
+    w = wq if wq is not None else wk
+    if not (on >= 0 and q.dtype in _ROW_TYPES and positions.dtype is _I32 and positions.shape == (T,)
+            and inv_freq.dtype is _F32 and inv_freq.dim() == 1 and positions.is_contiguous() and inv_freq.is_contiguous()
+            and positions.get_device() == on and inv_freq.get_device() == on
+            and all(t.dtype is q.dtype and t.shape == shape and t.get_device() == on for t, shape, _ in given)
+            and all(x is None or (x.dtype is w.dtype and x.dtype in _ROW_TYPES and x.shape == (D,) and x.is_contiguous()
+                                  and x.get_device() == on) for x in (wq, wk))):
+        _check_rows(given, (q, k), (wq, wk), positions, inv_freq, on)
+    oq, ok = (q.new_empty((T, Hq, D)), k.new_empty((T, H, D))) if out is None else out
+    gq, gk = (None if x is None else x.new_empty(D, dtype=_F32) for x in (wq, wk))
+    ws, ws_bytes = 0, 0
+    if w is not None:
+        workspace, ws, ws_bytes = _workspace(workspace, on, lambda: get_qk_norm_rope_backward_workspace_bytes(T, Hq, H, D))
+    _call("dg_qk_norm_rope_backward", on, dq.data_ptr(), dk.data_ptr(), q.data_ptr(), k.data_ptr(), _ROW_TYPES[q.dtype],
+          _rows(dq, "dq"), _rows(dk, "dk"), _rows(q, "q"), _rows(k, "k"), 0 if wq is None else wq.data_ptr(),
+          0 if wk is None else wk.data_ptr(), DG_F32 if w is None else _ROW_TYPES[w.dtype], positions.data_ptr(),
+          inv_freq.data_ptr(), oq.data_ptr(), ok.data_ptr(), _rows(oq, "out q"), _rows(ok, "out k"),
+          0 if gq is None else gq.data_ptr(), 0 if gk is None else gk.data_ptr(), eps, int(interleaved), T, Hq, H, D,
+          2 * inv_freq.shape[0], ws, ws_bytes)
+    return oq, ok, gq, gk
 
 
 def get_fp8_tree_attention_workspace_bytes(B: int, N: int, Hq: int, num_kv_heads: int, head_dim: int,

@@ -13,7 +13,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libdg.so")
 SOURCES = ["dg_api.cpp", "nt_kernel.hip", "tn_kernel.hip", "cast_kernel.hip", "mqa_kernel.hip",
-           "kv_cache_kernel.hip", "tree_attn_kernel.hip", "moe_few_kernel.hip", "plan_kernel.hip"]
+           "kv_cache_kernel.hip", "tree_attn_kernel.hip", "moe_few_kernel.hip", "plan_kernel.hip",
+           "norm_rope_kernel.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -785,6 +785,151 @@ dg_status dg_kv_cache_plan(int32_t* page_table, const int32_t* context_lens, con
     return ok();
 }
 
+// What the sizes of a norm and rotation have to be; "" where they are right.
+static const char* norm_rope_sizes_wrong(int64_t T, int64_t Hq, int64_t H, int64_t D) {
+    if (T < 0 || Hq < 0 || H < 0) return "T, Hq and H must not be negative";
+    if (!cache_dim_ok(D)) return "D must be 64, 128 or 256";
+    if (Hq > 65535 || H > 65535) return "Hq and H must be at most 65535";
+    if (T > INT_MAX || T * Hq > INT_MAX || T * H > INT_MAX) return "T * Hq and T * H must stay below 2^31";
+    return "";
+}
+
+// A buffer: its bytes from first to last, and for strided rows their distance and width.
+struct Rows {
+    const void* p;
+    int64_t n, stride, width;
+};
+
+// Whether two share no byte; rows side by side in the same wider rows do not.
+static bool rows_disjoint(const Rows& a, const Rows& b) {
+    if (a.n == 0 || b.n == 0 || disjoint(a.p, a.n, b.p, b.n)) return true;
+    if (a.stride == 0 || a.stride != b.stride) return false;
+    const int64_t d = reinterpret_cast<intptr_t>(b.p) - reinterpret_cast<intptr_t>(a.p);
+    const int64_t at = (d % a.stride + a.stride) % a.stride;
+    return at >= a.width && at + b.width <= a.stride;
+}
+
+// Both directions: what they share is checked here.
+static dg_status norm_rope(dg::NormRope p, dg_dtype dtype, dg_dtype w_dtype, int interleaved,
+                           int64_t workspace_bytes, void* stream) {
+    const char* wrong = norm_rope_sizes_wrong(p.T, p.Hq, p.H, p.D);
+    REQUIRE(!*wrong, "%s (T=%lld Hq=%lld H=%lld D=%lld)", wrong, (long long)p.T, (long long)p.Hq, (long long)p.H,
+            (long long)p.D);
+    REQUIRE(p.R >= 0 && p.R <= p.D && p.R % 16 == 0, "R=%lld must be a multiple of 16 from 0 to D", (long long)p.R);
+    REQUIRE(dtype == DG_BF16 || dtype == DG_F32, "dtype must be DG_BF16 or DG_F32");
+    REQUIRE(w_dtype == DG_BF16 || w_dtype == DG_F32, "w_dtype must be DG_BF16 or DG_F32");
+    REQUIRE(interleaved == 0 || interleaved == 1, "interleaved must be 0 or 1");
+    REQUIRE(std::isfinite(p.eps) && p.eps >= 0x1p-100f, "eps=%g must be finite and 2^-100 at least", (double)p.eps);
+    const int64_t size = dtype == DG_F32 ? 4 : 2, heads[2] = {p.Hq, p.H};
+    const bool any = p.T > 0 && (p.Hq > 0 || p.H > 0);
+    Rows in[9], out[5];                    // x, dz and w of both, positions, inv_freq; out and dw of both, workspace
+    int ins = 0, outs = 0;
+    for (int i = 0; i < 2; ++i) {
+        const struct { const void* p; int64_t stride; const char* name; bool used, written; } rows[3] = {
+            {p.x[i], p.x_stride[i], i ? "k" : "q", true, false},
+            {p.dz[i], p.dz_stride[i], i ? "dk" : "dq", p.backward, false},
+            {p.out[i], p.out_stride[i], p.backward ? (i ? "dk_in" : "dq_in") : (i ? "k_out" : "q_out"), true, true}};
+        for (const auto& r : rows) {
+            if (!r.used) continue;
+            REQUIRE(r.stride >= heads[i] * p.D && r.stride <= kOffsetLimit && r.stride * size % 16 == 0,
+                    "%s_stride=%lld must be a multiple of 16 bytes, from heads * D = %lld to 2^31", r.name,
+                    (long long)r.stride, (long long)(heads[i] * p.D));
+            if (p.T == 0 || heads[i] == 0) continue;
+            REQUIRE(r.p != nullptr, "%s is NULL", r.name);
+            REQUIRE(aligned(r.p, 16), "%s is not 16-byte aligned", r.name);
+            (r.written ? out[outs++] : in[ins++]) = Rows{r.p, ((p.T - 1) * r.stride + heads[i] * p.D) * size,
+                                                         r.stride * size, heads[i] * p.D * size};
+        }
+        REQUIRE(aligned(p.w[i], 16), "%s is not 16-byte aligned", i ? "k_weight" : "q_weight");
+        REQUIRE(aligned(p.dw[i], 16), "%s is not 16-byte aligned", i ? "dk_weight" : "dq_weight");
+        if (p.w[i]) in[ins++] = Rows{p.w[i], p.D * (w_dtype == DG_F32 ? 4 : 2), 0, 0};
+        if (p.dw[i]) out[outs++] = Rows{p.dw[i], p.D * 4, 0, 0};
+    }
+    if (!any && !p.dw[0] && !p.dw[1]) return ok();
+    if (any && p.R > 0) {
+        const int32_t* positions = p.positions;
+        const float* inv_freq = p.inv_freq;
+        REQUIRE_PTR(positions, 4);
+        REQUIRE_PTR(inv_freq, 4);
+        in[ins++] = Rows{positions, p.T * 4, 0, 0};
+        in[ins++] = Rows{inv_freq, p.R * 2, 0, 0};
+    }
+    if (any && (p.dw[0] || p.dw[1])) {
+        const int64_t need = dg::norm_rope_workspace_bytes(p.T, p.Hq, p.H, p.D);
+        void* workspace = p.workspace;
+        REQUIRE_PTR(workspace, 16);
+        REQUIRE(workspace_bytes >= need, "workspace_bytes=%lld < %lld needed for these sizes",
+                (long long)workspace_bytes, (long long)need);
+        out[outs++] = Rows{workspace, need, 0, 0};
+    }
+    for (int i = 0; i < outs; ++i) {
+        for (int k = 0; k < ins; ++k) {
+            // forward in place: a row is written by the lanes that have read it
+            bool in_place = false;
+            for (int t = 0; t < 2; ++t)
+                in_place |= !p.backward && out[i].p == p.out[t] && in[k].p == p.x[t] && out[i].p == in[k].p &&
+                            out[i].stride == in[k].stride && out[i].width == in[k].width;
+            REQUIRE(in_place || rows_disjoint(out[i], in[k]), "an output or the workspace overlaps an input");
+        }
+        for (int k = 0; k < i; ++k) REQUIRE(rows_disjoint(out[i], out[k]), "the outputs or the workspace overlap");
+    }
+    p.f32 = dtype == DG_F32;
+    p.w_f32 = w_dtype == DG_F32;
+    p.neighbours = interleaved != 0;
+    int dev = 0;
+    DeviceInfo info;
+    dg_status st = current_device(dev, info);
+    if (st != DG_OK) return st;
+    hipError_t e = dg::launch_norm_rope(p, reinterpret_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(DG_ERR_HIP, "kernel launch: %s", hipGetErrorString(e));
+    return ok();
+}
+
+dg_status dg_qk_norm_rope(const void* q, const void* k, dg_dtype dtype, int64_t q_stride, int64_t k_stride,
+                          const void* q_weight, const void* k_weight, dg_dtype w_dtype,
+                          const int32_t* positions, const float* inv_freq, void* q_out, void* k_out,
+                          int64_t q_out_stride, int64_t k_out_stride, float eps, int interleaved,
+                          int64_t T, int64_t Hq, int64_t H, int64_t D, int64_t R, void* stream) {
+    dg::NormRope p{};
+    p.x[0] = q; p.x[1] = k;
+    p.out[0] = q_out; p.out[1] = k_out;
+    p.x_stride[0] = q_stride; p.x_stride[1] = k_stride;
+    p.out_stride[0] = q_out_stride; p.out_stride[1] = k_out_stride;
+    p.w[0] = q_weight; p.w[1] = k_weight;
+    p.positions = positions; p.inv_freq = inv_freq; p.eps = eps;
+    p.T = T; p.Hq = Hq; p.H = H; p.D = D; p.R = R;
+    return norm_rope(p, dtype, w_dtype, interleaved, 0, stream);
+}
+
+int64_t dg_qk_norm_rope_backward_workspace_bytes(int64_t T, int64_t Hq, int64_t H, int64_t D) {
+    if (*norm_rope_sizes_wrong(T, Hq, H, D)) return 0;
+    return dg::norm_rope_workspace_bytes(T, Hq, H, D);
+}
+
+dg_status dg_qk_norm_rope_backward(const void* dq, const void* dk, const void* q, const void* k, dg_dtype dtype,
+                                   int64_t dq_stride, int64_t dk_stride, int64_t q_stride, int64_t k_stride,
+                                   const void* q_weight, const void* k_weight, dg_dtype w_dtype,
+                                   const int32_t* positions, const float* inv_freq, void* dq_in, void* dk_in,
+                                   int64_t dq_in_stride, int64_t dk_in_stride, float* dq_weight,
+                                   float* dk_weight, float eps, int interleaved, int64_t T, int64_t Hq,
+                                   int64_t H, int64_t D, int64_t R, void* workspace,
+                                   int64_t workspace_bytes, void* stream) {
+    dg::NormRope p{};
+    p.x[0] = q; p.x[1] = k;
+    p.dz[0] = dq; p.dz[1] = dk;
+    p.out[0] = dq_in; p.out[1] = dk_in;
+    p.x_stride[0] = q_stride; p.x_stride[1] = k_stride;
+    p.dz_stride[0] = dq_stride; p.dz_stride[1] = dk_stride;
+    p.out_stride[0] = dq_in_stride; p.out_stride[1] = dk_in_stride;
+    p.w[0] = q_weight; p.w[1] = k_weight;
+    p.dw[0] = dq_weight; p.dw[1] = dk_weight;
+    p.positions = positions; p.inv_freq = inv_freq; p.eps = eps;
+    p.T = T; p.Hq = Hq; p.H = H; p.D = D; p.R = R;
+    p.backward = true;
+    p.workspace = workspace;
+    return norm_rope(p, dtype, w_dtype, interleaved, workspace_bytes, stream);
+}
+
 // What the sizes of a tree attention call have to be; "" where they are right.
 static const char* tree_attn_sizes_wrong(int64_t B, int64_t N, int64_t Hq, int64_t H, int64_t D,
                                          int64_t page_size, int64_t max_pages) {

@@ -18,6 +18,7 @@
 // written codes are not, the attention that follows reads them.  16384 tokens of
 // that shape are written in 23 us, 4.4 TB/s of the 101 MB that pass.
 #include "fp8_values.h"
+#include "row_access.h"
 #include "serve_internal.h"
 
 namespace dg {
@@ -38,36 +39,6 @@ struct CopyArgs {
     int H, page_shift;
 };
 
-__device__ __forceinline__ void load8(const uint16_t* p, float (&x)[8]) {
-    const u32x4_t w = *reinterpret_cast<const u32x4_t*>(p);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-}
-
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-    const f32x4_t a = reinterpret_cast<const f32x4_t*>(p)[0], b = reinterpret_cast<const f32x4_t*>(p)[1];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = a[i], x[4 + i] = b[i];
-}
-
-__device__ __forceinline__ void store8(uint16_t* p, const float (&x)[8]) {
-    u32x4_t w;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = f32x2_to_bf16x2(x[2 * i], x[2 * i + 1]);
-    __builtin_nontemporal_store(w, reinterpret_cast<u32x4_t*>(p));
-}
-
-__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-    f32x4_t a, b;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] = x[i], b[i] = x[4 + i];
-    __builtin_nontemporal_store(a, reinterpret_cast<f32x4_t*>(p));
-    __builtin_nontemporal_store(b, reinterpret_cast<f32x4_t*>(p) + 1);
-}
-
 // x / s, correctly rounded, given y = 1 / s correctly rounded: each correction adds
 // the exact remainder x - q s times y, the first leaves q within a unit in the
 // last place, and from such a q a correction with a correctly rounded reciprocal
@@ -83,13 +54,6 @@ __device__ __forceinline__ float quotient(float x, float s, float y) {
     q = __builtin_fmaf(__builtin_fmaf(-q, s, x), y, q);
     q = __builtin_fmaf(__builtin_fmaf(-q, s, x), y, q);
     return __builtin_copysignf(q, x);         // the corrections lose the sign of a zero
-}
-
-// Row of the pool ([page][head][offset], in rows) of a slot and head.
-__device__ __forceinline__ int64_t pool_row(int slot, int h, int H, int page_shift) {
-    const int64_t page = slot >> page_shift;
-    const int at = slot & ((1 << page_shift) - 1);
-    return ((page * H + h) << page_shift) + at;
 }
 
 template <typename In, int D>

@@ -48,6 +48,24 @@ struct KvPlan {
 };
 hipError_t launch_kv_cache_plan(const KvPlan& p, hipStream_t stream);
 
+// Norms of queries [0] and keys [1] with the rotation, or (backward) their gradients.
+struct NormRope {
+    const void* x[2];              // [T, heads, D], strides in elements between tokens
+    const void* dz[2];             // backward
+    void* out[2];                  // z, or dx
+    int64_t x_stride[2], dz_stride[2], out_stride[2];
+    const void* w[2];              // [D] or NULL
+    float* dw[2];                  // backward, [D] or NULL
+    const int32_t* positions;      // [T]
+    const float* inv_freq;         // [R / 2]
+    float eps;
+    int64_t T, Hq, H, D, R;
+    bool f32, w_f32, neighbours, backward;
+    void* workspace;               // backward with a dw
+};
+int64_t norm_rope_workspace_bytes(int64_t T, int64_t Hq, int64_t H, int64_t D);
+hipError_t launch_norm_rope(const NormRope& p, hipStream_t stream);
+
 struct TreeAttnProblem {
     KvCache cache;
     const uint16_t* q;             // bf16 [B, N, Hq, D], q_stride elements between tokens

@@ -521,6 +521,57 @@ dg_status dg_kv_cache_plan(int32_t* page_table, const int32_t* context_lens, con
                            int64_t page_size, void* stream);
 
 /*
+ * Norms of each query and key head with the rotation by position in the same pass,
+ * as they stand between a projection and the cache.  For a row x of D values (one
+ * token, one head) with its tensor's weights w:
+ *   n = x / sqrt(mean x^2 + eps),  y = n * w,  and of each pair (y1, y2) of the
+ *   first R values, with t = positions[token] * inv_freq[i], i < R / 2,
+ *   z1 = y1 cos t - y2 sin t,  z2 = y2 cos t + y1 sin t;
+ * the pairs are the values i and i + R / 2 (interleaved == 0) or 2 i and 2 i + 1
+ * (interleaved == 1); values from R on are y.  Sums and products are fp32, the angle
+ * is taken in 64 bits from the int32 position and the fp32 frequency, z is rounded
+ * once.
+ *   q, k          [T, Hq, D], [T, H, D]  DG_BF16 or DG_F32, strides in elements from
+ *                 token to token (a slice of a fused projection will do), 16-byte
+ *                 multiples; heads and D dense
+ *   q_weight, k_weight  [D] of w_dtype, or NULL: ones
+ *   positions     [T]      int32
+ *   inv_freq      [R / 2]  fp32; R a multiple of 16 from 0 (no rotation) to D
+ *   q_out, k_out  like q and k, with strides of their own; in place (the same
+ *                 address and stride) will do
+ * Rules: D is 64, 128 or 256, eps at least 2^-100, T * Hq and T * H below 2^31.
+ * One kernel launch, no workspace.
+ */
+dg_status dg_qk_norm_rope(const void* q, const void* k, dg_dtype dtype, int64_t q_stride, int64_t k_stride,
+                          const void* q_weight, const void* k_weight, dg_dtype w_dtype,
+                          const int32_t* positions, const float* inv_freq, void* q_out, void* k_out,
+                          int64_t q_out_stride, int64_t k_out_stride, float eps, int interleaved,
+                          int64_t T, int64_t Hq, int64_t H, int64_t D, int64_t R, void* stream);
+
+/*
+ * The gradients of dg_qk_norm_rope: from those of its outputs (dq, dk) and its inputs
+ *   dy = dz turned back,  g = dy * w,  dx = (g - n * mean(g n)) / sqrt(mean x^2 + eps)
+ *   dw = the sum of dy * n over all rows of the tensor
+ *   dq, dk, q, k  of dtype, strides as above
+ *   dq_in, dk_in  gradients of q and k, of dtype, rounded once; not in place
+ *   dq_weight, dk_weight  [D] fp32, or NULL: not wanted
+ * Sums over rows are taken in a fixed order: the same inputs give the same bits.
+ * workspace: dg_qk_norm_rope_backward_workspace_bytes of the same sizes where a weight's
+ * gradient is wanted, never initialised, not shared by calls that may overlap.  One
+ * kernel launch, two where a weight's gradient is wanted.
+ */
+dg_status dg_qk_norm_rope_backward(const void* dq, const void* dk, const void* q, const void* k, dg_dtype dtype,
+                                   int64_t dq_stride, int64_t dk_stride, int64_t q_stride, int64_t k_stride,
+                                   const void* q_weight, const void* k_weight, dg_dtype w_dtype,
+                                   const int32_t* positions, const float* inv_freq, void* dq_in, void* dk_in,
+                                   int64_t dq_in_stride, int64_t dk_in_stride, float* dq_weight,
+                                   float* dk_weight, float eps, int interleaved, int64_t T, int64_t Hq,
+                                   int64_t H, int64_t D, int64_t R, void* workspace,
+                                   int64_t workspace_bytes, void* stream);
+/* A function of the sizes alone (no HIP call); 0 for sizes that are rejected. */
+int64_t dg_qk_norm_rope_backward_workspace_bytes(int64_t T, int64_t Hq, int64_t H, int64_t D);
+
+/*
  * Attention of the drafted tokens of B requests over the cache.  Request b has
  * c = context_lens[b] tokens in the cache and a tree of n = tree_lens[b] <= N
  * drafted tokens, whose keys and values are in the cache too, tree token j at

@@ -60,3 +60,64 @@ def random_pool(rng, B, page, ctx, spare):
     ring = np.full(P, -55, np.int32)
     ring[(head + np.arange(spare)) % P] = order[at:]
     return table, ring, np.array([head, spare], np.int32)
+
+
+# ---- norms with rotation -----------------------------------------------------------------------
+
+U = 2.0 ** -24             # half a step of fp32
+HALF_STEP = {"bf16": 2.0 ** -8, "f32": U}
+# Neighbours are never less than 2^-133 (bf16) or 2^-149 (fp32) apart, below 2^-126: half of that
+# for the one rounding to bf16, and in fp32 for each of some ten.
+LEAST = {"bf16": 2.0 ** -134 + 1e-44, "f32": 1e-44}
+
+
+def _turn(x, cos, sin, R, interleaved, back=False):
+    """The first R values of rows turned, and the same of absolute values (for bounds)."""
+    z, size = x.copy(), np.abs(x)
+    a, b = (np.s_[..., 0:R:2], np.s_[..., 1:R:2]) if interleaved else (np.s_[..., :R // 2], np.s_[..., R // 2:R])
+    s = -sin if back else sin
+    z[a], z[b] = x[a] * cos - x[b] * s, x[b] * cos + x[a] * s
+    size[a] = size[b] = np.abs(x[a]) + np.abs(x[b])
+    return z, size
+
+
+def _angles(positions, inv_freq):
+    t = np.asarray(positions, np.float64)[:, None] * np.asarray(inv_freq, np.float32).astype(np.float64)
+    # cosines and sines: two of fp32's last places (2 U each) and the angle's own, 2^-25 of an eighth of a
+    # turn from its rounding to fp32 and 2^-51 of it from the products in 64 bits
+    return np.cos(t)[:, None], np.sin(t)[:, None], 5 * U + 2.0 ** -51 * np.abs(t).max(initial=0.0)
+
+
+def norm_rope(x, w, positions, inv_freq, eps, interleaved, out):
+    """z of rows x [T, H, D] (64-bit) and its bound; out: "bf16" or "f32"."""
+    D, R = x.shape[-1], 2 * len(inv_freq)
+    cos, sin, off = _angles(positions, inv_freq)
+    y = x / np.sqrt((x * x).mean(-1, keepdims=True) + eps) * w
+    z, size = _turn(y, cos, sin, R, interleaved)
+    # r: half the error of a sum of 8 products and 5 exchanges and its mean (16 U), and a Newton step's 2 U;
+    # y: two products more; z: two products and a sum
+    bound = size * ((8 + 2 + 2 + 3) * U + off) * 1.01 + HALF_STEP[out] * np.abs(z) + LEAST[out]
+    return z, bound
+
+
+def norm_rope_backward(dz, x, w, positions, inv_freq, eps, interleaved, out):
+    """dx and dw of rows (64-bit) and their bounds."""
+    D, R = x.shape[-1], 2 * len(inv_freq)
+    cos, sin, off = _angles(positions, inv_freq)
+    r = 1 / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
+    n = x * r
+    dy, size = _turn(dz, cos, sin, R, interleaved, back=True)
+    e_dy, e_n = size * (3 * U + off), 11 * U * np.abs(n)
+    g = dy * w
+    e_g = np.abs(w) * e_dy + U * np.abs(g)
+    m = (g * n).mean(-1, keepdims=True)
+    # 8 products in a chain and 5 exchanges, and the mean
+    e_m = (e_g * np.abs(n) + np.abs(g) * e_n + 15 * U * np.abs(g * n)).mean(-1, keepdims=True)
+    dx = r * (g - n * m)
+    e_dx = r * (e_g + e_n * np.abs(m) + np.abs(n) * e_m + 2 * U * (np.abs(g) + np.abs(n * m))) + 11 * U * np.abs(dx)
+    rows = x.shape[0] * x.shape[1]
+    each = np.abs(dy * n)
+    # a lane's rows one after the other (1 / 16 of a workgroup's, of 1024 workgroups), 32 lanes, 32
+    # workgroups and 32 of those sums: what a term goes through
+    e_dw = (e_dy * np.abs(n) + np.abs(dy) * e_n).sum((0, 1)) + (128 + rows / 4096) * U * each.sum((0, 1))
+    return (dx, 1.01 * e_dx + HALF_STEP[out] * np.abs(dx) + LEAST[out]), ((dy * n).sum((0, 1)), 1.01 * e_dw + 1e-44)

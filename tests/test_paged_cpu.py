@@ -73,3 +73,103 @@ def test_reference_plan():
     assert slots.tolist() == [-1, -1, -1, -1]             # pages 8 and 9 of a cache of five
     assert positions.tolist() == [16, 0, 1, 0] and lens.tolist() == [17, 15, 2]
     assert ring.tolist() == [9, 7, 1, 4, 8] and state.tolist() == [1, 2]
+
+
+# ---- norms with rotation -------------------------------------------------------------------------
+
+def rope(lib, q=A[0], k=A[1], dt=dg.DG_BF16, qs=4096, ks=1024, wq=A[2], wk=A[3], wdt=dg.DG_BF16, positions=A[4], freq=A[5],
+         qo=A[6], ko=A[7], qos=4096, kos=1024, eps=1e-6, pairs=0, T=10, Hq=32, H=8, D=128, R=128):
+    return lib.dg_qk_norm_rope(q, k, dt, qs, ks, wq, wk, wdt, positions, freq, qo, ko, qos, kos, eps, pairs, T, Hq, H, D, R, None)
+
+
+def rope_grad(lib, dq=A[8], dk=A[9], q=A[0], k=A[1], dt=dg.DG_BF16, dqs=4096, dks=1024, qs=4096, ks=1024, wq=A[2], wk=A[3],
+              wdt=dg.DG_BF16, positions=A[4], freq=A[5], qo=A[6], ko=A[7], qos=4096, kos=1024, dwq=A[10], dwk=A[11], eps=1e-6,
+              pairs=0, T=10, Hq=32, H=8, D=128, R=128, ws=A[12], ws_bytes=1 << 22):
+    return lib.dg_qk_norm_rope_backward(dq, dk, q, k, dt, dqs, dks, qs, ks, wq, wk, wdt, positions, freq, qo, ko, qos, kos, dwq, dwk,
+                                        eps, pairs, T, Hq, H, D, R, ws, ws_bytes, None)
+
+
+ROPE_WRONG = [
+    (dict(T=-1), "negative"), (dict(H=-1), "negative"), (dict(D=96), "D must be"), (dict(Hq=1 << 17), "65535"),
+    (dict(T=1 << 28), "2^31"), (dict(T=BIG), "2^31"), (dict(R=24), "R=24"), (dict(R=144), "R=144"), (dict(R=-16), "R=-16"),
+    (dict(dt=0), "dtype"), (dict(wdt=7), "w_dtype"), (dict(pairs=2), "interleaved"), (dict(eps=0.0), "eps"),
+    (dict(eps=float("inf")), "eps"), (dict(qs=4088), "q_stride"), (dict(ks=1028), "k_stride"), (dict(qos=4095), "q"),
+    (dict(kos=1 << 32), "k"), (dict(q=None), "q is NULL"), (dict(k=BAD), "k is not 16-byte"), (dict(wq=BAD), "q_weight is not"),
+    (dict(positions=None), "positions is NULL"), (dict(freq=BAD), "inv_freq is not"), (dict(ko=None), "NULL"), (dict(qo=BAD), "16-byte"),
+    (dict(qo=A[1]), "overlaps an input"), (dict(ko=A[6]), "overlap"), (dict(ko=A[3]), "overlaps an input"),
+]
+
+
+@pytest.mark.parametrize("kw,needle", ROPE_WRONG + [(dict(qo=A[0], qos=4104), "overlaps an input")])
+def test_rope_rejects(lib, kw, needle):
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are made up")
+    assert rope(lib, **kw) == INVALID
+    assert needle in err(lib)
+
+
+@pytest.mark.parametrize("kw,needle", ROPE_WRONG + [
+    (dict(dqs=4088), "dq_stride"), (dict(dk=None), "dk is NULL"), (dict(qo=A[0]), "overlaps an input"), (dict(qo=A[8]), "overlaps an input"),
+    (dict(dwq=BAD), "dq_weight is not"), (dict(dwk=A[2]), "overlaps an input"), (dict(dwk=A[10]), "overlap"), (dict(ws=None), "workspace is NULL"),
+    (dict(ws_bytes=64), "needed"), (dict(ws=A[6]), "overlap"),
+])
+def test_rope_gradients_reject(lib, kw, needle):
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are made up")
+    assert rope_grad(lib, **kw) == INVALID
+    assert needle in err(lib)
+
+
+def test_rope_without_work_or_device(lib):
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are made up")
+    assert rope(lib, T=0, q=None, positions=None) == dg.DG_OK and rope(lib, Hq=0, H=0, q=None, k=None) == dg.DG_OK
+    assert rope(lib) in NO_DEVICE and rope(lib, qo=A[0], ko=A[1]) in NO_DEVICE and rope(lib, wq=None, wk=None, R=0, freq=None) in NO_DEVICE
+    # slices of one row, in place and beside each other
+    q, k = ctypes.c_void_p(0x10000000), ctypes.c_void_p(0x10000000 + 8192)
+    side = dict(q=q, k=k, qs=6144, ks=6144)
+    assert rope(lib, **side, qo=q, ko=k, qos=6144, kos=6144) in NO_DEVICE
+    assert rope(lib, **side, qo=k, ko=q, qos=6144, kos=6144) == INVALID
+    assert rope_grad(lib) in NO_DEVICE and rope_grad(lib, dwq=None, dwk=None, ws=None, ws_bytes=0) in NO_DEVICE
+    assert rope_grad(lib, T=0, dwq=None, dwk=None) == dg.DG_OK and rope_grad(lib, T=0, ws=None) in NO_DEVICE
+    f = lib.dg_qk_norm_rope_backward_workspace_bytes
+    assert f(-1, 32, 8, 128) == 0 and f(10, 32, 8, 96) == 0 and f(0, 32, 8, 128) == 0
+    assert all(0 < f(T, 32, 8, D) <= 1100 * D * 4 for T in (1, 333, 16384, 1 << 25) for D in (64, 128, 256))
+
+
+def test_reference_norm_rope():
+    """A quarter turn swaps a pair; the gradient is orthogonal to the row where eps is nothing."""
+    x = np.zeros((1, 1, 64))
+    x[0, 0, 0], x[0, 0, 16] = 3, 4
+    f = np.zeros(16, np.float32)
+    f[0] = np.float32(np.pi / 2)
+    z, _ = paged.norm_rope(x, 1.0, [1], f, 0.0, False, "f32")
+    np.testing.assert_allclose(z[0, 0, [0, 16]], np.array([-4, 3]) * 8 / 5, atol=1e-6)
+    rng = np.random.default_rng(0)
+    x, dz, w = rng.standard_normal((5, 2, 64)), rng.standard_normal((5, 2, 64)), rng.standard_normal(64)
+    for interleaved in (False, True):
+        (dx, _), (dw, _) = paged.norm_rope_backward(dz, x, w, np.arange(5), f, 1e-30, interleaved, "f32")
+        np.testing.assert_allclose((dx * x).sum(-1), 0, atol=1e-12)
+        a = torch.tensor(x, requires_grad=True)
+        b = torch.tensor(w, requires_grad=True)
+        y = a * torch.rsqrt(a.square().mean(-1, keepdim=True)) * b
+        t = torch.arange(5).double()[:, None] * torch.tensor(f).double()
+        c, s = t.cos()[:, None], t.sin()[:, None]
+        p, q = (y[..., 0:32:2], y[..., 1:32:2]) if interleaved else (y[..., :16], y[..., 16:32])
+        u, v = p * c - q * s, p * s + q * c
+        turned = torch.stack([u, v], -1).flatten(-2) if interleaved else torch.cat([u, v], -1)
+        (torch.cat([turned, y[..., 32:]], -1) * torch.tensor(dz)).sum().backward()
+        np.testing.assert_allclose(dx, a.grad.numpy(), atol=1e-12)
+        np.testing.assert_allclose(dw, b.grad.numpy(), atol=1e-12)
+
+
+# ---- the compiled kernels --------------------------------------------------------------------------
+
+@pytest.mark.skipif(not os.path.exists(HIPCC), reason="hipcc not available")
+@pytest.mark.parametrize("src,least", [("plan_kernel.hip", 2), ("norm_rope_kernel.hip", 49)])
+def test_no_vgpr_spill_no_scratch(src, least):
+    reports = kernel_reports(src)
+    assert len(reports) >= least, sorted(reports)
+    bad = [f"{n}: {r}" for n, r in reports.items() if int(r["VGPRs Spill"]) or int(r["ScratchSize [bytes/lane]"])
+           or r["Dynamic Stack"] != "False"]
+    assert not bad, "\n".join(bad)
