@@ -72,6 +72,10 @@ EXPORTED = (
     "dg_qk_norm_rope",
     "dg_qk_norm_rope_backward",
     "dg_qk_norm_rope_backward_workspace_bytes",
+    "dg_fp4_kv_cache_write",
+    "dg_fp4_kv_cache_read",
+    "dg_fp4_tree_attention",
+    "dg_fp4_tree_attention_workspace_bytes",
 )
 DG_CAST_POW2_SCALE = 1
 
@@ -148,16 +152,17 @@ def load_library(path: Optional[str] = None):
     lib.dg_qk_norm_rope_backward_workspace_bytes.restype = I64
     lib.dg_kv_cache_plan.argtypes = [P] * 9 + [I64, I64, I, I64, I64, I64, P]
     lib.dg_kv_cache_plan.restype = I
-    lib.dg_fp8_kv_cache_write.argtypes = [P, P, I, I64, I64, P, P, P, P, P, I64, I64, I64, I64, I64, P]
-    lib.dg_fp8_kv_cache_read.argtypes = [P, P, P, P, P, P, P, I, I64, I64, I64, I64, I64, P]
-    lib.dg_fp8_tree_attention.argtypes = [P, I64, P, P, P, P, P, P, P, P, P, P, F, I64, I64, I64, I64,
-                                          I64, I64, I64, I64, P, I64, P]
+    for bits in ("fp8", "fp4"):
+        write, read, attention, need = (getattr(lib, f"dg_{bits}_{name}") for name in (
+            "kv_cache_write", "kv_cache_read", "tree_attention", "tree_attention_workspace_bytes"))
+        write.argtypes = [P, P, I, I64, I64, P, P, P, P, P, I64, I64, I64, I64, I64, P]
+        read.argtypes = [P, P, P, P, P, P, P, I, I64, I64, I64, I64, I64, P]
+        attention.argtypes = [P, I64, P, P, P, P, P, P, P, P, P, P, F, I64, I64, I64, I64, I64, I64, I64, I64, P, I64, P]
+        need.argtypes, need.restype = [I64] * 7, I64
+        for f in (write, read, attention):
+            f.restype = I
     lib.dg_fp8_moe_few_tokens.argtypes = [P, P, P, P, P, P, P, P, I, I64, I64, I64, I64, I64, P, I64, P]
-    for name in ("dg_fp8_kv_cache_write", "dg_fp8_kv_cache_read", "dg_fp8_tree_attention",
-                 "dg_fp8_moe_few_tokens"):
-        getattr(lib, name).restype = I
-    lib.dg_fp8_tree_attention_workspace_bytes.argtypes = [I64] * 7
-    lib.dg_fp8_tree_attention_workspace_bytes.restype = I64
+    lib.dg_fp8_moe_few_tokens.restype = I
     lib.dg_fp8_moe_few_tokens_workspace_bytes.argtypes = [I64] * 5
     lib.dg_fp8_moe_few_tokens_workspace_bytes.restype = I64
     if path is None:
@@ -681,14 +686,9 @@ def _call(fn: str, device: int, *args):
         _check(status)
 
 
-def fp8_kv_cache_write(k: torch.Tensor, v: torch.Tensor, cache, slots: torch.Tensor):
-    """Quantises k, v [T, H, D] (bf16 or fp32; tokens may be strided, as in a
-    slice of a fused projection) into the cache's slots (int32 [T], page *
-    page_size + offset; a slot outside the cache stores nothing, one given twice
-    is left with either token's codes and either one's scale).  One fp32 scale
-    per token and head.  Changes and returns the cache
-    (make_fp8_kv_cache)."""
-    kc, ks, vc, vs, (P, H, page, D), on = _cache(cache)
+def _write(fn: str, parts, k: torch.Tensor, v: torch.Tensor, cache, slots: torch.Tensor):
+    """A write into a cache, given its checked parts (_cache, _cache4)."""
+    kc, ks, vc, vs, (P, H, page, D), on = parts
     T = slots.shape[0] if slots.dim() == 1 else -1
     if not (k.dtype in _ROW_TYPES and v.dtype is k.dtype and k.shape == (T, H, D) and v.shape == k.shape
             and slots.dtype is _I32 and slots.is_contiguous()
@@ -701,17 +701,24 @@ def fp8_kv_cache_write(k: torch.Tensor, v: torch.Tensor, cache, slots: torch.Ten
                              f"the cache has {H} heads of {D}")
         _dev(slots, "slots"), _rows(k, "k"), _rows(v, "v")
         _same_device(kc, k, v, slots)
-    _call("dg_fp8_kv_cache_write", on, k.data_ptr(), v.data_ptr(), _ROW_TYPES[k.dtype], _rows(k, "k"), _rows(v, "v"),
+    _call(fn, on, k.data_ptr(), v.data_ptr(), _ROW_TYPES[k.dtype], _rows(k, "k"), _rows(v, "v"),
           slots.data_ptr(), kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), T, H, D, P, page)
     return cache
 
 
-def fp8_kv_cache_read(cache, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
-                      out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None):
-    """The keys and values at slots (int32 [T]) of the cache as (k, v) [T, H, D]
-    of dtype (bfloat16 or float32), or into out; a slot outside the cache gives
-    zeros."""
-    kc, ks, vc, vs, (P, H, page, D), on = _cache(cache)
+def fp8_kv_cache_write(k: torch.Tensor, v: torch.Tensor, cache, slots: torch.Tensor):
+    """Quantises k, v [T, H, D] (bf16 or fp32; tokens may be strided, as in a
+    slice of a fused projection) into the cache's slots (int32 [T], page *
+    page_size + offset; a slot outside the cache stores nothing, one given twice
+    is left with either token's codes and either one's scale).  One fp32 scale
+    per token and head.  Changes and returns the cache
+    (make_fp8_kv_cache)."""
+    return _write("dg_fp8_kv_cache_write", _cache(cache), k, v, cache, slots)
+
+
+def _read(fn: str, parts, slots: torch.Tensor, dtype: torch.dtype, out):
+    """A read of a cache, given its checked parts."""
+    kc, ks, vc, vs, (P, H, page, D), on = parts
     if not (slots.dtype is _I32 and slots.dim() == 1 and slots.is_contiguous() and slots.get_device() == on):
         if _i32(slots, "slots").dim() != 1:
             raise ValueError(f"slots must be [T], got {tuple(slots.shape)}")
@@ -729,9 +736,17 @@ def fp8_kv_cache_read(cache, slots: torch.Tensor, dtype: torch.dtype = torch.bfl
         if tuple(k.shape) != (T, H, D) or v.shape != k.shape:
             raise ValueError(f"out shapes {tuple(k.shape)} {tuple(v.shape)}, want {(T, H, D)}")
         _same_device(kc, k, v)
-    _call("dg_fp8_kv_cache_read", on, kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), slots.data_ptr(),
+    _call(fn, on, kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), slots.data_ptr(),
           k.data_ptr(), v.data_ptr(), _ROW_TYPES[k.dtype], T, H, D, P, page)
     return k, v
+
+
+def fp8_kv_cache_read(cache, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
+                      out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None):
+    """The keys and values at slots (int32 [T]) of the cache as (k, v) [T, H, D]
+    of dtype (bfloat16 or float32), or into out; a slot outside the cache gives
+    zeros."""
+    return _read("dg_fp8_kv_cache_read", _cache(cache), slots, dtype, out)
 
 
 def make_kv_page_pool(num_pages: int, device=None):
@@ -927,23 +942,9 @@ def make_fp8_tree_attention_workspace(q: torch.Tensor, cache, page_table: torch.
     return torch.empty(need, dtype=torch.uint8, device=q.device)
 
 
-def fp8_tree_attention(q: torch.Tensor, cache, page_table: torch.Tensor, context_lens: torch.Tensor,
-                       tree_lens: Optional[torch.Tensor] = None, tree_mask: Optional[torch.Tensor] = None,
-                       scale: Optional[float] = None,
-                       out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
-                       workspace: Optional[torch.Tensor] = None):
-    """Attention of drafted tokens q [B, N, Hq, D] (bf16; tokens may be strided)
-    over the FP8 cache.  page_table int32 [B, max_pages]; request b has
-    context_lens[b] tokens in the cache, then its tree_lens[b] (int32 [B], N
-    when None) drafted ones.  tree_mask int64 [B, N, ceil(N/64)]: bit j % 64 of
-    word j / 64 of token i lets it see drafted token j (None: a chain, j <= i);
-    every context token is seen.  scale defaults to D ** -0.5.  Returns (o bf16
-    like q, lse fp32 [B, N, Hq]), or fills out; rows past a tree's end, and rows
-    that see nothing, are 0 and -inf.  workspace: a uint8 buffer
-    (make_fp8_tree_attention_workspace); when None, one is allocated for the
-    call."""
-    kc, ks, vc, vs, (P, H, page, D), on = _cache(cache)
-    table, ctx = page_table, context_lens
+def _tree_attention(fn: str, need, parts, q, table, ctx, tree_lens, tree_mask, scale, out, workspace):
+    """Attention over a cache, given its checked parts; need: workspace bytes of these sizes."""
+    kc, ks, vc, vs, (P, H, page, D), on = parts
     if q.dim() != 4 or q.shape[3] != D:
         raise ValueError(f"q {tuple(q.shape)} must be [B, N, Hq, {D}]")
     B, N, Hq, _ = q.shape
@@ -986,13 +987,107 @@ def fp8_tree_attention(q: torch.Tensor, cache, page_table: torch.Tensor, context
         if o.shape != q.shape or tuple(lse.shape) != (B, N, Hq):
             raise ValueError(f"out shapes {tuple(o.shape)} {tuple(lse.shape)}, want {tuple(q.shape)} and {(B, N, Hq)}")
         _same_device(kc, o, lse)
-    workspace, ws, ws_bytes = _workspace(workspace, on, lambda: get_fp8_tree_attention_workspace_bytes(
-        B, N, Hq, H, D, page, table.shape[1]))
-    _call("dg_fp8_tree_attention", on, q.data_ptr(), stride, kc.data_ptr(), ks.data_ptr(), vc.data_ptr(),
+    workspace, ws, ws_bytes = _workspace(workspace, on, lambda: need(B, N, Hq, H, D, page, table.shape[1]))
+    _call(fn, on, q.data_ptr(), stride, kc.data_ptr(), ks.data_ptr(), vc.data_ptr(),
           vs.data_ptr(), table.data_ptr(), ctx.data_ptr(), 0 if tree_lens is None else tree_lens.data_ptr(),
           0 if tree_mask is None else tree_mask.data_ptr(), o.data_ptr(), lse.data_ptr(),
           D ** -0.5 if scale is None else scale, B, N, Hq, H, D, P, page, table.shape[1], ws, ws_bytes)
     return o, lse
+
+
+def fp8_tree_attention(q: torch.Tensor, cache, page_table: torch.Tensor, context_lens: torch.Tensor,
+                       tree_lens: Optional[torch.Tensor] = None, tree_mask: Optional[torch.Tensor] = None,
+                       scale: Optional[float] = None,
+                       out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
+                       workspace: Optional[torch.Tensor] = None):
+    """Attention of drafted tokens q [B, N, Hq, D] (bf16; tokens may be strided)
+    over the FP8 cache.  page_table int32 [B, max_pages]; request b has
+    context_lens[b] tokens in the cache, then its tree_lens[b] (int32 [B], N
+    when None) drafted ones.  tree_mask int64 [B, N, ceil(N/64)]: bit j % 64 of
+    word j / 64 of token i lets it see drafted token j (None: a chain, j <= i);
+    every context token is seen.  scale defaults to D ** -0.5.  Returns (o bf16
+    like q, lse fp32 [B, N, Hq]), or fills out; rows past a tree's end, and rows
+    that see nothing, are 0 and -inf.  workspace: a uint8 buffer
+    (make_fp8_tree_attention_workspace); when None, one is allocated for the
+    call."""
+    return _tree_attention("dg_fp8_tree_attention", get_fp8_tree_attention_workspace_bytes, _cache(cache), q, page_table,
+                           context_lens, tree_lens, tree_mask, scale, out, workspace)
+
+
+# ---- the cache in 4 bits ---------------------------------------------------------------------
+
+def make_fp4_kv_cache(num_pages: int, num_kv_heads: int, page_size: int, head_dim: int, device=None):
+    """An empty paged FP4 cache: ((k codes, k scales), (v codes, v scales)), codes
+    uint8 [num_pages, num_kv_heads, page_size, head_dim / 2], two e2m1 a byte, scales uint8
+    [num_pages, num_kv_heads, page_size, head_dim / 32], exponents of powers of two, one for
+    32 values.  page_size is a power of two from 16 to 4096, head_dim 64, 128 or 256."""
+    shape = (num_pages, num_kv_heads, page_size)
+    device = torch.cuda.current_device() if device is None else device
+    return tuple((torch.zeros(shape + (head_dim // 2,), dtype=torch.uint8, device=device),
+                  torch.full(shape + (head_dim // 32,), 127, dtype=torch.uint8, device=device)) for _ in range(2))
+
+
+def _cache4(cache):
+    """The FP4 cache's four tensors, checked, its sizes and its device's index."""
+    (kc, ks), (vc, vs) = cache
+    shape, sf_shape, on = kc.shape, ks.shape, kc.get_device()
+    if not (kc.dtype is _U8 and vc.dtype is _U8 and ks.dtype is _U8 and vs.dtype is _U8 and on >= 0
+            and vc.shape == shape and len(shape) == 4 and len(sf_shape) == 4 and shape[:3] == sf_shape[:3]
+            and shape[3] == 16 * sf_shape[3] and vs.shape == sf_shape
+            and kc.is_contiguous() and vc.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()
+            and ks.get_device() == on and vc.get_device() == on and vs.get_device() == on):
+        for t, name in ((kc, "k codes"), (ks, "k scales"), (vc, "v codes"), (vs, "v scales")):
+            if t.dtype != torch.uint8:
+                raise TypeError(f"{name} must be uint8, got {t.dtype}")
+            _dev(t, name)
+        if (kc.dim() != 4 or kc.shape != vc.shape or ks.dim() != 4 or ks.shape[:3] != kc.shape[:3] or vs.shape != ks.shape
+                or kc.shape[3] != 16 * ks.shape[3]):
+            raise ValueError(f"cache shapes: codes {tuple(kc.shape)} {tuple(vc.shape)}, scales {tuple(ks.shape)} "
+                             f"{tuple(vs.shape)}, want [pages, heads, page_size, head_dim / 2] and [..., head_dim / 32]")
+        _same_device(kc, ks, vc, vs)
+    return kc, ks, vc, vs, (shape[0], shape[1], shape[2], 2 * shape[3]), on
+
+
+def fp4_kv_cache_write(k: torch.Tensor, v: torch.Tensor, cache, slots: torch.Tensor):
+    """fp8_kv_cache_write for an FP4 cache (make_fp4_kv_cache): k, v [T, H, D] quantised
+    into slots, e2m1 codes with the least power of two that brings each 32 values to 6 at
+    most.  Changes and returns the cache."""
+    return _write("dg_fp4_kv_cache_write", _cache4(cache), k, v, cache, slots)
+
+
+def fp4_kv_cache_read(cache, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
+                      out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None):
+    """The keys and values at slots (int32 [T]) of an FP4 cache as (k, v) [T, H, D] of
+    dtype (bfloat16 or float32; both hold them exactly), or into out; a slot outside the
+    cache gives zeros."""
+    return _read("dg_fp4_kv_cache_read", _cache4(cache), slots, dtype, out)
+
+
+def get_fp4_tree_attention_workspace_bytes(B: int, N: int, Hq: int, num_kv_heads: int, head_dim: int,
+                                           page_size: int, max_pages: int) -> int:
+    """Workspace bytes a tree attention call over an FP4 cache needs (0: none)."""
+    return int(load_library().dg_fp4_tree_attention_workspace_bytes(B, N, Hq, num_kv_heads, head_dim,
+                                                                    page_size, max_pages))
+
+
+def make_fp4_tree_attention_workspace(q: torch.Tensor, cache, page_table: torch.Tensor) -> torch.Tensor:
+    """A workspace for fp4_tree_attention calls with arguments of these shapes.
+    Stream-ordered calls may share it."""
+    B, N, Hq, D = q.shape
+    _, H, page, _ = cache[0][0].shape
+    need = get_fp4_tree_attention_workspace_bytes(B, N, Hq, H, D, page, page_table.shape[1])
+    return torch.empty(need, dtype=torch.uint8, device=q.device)
+
+
+def fp4_tree_attention(q: torch.Tensor, cache, page_table: torch.Tensor, context_lens: torch.Tensor,
+                       tree_lens: Optional[torch.Tensor] = None, tree_mask: Optional[torch.Tensor] = None,
+                       scale: Optional[float] = None,
+                       out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
+                       workspace: Optional[torch.Tensor] = None):
+    """fp8_tree_attention over an FP4 cache (make_fp4_kv_cache): the same arguments and
+    results.  workspace: make_fp4_tree_attention_workspace."""
+    return _tree_attention("dg_fp4_tree_attention", get_fp4_tree_attention_workspace_bytes, _cache4(cache), q, page_table,
+                           context_lens, tree_lens, tree_mask, scale, out, workspace)
 
 
 def get_fp8_moe_few_tokens_workspace_bytes(T: int, topk: int, E: int, H: int, I: int) -> int:

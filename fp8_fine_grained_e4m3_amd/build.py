@@ -14,7 +14,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libdg.so")
 SOURCES = ["dg_api.cpp", "nt_kernel.hip", "tn_kernel.hip", "cast_kernel.hip", "mqa_kernel.hip",
            "kv_cache_kernel.hip", "tree_attn_kernel.hip", "moe_few_kernel.hip", "plan_kernel.hip",
-           "norm_rope_kernel.hip"]
+           "norm_rope_kernel.hip", "kv4_cache_kernel.hip", "tree_attn4_kernel.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
@@ -37,7 +37,8 @@ FLAGS = [
 # once, so they ask for the MFMA form that writes VGPRs (no accumulator-register
 # reads); the GEMM kernels keep the default.
 _VGPR_MFMA = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
-SEPARATE = {src: _VGPR_MFMA for src in ("mqa_kernel.hip", "tree_attn_kernel.hip", "moe_few_kernel.hip")}
+SEPARATE = {src: _VGPR_MFMA for src in ("mqa_kernel.hip", "tree_attn_kernel.hip", "moe_few_kernel.hip",
+                                      "tree_attn4_kernel.hip")}
 OBJ_DIR = os.path.join(HERE, "_build")
 
 

@@ -633,7 +633,7 @@ static bool cache_dim_ok(int64_t D) { return D == 64 || D == 128 || D == 256; }
 
 static dg_status check_cache(const dg::KvCache& c) {
     const uint8_t *k_codes = c.k_codes, *v_codes = c.v_codes;
-    const float *k_sf = c.k_sf, *v_sf = c.v_sf;
+    const void *k_sf = c.k_sf, *v_sf = c.v_sf;
     REQUIRE_PTR(k_codes, 16);
     REQUIRE_PTR(k_sf, 16);
     REQUIRE_PTR(v_codes, 16);
@@ -654,9 +654,8 @@ static dg_status check_cache_sizes(const dg::KvCache& c) {
 
 // Whether [p, p + n) stays clear of the cache's four arrays.
 static bool clear_of_cache(const dg::KvCache& c, const void* p, int64_t n) {
-    const int64_t rows = c.num_pages * c.H * c.page_size;
-    return disjoint(p, n, c.k_codes, rows * c.D) && disjoint(p, n, c.v_codes, rows * c.D) &&
-           disjoint(p, n, c.k_sf, rows * 4) && disjoint(p, n, c.v_sf, rows * 4);
+    return disjoint(p, n, c.k_codes, c.code_bytes()) && disjoint(p, n, c.v_codes, c.code_bytes()) &&
+           disjoint(p, n, c.k_sf, c.sf_bytes()) && disjoint(p, n, c.v_sf, c.sf_bytes());
 }
 
 static dg_status kv_cache_copy(dg::KvCopy p, dg_dtype dtype, bool write, void* stream) {
@@ -687,10 +686,10 @@ static dg_status kv_cache_copy(dg::KvCopy p, dg_dtype dtype, bool write, void* s
             "k, v or slots overlap the cache");
     if (write) {
         const dg::KvCache& c = p.cache;
-        const int64_t rows = c.num_pages * H * c.page_size;
-        REQUIRE(disjoint(c.k_codes, rows * D, c.v_codes, rows * D) && disjoint(c.k_sf, rows * 4, c.v_sf, rows * 4) &&
-                    disjoint(c.k_codes, rows * D, c.k_sf, rows * 4) && disjoint(c.k_codes, rows * D, c.v_sf, rows * 4) &&
-                    disjoint(c.v_codes, rows * D, c.k_sf, rows * 4) && disjoint(c.v_codes, rows * D, c.v_sf, rows * 4),
+        const int64_t codes = c.code_bytes(), sf = c.sf_bytes();
+        REQUIRE(disjoint(c.k_codes, codes, c.v_codes, codes) && disjoint(c.k_sf, sf, c.v_sf, sf) &&
+                    disjoint(c.k_codes, codes, c.k_sf, sf) && disjoint(c.k_codes, codes, c.v_sf, sf) &&
+                    disjoint(c.v_codes, codes, c.k_sf, sf) && disjoint(c.v_codes, codes, c.v_sf, sf),
                 "the cache's arrays overlap");
     } else {
         REQUIRE(disjoint(k, kn, v, vn) && disjoint(k, kn, slots, 4 * p.T) && disjoint(v, vn, slots, 4 * p.T),
@@ -702,7 +701,8 @@ static dg_status kv_cache_copy(dg::KvCopy p, dg_dtype dtype, bool write, void* s
     st = current_device(dev, info);
     if (st != DG_OK) return st;
     hipStream_t on = reinterpret_cast<hipStream_t>(stream);
-    hipError_t e = write ? dg::launch_kv_cache_write(p, on) : dg::launch_kv_cache_read(p, on);
+    hipError_t e = p.cache.fp4 ? (write ? dg::launch_kv4_cache_write(p, on) : dg::launch_kv4_cache_read(p, on))
+                               : (write ? dg::launch_kv_cache_write(p, on) : dg::launch_kv_cache_read(p, on));
     if (e != hipSuccess) return fail(DG_ERR_HIP, "kernel launch: %s", hipGetErrorString(e));
     return ok();
 }
@@ -712,7 +712,7 @@ dg_status dg_fp8_kv_cache_write(const void* k, const void* v, dg_dtype dtype, in
                                 float* k_sf, uint8_t* v_codes, float* v_sf, int64_t T, int64_t H,
                                 int64_t D, int64_t num_pages, int64_t page_size, void* stream) {
     dg::KvCopy p{};
-    p.cache = dg::KvCache{k_codes, k_sf, v_codes, v_sf, num_pages, H, page_size, D};
+    p.cache = dg::KvCache{k_codes, k_sf, v_codes, v_sf, num_pages, H, page_size, D, false};
     p.slots = slots;
     p.k = const_cast<void*>(k); p.v = const_cast<void*>(v);
     p.k_stride = k_stride; p.v_stride = v_stride; p.T = T;
@@ -726,7 +726,34 @@ dg_status dg_fp8_kv_cache_read(const uint8_t* k_codes, const float* k_sf, const 
     dg::KvCopy p{};
     p.cache = dg::KvCache{const_cast<uint8_t*>(k_codes), const_cast<float*>(k_sf),
                           const_cast<uint8_t*>(v_codes), const_cast<float*>(v_sf),
-                          num_pages, H, page_size, D};
+                          num_pages, H, page_size, D, false};
+    p.slots = slots;
+    p.k = k; p.v = v;
+    p.k_stride = p.v_stride = H > 0 && H <= 65535 && cache_dim_ok(D) ? H * D : 0;
+    p.T = T;
+    return kv_cache_copy(p, dtype, false, stream);
+}
+
+dg_status dg_fp4_kv_cache_write(const void* k, const void* v, dg_dtype dtype, int64_t k_stride,
+                                int64_t v_stride, const int32_t* slots, uint8_t* k_codes,
+                                uint8_t* k_sf, uint8_t* v_codes, uint8_t* v_sf, int64_t T, int64_t H,
+                                int64_t D, int64_t num_pages, int64_t page_size, void* stream) {
+    dg::KvCopy p{};
+    p.cache = dg::KvCache{k_codes, k_sf, v_codes, v_sf, num_pages, H, page_size, D, true};
+    p.slots = slots;
+    p.k = const_cast<void*>(k); p.v = const_cast<void*>(v);
+    p.k_stride = k_stride; p.v_stride = v_stride; p.T = T;
+    return kv_cache_copy(p, dtype, true, stream);
+}
+
+dg_status dg_fp4_kv_cache_read(const uint8_t* k_codes, const uint8_t* k_sf, const uint8_t* v_codes,
+                               const uint8_t* v_sf, const int32_t* slots, void* k, void* v,
+                               dg_dtype dtype, int64_t T, int64_t H, int64_t D, int64_t num_pages,
+                               int64_t page_size, void* stream) {
+    dg::KvCopy p{};
+    p.cache = dg::KvCache{const_cast<uint8_t*>(k_codes), const_cast<uint8_t*>(k_sf),
+                          const_cast<uint8_t*>(v_codes), const_cast<uint8_t*>(v_sf),
+                          num_pages, H, page_size, D, true};
     p.slots = slots;
     p.k = k; p.v = v;
     p.k_stride = p.v_stride = H > 0 && H <= 65535 && cache_dim_ok(D) ? H * D : 0;
@@ -949,8 +976,8 @@ int64_t dg_fp8_tree_attention_workspace_bytes(int64_t B, int64_t N, int64_t Hq, 
     return dg::tree_attn_workspace_bytes(B, N, Hq, H, D, max_pages, page_size);
 }
 
-dg_status dg_fp8_tree_attention(const void* q, int64_t q_stride, const uint8_t* k_codes,
-                                const float* k_sf, const uint8_t* v_codes, const float* v_sf,
+static dg_status tree_attention(bool fp4, const void* q, int64_t q_stride, const uint8_t* k_codes,
+                                const void* k_sf, const uint8_t* v_codes, const void* v_sf,
                                 const int32_t* page_table, const int32_t* context_lens,
                                 const int32_t* tree_lens, const uint64_t* tree_mask, void* o,
                                 float* lse, float scale, int64_t B, int64_t N, int64_t Hq,
@@ -969,9 +996,9 @@ dg_status dg_fp8_tree_attention(const void* q, int64_t q_stride, const uint8_t* 
     REQUIRE(std::isfinite(scale), "scale is not finite");
     if (B == 0 || N == 0 || Hq == 0) return ok();
     dg::TreeAttnProblem p{};
-    p.cache = dg::KvCache{const_cast<uint8_t*>(k_codes), const_cast<float*>(k_sf),
-                          const_cast<uint8_t*>(v_codes), const_cast<float*>(v_sf),
-                          num_pages, H, page_size, D};
+    p.cache = dg::KvCache{const_cast<uint8_t*>(k_codes), const_cast<void*>(k_sf),
+                          const_cast<uint8_t*>(v_codes), const_cast<void*>(v_sf),
+                          num_pages, H, page_size, D, fp4};
     REQUIRE_PTR(q, 16);
     dg_status st = check_cache(p.cache);
     if (st != DG_OK) return st;
@@ -981,7 +1008,8 @@ dg_status dg_fp8_tree_attention(const void* q, int64_t q_stride, const uint8_t* 
     if (tree_mask) REQUIRE_PTR(tree_mask, 8);
     REQUIRE_PTR(o, 16);
     REQUIRE_PTR(lse, 4);
-    const int64_t need = dg::tree_attn_workspace_bytes(B, N, Hq, H, D, max_pages, page_size);
+    const int64_t need = fp4 ? dg::tree_attn4_workspace_bytes(B, N, Hq, H, D, max_pages, page_size)
+                             : dg::tree_attn_workspace_bytes(B, N, Hq, H, D, max_pages, page_size);
     REQUIRE(workspace_bytes >= need, "workspace_bytes=%lld < %lld needed for these sizes",
             (long long)workspace_bytes, (long long)need);
     if (need > 0) REQUIRE_PTR(workspace, 16);
@@ -1009,9 +1037,42 @@ dg_status dg_fp8_tree_attention(const void* q, int64_t q_stride, const uint8_t* 
     DeviceInfo info;
     st = current_device(dev, info);
     if (st != DG_OK) return st;
-    hipError_t e = dg::launch_tree_attn(p, reinterpret_cast<hipStream_t>(stream));
+    hipStream_t on_stream = reinterpret_cast<hipStream_t>(stream);
+    hipError_t e = fp4 ? dg::launch_tree_attn4(p, on_stream) : dg::launch_tree_attn(p, on_stream);
     if (e != hipSuccess) return fail(DG_ERR_HIP, "kernel launch: %s", hipGetErrorString(e));
     return ok();
+}
+
+dg_status dg_fp8_tree_attention(const void* q, int64_t q_stride, const uint8_t* k_codes,
+                                const float* k_sf, const uint8_t* v_codes, const float* v_sf,
+                                const int32_t* page_table, const int32_t* context_lens,
+                                const int32_t* tree_lens, const uint64_t* tree_mask, void* o,
+                                float* lse, float scale, int64_t B, int64_t N, int64_t Hq,
+                                int64_t H, int64_t D, int64_t num_pages, int64_t page_size,
+                                int64_t max_pages, void* workspace, int64_t workspace_bytes,
+                                void* stream) {
+    return tree_attention(false, q, q_stride, k_codes, k_sf, v_codes, v_sf, page_table, context_lens, tree_lens,
+                          tree_mask, o, lse, scale, B, N, Hq, H, D, num_pages, page_size, max_pages, workspace,
+                          workspace_bytes, stream);
+}
+
+dg_status dg_fp4_tree_attention(const void* q, int64_t q_stride, const uint8_t* k_codes,
+                                const uint8_t* k_sf, const uint8_t* v_codes, const uint8_t* v_sf,
+                                const int32_t* page_table, const int32_t* context_lens,
+                                const int32_t* tree_lens, const uint64_t* tree_mask, void* o,
+                                float* lse, float scale, int64_t B, int64_t N, int64_t Hq,
+                                int64_t H, int64_t D, int64_t num_pages, int64_t page_size,
+                                int64_t max_pages, void* workspace, int64_t workspace_bytes,
+                                void* stream) {
+    return tree_attention(true, q, q_stride, k_codes, k_sf, v_codes, v_sf, page_table, context_lens, tree_lens,
+                          tree_mask, o, lse, scale, B, N, Hq, H, D, num_pages, page_size, max_pages, workspace,
+                          workspace_bytes, stream);
+}
+
+int64_t dg_fp4_tree_attention_workspace_bytes(int64_t B, int64_t N, int64_t Hq, int64_t H,
+                                              int64_t D, int64_t page_size, int64_t max_pages) {
+    if (B <= 0 || N <= 0 || Hq <= 0 || *tree_attn_sizes_wrong(B, N, Hq, H, D, page_size, max_pages)) return 0;
+    return dg::tree_attn4_workspace_bytes(B, N, Hq, H, D, max_pages, page_size);
 }
 
 static const char* moe_few_sizes_wrong(int64_t T, int64_t topk, int64_t E, int64_t H, int64_t I) {

@@ -160,7 +160,7 @@ hipError_t launch(const KvCopy& p, bool write, hipStream_t stream) {
     a.slots = p.slots;
     a.rows[0] = p.k; a.rows[1] = p.v;
     a.codes[0] = p.cache.k_codes; a.codes[1] = p.cache.v_codes;
-    a.sf[0] = p.cache.k_sf; a.sf[1] = p.cache.v_sf;
+    a.sf[0] = static_cast<float*>(p.cache.k_sf); a.sf[1] = static_cast<float*>(p.cache.v_sf);
     a.stride[0] = p.k_stride; a.stride[1] = p.v_stride;
     a.slot_count = p.cache.num_pages * p.cache.page_size;
     a.H = (int)p.cache.H;

@@ -8,14 +8,19 @@
 
 namespace dg {
 
-// A paged FP8 cache: codes [num_pages, H, page_size, D] e4m3, scales
-// [num_pages, H, page_size] fp32, for the keys and for the values.
+// A paged cache, for the keys and for the values: FP8, codes [num_pages, H, page_size,
+// D] e4m3, scales [num_pages, H, page_size] fp32; or FP4, codes [num_pages, H,
+// page_size, D / 2], two e2m1 a byte, scales [num_pages, H, page_size, D / 32] E8M0.
 struct KvCache {
     uint8_t* k_codes;
-    float* k_sf;
+    void* k_sf;
     uint8_t* v_codes;
-    float* v_sf;
+    void* v_sf;
     int64_t num_pages, H, page_size, D;
+    bool fp4;
+
+    int64_t code_bytes() const { return num_pages * H * page_size * (fp4 ? D / 2 : D); }
+    int64_t sf_bytes() const { return num_pages * H * page_size * (fp4 ? D / 32 : 4); }
 };
 
 // slots [T]: page * page_size + offset of each row; others are skipped (write)
@@ -31,6 +36,8 @@ struct KvCopy {
 };
 hipError_t launch_kv_cache_write(const KvCopy& p, hipStream_t stream);
 hipError_t launch_kv_cache_read(const KvCopy& p, hipStream_t stream);
+hipError_t launch_kv4_cache_write(const KvCopy& p, hipStream_t stream);
+hipError_t launch_kv4_cache_read(const KvCopy& p, hipStream_t stream);
 
 // Pages and slots from request lengths (dg_kv_cache_plan).
 struct KvPlan {
@@ -84,6 +91,10 @@ struct TreeAttnProblem {
 int64_t tree_attn_workspace_bytes(int64_t B, int64_t N, int64_t Hq, int64_t H, int64_t D,
                                   int64_t max_pages, int64_t page_size);
 hipError_t launch_tree_attn(const TreeAttnProblem& p, hipStream_t stream);
+// The same over the FP4 cache.
+int64_t tree_attn4_workspace_bytes(int64_t B, int64_t N, int64_t Hq, int64_t H, int64_t D,
+                                   int64_t max_pages, int64_t page_size);
+hipError_t launch_tree_attn4(const TreeAttnProblem& p, hipStream_t stream);
 
 constexpr int64_t kMoeMaxTokens = 256;
 constexpr int64_t kMoeMaxTopk = 16;

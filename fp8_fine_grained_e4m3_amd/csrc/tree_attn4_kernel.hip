@@ -1,0 +1,628 @@
+// Attention for a tree of drafted tokens, or one token, over the FP4 cache, gfx950.
+//
+// What is seen, o and lse are as over the FP8 cache (tree_attn_kernel.hip):
+//   S_j = scale * (q . k_j),  o = sum_j softmax(S)_j v_j,  lse = ln sum_j exp S_j
+// with k and v in e2m1 codes, a power-of-two scale (E8M0) for 32 values of a row.
+//
+// A value, code times scale, is a number of bf16, and one instruction makes two of
+// them of a byte and a scale: both products run on the matrix unit in bf16, with keys
+// and values exact.
+//  * S^T = K q^T: lane l converts the D / 8 bytes of key l & 15 that it loaded itself,
+//    values of one block of 32 (two for D = 256; half of one for D = 64); the query has
+//    the same order of D in its fragments.
+//  * S^T leaves lane l with keys 4 (l >> 4) + i of both 16-key tiles for row l & 15,
+//    the operand layout of O^T = V^T P^T when the 32 keys are summed in that order: P
+//    never leaves its lane.  V's operand needs 8 keys of one D value in a lane; a lane
+//    loads D / 16 consecutive values of those 8 keys, all of one block, and exchanges
+//    halves of words (v_perm) once they are bf16.  A key's scale of the block is a
+//    rotation of the word of its scales: the conversion looks at the eight bits of the
+//    exponent alone.
+//  * P is split into two bf16 parts, the first 8 bits and the next 8, each multiplied:
+//    16 bits, which the plain product's 8 would make the largest error of all.  bf16 has
+//    fp32's exponents, so no weight or value is out of range, whatever its scale.
+//    Where a row's O passes fp32's largest number all the same (values beyond 2^90), a wave
+//    takes its steps again with that row's weights 2^-kDown as large, which 2^30 weights of
+//    2^kLazy do not outgrow; always so, the exponentials' arguments would lose their last
+//    five bits.
+//  * Maximum, sum and O are fp32; the maximum follows where a score passes it by 2^4.
+// Codes hold neither NaN nor infinity and a hidden key's weight is 0, so what a row
+// does not see reaches it only through a scale that is NaN.  Past the end of a request
+// scales are replaced; where rows of one request see different keys, a NaN of a value
+// is counted by a product of its own for the rows that see it.
+//
+// Work is cut into runs and joined as over the FP8 cache.
+#include "tree_attn_common.h"
+
+#include <type_traits>
+
+namespace dg {
+namespace {
+
+constexpr int kWaves = 4;                 // of a workgroup where requests are split
+constexpr int kBrief = 24, kFew = 64;     // steps of requests that stay whole in a long table
+constexpr float kLazy = 4.0f;             // how far, in powers of two, scores pass m before m follows
+constexpr float kDown = 34.0f;             // powers of two that weights are less where O would overflow
+
+// One step's share of the cache in a lane.
+template <int D>
+struct Keys4 {
+    static constexpr int VW = D == 256 ? 2 : 1, VS = D == 64 ? 2 : 4;
+    uint32_t k[2][D / 32];
+    uint32_t v[2][4][VW];
+    uint32_t ks[2];
+    uint32_t vs[2][VS];
+};
+
+// Where a step's two 16-key tiles lie (rows of the pool), uniform.
+struct Place {
+    int64_t row[2];
+    bool live[2];                         // the tile has keys and a valid page
+};
+
+// The requests and steps of a run.
+struct Span {
+    int b, stride, end;                   // first request, from one to the next, past the last
+    int64_t s0, s1, start, total, runs;   // steps of all requests': the run's, where request b starts, all; runs in use
+    bool none;                            // the run has nothing to do
+};
+
+// Several requests with no more than kBrief steps, or kFew where there are as many of
+// them as runs, stay whole and are dealt to the runs in turn.
+template <int W>
+__device__ __forceinline__ Span span_of(const AttnArgs& a, int run, int row0, int lane) {
+    Span s = {run, 1, a.B, 0, 1ll << 62, 0, 0, 1, false};
+    if (a.whole) {
+        s.end = run + 1;
+    } else {
+        // this run's steps of all requests', and the request that they start in
+        uint32_t upto = 0;                // of the lane's request and those before it of its 64, 2^31 at most
+        bool brief = a.B > 1, few = a.B >= a.runs;
+        for (int base = 0; base < a.B; base += 64) {
+            const int own = steps_of_lane(a, base + lane, row0);
+            brief = brief && !__any(own > kBrief);
+            few = few && !__any(own > kFew);
+            upto = sum_up_to_lane(own);
+            s.total += (uint32_t)__builtin_amdgcn_readlane(upto, 63);
+        }
+        if (brief || few) {
+            s.stride = a.runs;
+        } else {
+            s.runs = max((int64_t)1, min((int64_t)a.runs, s.total / W));
+            if (run >= s.runs) {
+                s.none = true;
+                return s;
+            }
+            s.s0 = s.total * run / s.runs;
+            s.s1 = s.total * (run + 1) / s.runs;
+            s.b = a.B;
+            for (int base = 0; base < a.B; base += 64) {
+                if (a.B > 64) upto = sum_up_to_lane(steps_of_lane(a, base + lane, row0));
+                const uint32_t before = __shfl_up(upto, 1);
+                const int64_t from = s.start + (lane > 0 ? before : 0u);
+                const uint64_t hit = __ballot(base + lane < a.B && (s.start + upto > s.s0 || from >= s.s0));
+                if (hit != 0) {
+                    const int at = __builtin_ctzll(hit);
+                    s.b = base + at;
+                    if (at > 0) s.start += (uint32_t)__builtin_amdgcn_readlane(upto, at - 1);
+                    break;
+                }
+                s.start += (uint32_t)__builtin_amdgcn_readlane(upto, 63);
+            }
+        }
+    }
+
+    return s;
+}
+
+// Two values of byte B of a word of codes as two bf16.
+template <int B>
+__device__ __forceinline__ uint32_t e2m1x2_to_bf16x2(uint32_t w, float scale) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, B));
+}
+
+// Eight values of a word as an MFMA fragment.
+__device__ __forceinline__ bf16x8_t e2m1x8_to_bf16x8(uint32_t w, float scale) {
+    const u32x4_t r = {e2m1x2_to_bf16x2<0>(w, scale), e2m1x2_to_bf16x2<1>(w, scale), e2m1x2_to_bf16x2<2>(w, scale),
+                       e2m1x2_to_bf16x2<3>(w, scale)};
+    return __builtin_bit_cast(bf16x8_t, r);
+}
+
+// RT: row tiles, of each of a workgroup's W waves the same.
+template <int D, int RT, int W>
+__global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) void tree_attn4_kernel(AttnArgs a) {
+    constexpr int DT = D / 16;            // 16-row tiles of O^T
+    constexpr int ROWS = 16 * RT;
+    constexpr int PITCH = D + 4;          // of a row of O in LDS
+    constexpr int PART = ROWS * (D + 2);  // floats of a part
+    typedef Keys4<D> Keys;
+    __shared__ __attribute__((aligned(16))) float sm_o[W][ROWS * PITCH];
+    __shared__ f32x2_t sm_ml[W][ROWS];
+    const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // The row blocks of a run follow one another on one XCD (workgroups go to the
+    // eight in turn), whose cache then has their keys.
+    const int in_xcd = blockIdx.x >> 3, rb = in_xcd % a.row_blocks;
+    const int run_head = (in_xcd / a.row_blocks) * 8 + (blockIdx.x & 7);
+    if (run_head >= a.runs * a.H) return;
+    const int run = run_head / a.H, h = run_head - run * a.H;
+    const int row0 = rb * ROWS;
+    const int all_rows = a.N * a.G, Hq = a.H * a.G;
+
+    const Span span = span_of<W>(a, run, row0, lane);
+    if (span.none) return;
+    int64_t start = span.start;           // of request b
+    for (int b = span.b; b < span.end && (start < span.s1 || (run == span.runs - 1 && start == span.total)); b += span.stride) {
+    const Request rq = request(a, b, row0);
+    const int ctx = rq.ctx, rows = rq.n * a.G;
+    // a token alone that does not see itself is as good as past the end
+    const bool blind = a.N == 1 && a.mask && !(uniform_input(reinterpret_cast<const int32_t*>(a.mask + b)) & 1);
+    const int L = blind ? min(ctx, rq.L) : rq.L;
+    const int lo = (int)max(span.s0 - start, (int64_t)0), hi = (int)min(span.s1 - start, (int64_t)rq.steps);
+    start += rq.steps;
+    auto out_row = [&](int r) { return ((int64_t)b * a.N + r / a.G) * Hq + h * a.G + r % a.G; };
+    const bool whole = lo == 0 && hi == rq.steps;
+    if (lo == 0 && threadIdx.x == 0 && !a.whole && a.runs > 1) {
+        // the last run that starts at or before the request's last step
+        const int64_t last = whole ? run - 1 : (start * span.runs + span.total - 1) / span.total - 1;
+        a.split[((int64_t)b * a.H + h) * a.row_blocks + rb] = make_int2(run, (int)last);
+    }
+    if (rq.steps == 0) {                  // no row of the block sees anything
+        for (int i = threadIdx.x; i < ROWS * D / 8; i += W * 64) {
+            const int r = row0 + i / (D / 8);
+            if (r >= all_rows) break;
+            const int64_t at = out_row(r);
+            *reinterpret_cast<u32x4_t*>(a.o + at * D + i % (D / 8) * 8) = u32x4_t{0, 0, 0, 0};
+            if (i % (D / 8) == 0) a.lse[at] = -__builtin_inff();
+        }
+        continue;
+    }
+
+    // the lane's query row of each row tile, its D values in the keys' order
+    const int qlane = fresh(lane), qr16 = qlane & 15, qg = qlane >> 4;
+    bf16x8_t qf[RT][D / 32];
+    int tok[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        const int r = row0 + 16 * t + qr16;
+        tok[t] = r / a.G;
+        const int hq = h * a.G + r - tok[t] * a.G;
+        const uint16_t* src = a.q + ((int64_t)b * a.N + tok[t]) * a.q_stride + (int64_t)hq * D + qg * (D / 4);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+            u32x4_t w = {0, 0, 0, 0};
+            if (r < rows) w = *reinterpret_cast<const u32x4_t*>(src + c * 8);
+            qf[t][c] = __builtin_bit_cast(bf16x8_t, w);
+        }
+        tok[t] = min(tok[t], a.N - 1);
+    }
+
+    const int32_t* table = a.table + (int64_t)b * a.max_pages;
+    // Lanes 2 n and 2 n + 1 ask for the pages of a step's two tiles: vector loads,
+    // in the order of the others, two steps ahead.
+    auto ask = [&](int step) {
+        return table[min((step * kStep + 16 * (lane & 1)) >> a.page_shift, a.max_pages - 1)];
+    };
+    auto place = [&](int step, int pages) {
+        Place w;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const int j0 = step * kStep + 16 * t, page = __builtin_amdgcn_readlane(pages, t);
+            w.live[t] = j0 < L && page >= 0 && page < a.num_pages;
+            w.row[t] = w.live[t] ? (((int64_t)page * a.H + h) << a.page_shift) + (j0 & ((1 << a.page_shift) - 1)) : 0;
+        }
+        return w;
+    };
+    f32x4_t acc[RT][DT];
+    float m[RT], base[RT], l[RT];         // base: m + down, or 0 while nothing was seen, so that exp2 stays 0
+    float down[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) down[t] = 0.0f;
+    for (int again = 0; again < 2; ++again) {
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        m[t] = -__builtin_inff();
+        base[t] = 0.0f;
+        l[t] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < DT; ++i) acc[t][i] = f32x4_t{0, 0, 0, 0};
+    }
+    const float c2 = a.scale * kLog2e;
+    const bool apart = a.N > 1;           // rows of several tokens: they may see different keys
+    if (lo + wave < hi) {
+    // uniform bases, a lane's place in 32 bits
+    const uint32_t k_off = r16 * (D / 2) + g * (D / 8), ks_off = r16 * (D / 32) + (D == 64 ? g / 2 : g * (D / 128));
+    const uint32_t v_off = 4 * g * (D / 2) + r16 * (D / 32), vs_off = 4 * g * (D / 32) + (D == 256 ? r16 / 8 * 4 : 0);
+    // rotation that brings the block's byte of a word of scales to the exponent's place
+    const uint32_t turn = (8 * (D == 64 ? r16 / 8 : D == 128 ? r16 / 4 : r16 / 2 % 4) - 23) & 31;
+    Keys x;
+    const uint8_t* const k_sf = static_cast<const uint8_t*>(a.ks);
+    const uint8_t* const v_sf = static_cast<const uint8_t*>(a.vs);
+    auto fetch_k = [&](const Place& w, int t) {
+        const uint8_t* from = a.kc + w.row[t] * (D / 2) + k_off;
+        if constexpr (D == 64) {
+            const u32x2_t v = *reinterpret_cast<const u32x2_t*>(from);
+            x.k[t][0] = v.x;
+            x.k[t][1] = v.y;
+        } else {
+#pragma unroll
+            for (int c = 0; c < D / 128; ++c) {
+                const u32x4_t v = reinterpret_cast<const u32x4_t*>(from)[c];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x.k[t][4 * c + i] = v[i];
+            }
+        }
+        const uint8_t* sf = k_sf + w.row[t] * (D / 32) + ks_off;
+        if constexpr (D == 256) x.ks[t] = *reinterpret_cast<const uint16_t*>(sf);
+        else x.ks[t] = *sf;
+    };
+    auto fetch_v = [&](const Place& w) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const uint8_t* from = a.vc + w.row[t] * (D / 2) + v_off;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (D == 64) {
+                    x.v[t][i][0] = *reinterpret_cast<const uint16_t*>(from + i * (D / 2));
+                } else if constexpr (D == 128) {
+                    x.v[t][i][0] = *reinterpret_cast<const uint32_t*>(from + i * (D / 2));
+                } else {
+                    const u32x2_t v = *reinterpret_cast<const u32x2_t*>(from + i * (D / 2));
+                    x.v[t][i][0] = v.x;
+                    x.v[t][i][1] = v.y;
+                }
+            }
+            const uint8_t* sf = v_sf + w.row[t] * (D / 32) + vs_off;
+            if constexpr (D == 64) {
+                const u32x2_t v = *reinterpret_cast<const u32x2_t*>(sf);
+                x.vs[t][0] = v.x;
+                x.vs[t][1] = v.y;
+            } else if constexpr (D == 128) {
+                const u32x4_t v = *reinterpret_cast<const u32x4_t*>(sf);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x.vs[t][i] = v[i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x.vs[t][i] = *reinterpret_cast<const uint32_t*>(sf + i * (D / 32));
+            }
+        }
+    };
+    const int s_last = hi - 1;
+    int pages = ask(min(lo + wave, s_last)), pages_next = ask(min(lo + wave + W, s_last));
+    Place at = place(min(lo + wave, s_last), pages);
+    pages = ask(min(lo + wave + 2 * W, s_last));
+    fetch_k(at, 0);
+    fetch_k(at, 1);
+    __builtin_amdgcn_sched_barrier(0);
+    fetch_v(at);
+    __builtin_amdgcn_sched_barrier(0);
+    // A query row with an infinity becomes one of NaN, which its softmax is: scores that
+    // are all -infinity would look like those of hidden keys.  0 * q sums to 0 or to NaN.
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        f32x4_t zero = {0, 0, 0, 0};
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) zero = mfma_bf16(bf16x8_t(0.0f), qf[t][c], zero);
+        const bool finite = zero.x == 0.0f;
+        if (!__all(finite)) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c)
+                if (!finite) qf[t][c] = bf16x8_t(__builtin_nanf(""));
+        }
+    }
+    for (int s = lo + wave; s < hi; s += W) {
+        const int j0 = s * kStep;
+        const Place next = place(min(s + W, s_last), pages_next);
+        pages_next = pages;
+        pages = ask(min(s + 3 * W, s_last));
+        __builtin_amdgcn_sched_barrier(0);
+        const bool all = j0 + kStep <= ctx && at.live[0] && at.live[1];      // uniform: no mask here
+        float sc[RT][2][4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            bf16x8_t kf[D / 32];
+            const float s0 = __uint_as_float(x.ks[u] << 23), s1 = D == 256 ? __uint_as_float(x.ks[u] << 15) : s0;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) kf[c] = e2m1x8_to_bf16x8(x.k[u][c], c < 4 ? s0 : s1);
+            __builtin_amdgcn_sched_barrier(0);
+            fetch_k(next, u);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+                f32x4_t p = {0, 0, 0, 0};
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) p = mfma_bf16(kf[c], qf[t][c], p);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sc[t][u][i] = p[i] * c2;
+            }
+        }
+        // scales of the lane's block of its 8 keys' values
+        uint32_t vscale[2][4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t w = x.vs[u][D == 64 ? i / 2 : i];
+                vscale[u][i] = __builtin_amdgcn_alignbit(w, w, D == 64 ? turn + 16 * (i & 1) : turn);
+            }
+        if (!all) {
+            const int mlane = fresh(lane), g = mlane >> 4;
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int j = j0 + 16 * u + 4 * g + i;      // position
+                        const int d = j - ctx;                      // number in the tree
+                        bool seen = at.live[u] && j < L;
+                        if (seen && d >= 0 && apart)
+                            seen = a.mask ? (a.mask[((int64_t)b * a.N + tok[t]) * a.mask_words + (d >> 6)] >> (d & 63)) & 1
+                                          : d <= tok[t];
+                        if (!seen) sc[t][u][i] = -__builtin_inff();
+                    }
+            // scales past the end may be NaN: 0 * NaN must not reach O
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (!at.live[u] || j0 + 16 * u + 4 * g + i >= L) vscale[u][i] = 0x3F800000u;
+            if (apart) {
+                bool bad = false;
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) bad |= (vscale[u][i] & 0x7F800000u) == 0x7F800000u;
+                if (__any(bad)) {
+                    // ones where a value is NaN, times ones where a row sees its key: rows that see any
+                    u32x4_t ind;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const bool first = (vscale[u][2 * i] & 0x7F800000u) == 0x7F800000u;
+                            const bool second = (vscale[u][2 * i + 1] & 0x7F800000u) == 0x7F800000u;
+                            ind[2 * u + i] = (first ? 0x3F80u : 0) | (second ? 0x3F800000u : 0);
+                            if (first) vscale[u][2 * i] = 0x3F800000u;
+                            if (second) vscale[u][2 * i + 1] = 0x3F800000u;
+                        }
+#pragma unroll
+                    for (int t = 0; t < RT; ++t) {
+                        u32x4_t see;
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                see[2 * u + i] = (sc[t][u][2 * i] != -__builtin_inff() ? 0x3F80u : 0) |
+                                                 (sc[t][u][2 * i + 1] != -__builtin_inff() ? 0x3F800000u : 0);
+                        const f32x4_t count = mfma_bf16(__builtin_bit_cast(bf16x8_t, ind), __builtin_bit_cast(bf16x8_t, see),
+                                                        f32x4_t{0, 0, 0, 0});
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (count[k] > 0.0f)
+#pragma unroll
+                                for (int i = 0; i < DT; ++i) acc[t][i][k] = __builtin_nanf("");
+                    }
+                }
+            }
+        }
+        // A wave in its softmax goes before one in its products.
+        __builtin_amdgcn_s_setprio(1);
+        // Whether a score outgrows what O is relative to.  The lanes look at their own;
+        // only then is the row's maximum exchanged.
+        float mx[RT];
+        bool over = false;
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            mx[t] = sc[t][0][0];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mx[t] = __builtin_fmaxf(mx[t], sc[t][u][i]);
+            over |= mx[t] > m[t] + kLazy;
+        }
+        if (__any(over)) {
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+                mx[t] = __builtin_fmaxf(max_of_groups(mx[t]), m[t]);
+                const float from = base[t];
+                if (mx[t] != -__builtin_inff()) base[t] = mx[t] + down[t];
+                const float f = m[t] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(from - base[t]);
+                l[t] *= f;
+#pragma unroll
+                for (int i = 0; i < DT; ++i) acc[t][i] *= f;
+                m[t] = mx[t];
+            }
+        }
+        bf16x8_t p_hi[RT], p_lo[RT];
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            u32x4_t top, rest;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float e0 = __builtin_amdgcn_exp2f(sc[t][u][2 * i] - base[t]);
+                    const float e1 = __builtin_amdgcn_exp2f(sc[t][u][2 * i + 1] - base[t]);
+                    l[t] += e0;
+                    l[t] += e1;
+                    const uint32_t b0 = __float_as_uint(e0), b1 = __float_as_uint(e1);
+                    top[2 * u + i] = __builtin_amdgcn_perm(b1, b0, 0x07060302u);
+                    rest[2 * u + i] = f32x2_to_bf16x2(e0 - __uint_as_float(b0 & 0xFFFF0000u), e1 - __uint_as_float(b1 & 0xFFFF0000u));
+                }
+            p_hi[t] = __builtin_bit_cast(bf16x8_t, top);
+            p_lo[t] = __builtin_bit_cast(bf16x8_t, rest);
+        }
+        __builtin_amdgcn_s_setprio(0);
+        // V^T: tile i takes D value r16 * DT + i of the lane's 8 keys
+        auto tiles = [&](auto byte) {
+            constexpr int B = decltype(byte)::value, word = B / 4;
+            u32x4_t even, odd;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t ka = e2m1x2_to_bf16x2<B % 4>(x.v[u][2 * i][word], __uint_as_float(vscale[u][2 * i]));
+                    const uint32_t kb = e2m1x2_to_bf16x2<B % 4>(x.v[u][2 * i + 1][word], __uint_as_float(vscale[u][2 * i + 1]));
+                    even[2 * u + i] = __builtin_amdgcn_perm(kb, ka, 0x05040100u);
+                    odd[2 * u + i] = __builtin_amdgcn_perm(kb, ka, 0x07060302u);
+                }
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+                acc[t][2 * B] = mfma_bf16(__builtin_bit_cast(bf16x8_t, even), p_lo[t], acc[t][2 * B]);
+                acc[t][2 * B + 1] = mfma_bf16(__builtin_bit_cast(bf16x8_t, odd), p_lo[t], acc[t][2 * B + 1]);
+                acc[t][2 * B] = mfma_bf16(__builtin_bit_cast(bf16x8_t, even), p_hi[t], acc[t][2 * B]);
+                acc[t][2 * B + 1] = mfma_bf16(__builtin_bit_cast(bf16x8_t, odd), p_hi[t], acc[t][2 * B + 1]);
+            }
+        };
+        tiles(std::integral_constant<int, 0>());
+        tiles(std::integral_constant<int, 1>());
+        if constexpr (D >= 128) {
+            tiles(std::integral_constant<int, 2>());
+            tiles(std::integral_constant<int, 3>());
+        }
+        if constexpr (D == 256) {
+            tiles(std::integral_constant<int, 4>());
+            tiles(std::integral_constant<int, 5>());
+            tiles(std::integral_constant<int, 6>());
+            tiles(std::integral_constant<int, 7>());
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        fetch_v(next);
+        __builtin_amdgcn_sched_barrier(0);
+        at = next;
+    }
+    }
+    // rows whose O is not finite take their steps again
+    bool off = false;
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        float sum = 0.0f;                 // 0, or NaN
+#pragma unroll
+        for (int i = 0; i < DT; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sum = __builtin_fmaf(acc[t][i][k], 0.0f, sum);
+        down[t] = max_of_groups(sum == 0.0f ? 0.0f : kDown);
+        off |= down[t] > 0.0f;
+    }
+    if (!__any(off)) break;
+    }
+
+    // The waves put down their O and meet: a thread then adds up four values of a
+    // row, wave by wave, relative to the largest of their maxima.
+    const int elane = fresh(lane), er16 = elane & 15, eg = elane >> 4;
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        l[t] = sum_of_groups(l[t]);
+        // the sum's power of two goes to the maximum
+        const int k = __builtin_amdgcn_frexp_expf(l[t]), shift = -k - kSpare;
+        const float top = m[t] == -__builtin_inff() ? m[t] : base[t] + (float)k;
+        if (eg == 0) sm_ml[wave][16 * t + er16] = f32x2_t{top, __builtin_amdgcn_ldexpf(l[t], -k)};
+        float* mine = sm_o[wave] + (16 * t + er16) * PITCH + 4 * eg * DT;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < DT / 4; ++c)
+                *reinterpret_cast<f32x4_t*>(mine + i * DT + 4 * c) =
+                    f32x4_t{__builtin_amdgcn_ldexpf(acc[t][4 * c][i], shift), __builtin_amdgcn_ldexpf(acc[t][4 * c + 1][i], shift),
+                            __builtin_amdgcn_ldexpf(acc[t][4 * c + 2][i], shift),
+                            __builtin_amdgcn_ldexpf(acc[t][4 * c + 3][i], shift)};
+    }
+    __syncthreads();
+    // A run has one part of a request that goes on from the run before (the first
+    // of its two places) and one of a request that begins in it (the second).
+    float* part = a.parts + (((int64_t)run_head * a.row_blocks + rb) * 2 + (lo > 0 ? 0 : 1)) * PART;
+    for (int i = fresh(threadIdx.x); i < ROWS * D / 4; i += W * 64) {
+        const int r = i / (D / 4), d = i % (D / 4) * 4;
+        float top = -__builtin_inff(), sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) top = __builtin_fmaxf(top, sm_ml[w][r].x);
+        f32x4_t v = {0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const f32x2_t ml = sm_ml[w][r];
+            const float f = ml.x == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(ml.x - top);
+            sum += f * ml.y;
+            v += f * *reinterpret_cast<const f32x4_t*>(sm_o[w] + r * PITCH + d);
+        }
+        if (!whole) {
+            *reinterpret_cast<f32x4_t*>(part + r * D + d) = v;
+            if (d == 0) *reinterpret_cast<f32x2_t*>(part + ROWS * D + 2 * r) = f32x2_t{top, sum};
+        } else if (row0 + r < all_rows) {
+            const bool none = row0 + r >= rows || sum == 0.0f;      // a sum of NaN is none of it
+            const float inv = none ? 0.0f : (1 << kSpare) / sum;
+            const int64_t at = out_row(row0 + r);
+            u32x2_t w = {0, 0};
+            if (!none) w = u32x2_t{f32x2_to_bf16x2(v.x * inv, v.y * inv), f32x2_to_bf16x2(v.z * inv, v.w * inv)};
+            *reinterpret_cast<u32x2_t*>(a.o + at * D + d) = w;
+            if (d == 0) a.lse[at] = none ? -__builtin_inff() : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+        }
+    }
+    __syncthreads();                      // before the next request's
+    }
+}
+
+// Row tiles, whole requests and runs by the same rules as over the FP8 cache.
+Shape shape_of(int64_t B, int64_t N, int64_t Hq, int64_t H, int64_t D, int64_t max_pages, int64_t page_size) {
+    const int64_t rows = N * (Hq / H);
+    Shape s;
+    s.row_tiles = rows <= 16 || D == 256 ? 1 : 2;
+    s.row_blocks = (int)((rows + s.rows() - 1) / s.rows());
+    const int64_t groups = H * s.row_blocks, most = (max_pages * page_size + kStep - 1) / kStep, steps = B * most;
+    const int64_t workgroups = B * groups;
+    s.whole = most <= (D == 256 ? 16 : 32) || (most <= (s.row_tiles == 2 ? 128 : 64) && workgroups >= 128) ||
+              (most <= 128 && workgroups >= 256);
+    if (workgroups > (1 << 20)) s.whole = false;       // a grid has fewer than 2^32 threads
+    s.waves = kWaves;
+    if (s.whole) {
+        const int64_t resident = 1024 * (D == 256 ? 1 : D == 128 ? 2 : 3);
+        s.waves = s.row_tiles == 2 ? 8 : 4;
+        while (s.waves > 1 && workgroups * s.waves > resident && 2 * most <= 16 * s.waves) s.waves /= 2;
+    }
+    s.runs = (int)B;
+    if (s.whole) return s;
+    const int64_t wanted = D == 256 ? 256 : 512;
+    s.runs = (int)std::max<int64_t>(1, std::min(wanted / groups, steps / kWaves));
+    return s;
+}
+
+template <int D, int RT>
+void launch_waves(const AttnArgs& a, int waves, dim3 grid, hipStream_t stream) {
+    if (waves == 1) hipLaunchKernelGGL((tree_attn4_kernel<D, RT, 1>), grid, dim3(64), 0, stream, a);
+    else if (waves == 2) hipLaunchKernelGGL((tree_attn4_kernel<D, RT, 2>), grid, dim3(128), 0, stream, a);
+    else if (waves == 4) hipLaunchKernelGGL((tree_attn4_kernel<D, RT, 4>), grid, dim3(256), 0, stream, a);
+    else if constexpr (RT == 2) hipLaunchKernelGGL((tree_attn4_kernel<D, RT, 8>), grid, dim3(512), 0, stream, a);
+}
+
+template <int D>
+hipError_t launch(const AttnArgs& a, const Shape& s, hipStream_t stream) {
+    const int64_t groups = ((int64_t)a.runs * a.H + 7) / 8 * 8;
+    const dim3 grid((unsigned)(groups * a.row_blocks));
+    if (s.row_tiles == 1) {
+        launch_waves<D, 1>(a, s.waves, grid, stream);
+    } else if constexpr (D <= 128) {
+        launch_waves<D, 2>(a, s.waves, grid, stream);
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.whole || a.runs == 1) return e;
+    return launch_join<D>(a, s.rows(), stream);
+}
+
+}  // namespace
+
+int64_t tree_attn4_workspace_bytes(int64_t B, int64_t N, int64_t Hq, int64_t H, int64_t D,
+                                   int64_t max_pages, int64_t page_size) {
+    return shape_workspace_bytes(B, H, D, shape_of(B, N, Hq, H, D, max_pages, page_size));
+}
+
+hipError_t launch_tree_attn4(const TreeAttnProblem& p, hipStream_t stream) {
+    const Shape s = shape_of(p.B, p.N, p.Hq, p.cache.H, p.cache.D, p.max_pages, p.cache.page_size);
+    const AttnArgs a = args_of(p, s);
+    switch (p.cache.D) {
+    case 64: return launch<64>(a, s, stream);
+    case 128: return launch<128>(a, s, stream);
+    case 256: return launch<256>(a, s, stream);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace dg

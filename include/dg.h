@@ -624,6 +624,56 @@ int64_t dg_fp8_tree_attention_workspace_bytes(int64_t B, int64_t N, int64_t Hq, 
                                               int64_t D, int64_t page_size, int64_t max_pages);
 
 /*
+ * The cache in 4 bits: for the keys and for the values
+ *   codes [num_pages, H, page_size, D / 2]   two e2m1 a byte, value 2 i of a row in the
+ *                                            low half of byte i
+ *   sf    [num_pages, H, page_size, D / 32]  E8M0: byte s stands for 2^(s - 127), 255
+ *                                            for NaN; one for 32 values of a row
+ * e2m1 has the values 0, 0.5, 1, 1.5, 2, 3, 4, 6 (codes 0 to 7) and, with bit 3 set,
+ * their negatives.  value = code * sf.  Sizes, slots and pages are those of the FP8 cache,
+ * and so are the rules of the calls below where nothing else is said.
+ *
+ * dg_fp4_kv_cache_write, for each block of 32 values:
+ *   s    = the least 2^e, -125 <= e <= 125, with max |x| <= 6 s; 1 where that is 0
+ *   code = the e2m1 value nearest to x / s, 6 at most, ties to the even mantissa
+ * A block that holds a NaN or an infinity gets the scale NaN and codes 0; the other
+ * blocks of its row are not touched by it.
+ * dg_fp4_kv_cache_read gives code * sf, exact in DG_BF16 and DG_F32 for what a write makes
+ * (a caller's own scales from 2^-126 on to 2^125).
+ */
+dg_status dg_fp4_kv_cache_write(const void* k, const void* v, dg_dtype dtype,
+                                int64_t k_stride, int64_t v_stride, const int32_t* slots,
+                                uint8_t* k_codes, uint8_t* k_sf, uint8_t* v_codes, uint8_t* v_sf,
+                                int64_t T, int64_t H, int64_t D, int64_t num_pages,
+                                int64_t page_size, void* stream);
+dg_status dg_fp4_kv_cache_read(const uint8_t* k_codes, const uint8_t* k_sf,
+                               const uint8_t* v_codes, const uint8_t* v_sf, const int32_t* slots,
+                               void* k, void* v, dg_dtype dtype,
+                               int64_t T, int64_t H, int64_t D, int64_t num_pages,
+                               int64_t page_size, void* stream);
+
+/*
+ * Attention over the FP4 cache: dg_fp8_tree_attention with
+ *   - weights kept to 16 bits, values and keys exact (nothing depends on the largest
+ *     scale); terms below 2^-92 of the values' unit may count as 0;
+ *   - a NaN scale in a key that a token sees makes the token's o and lse NaN; one in a
+ *     value makes the 32 values of o that it belongs to NaN;
+ *   - any codes and scales past a request's last token and in hidden pages.
+ */
+dg_status dg_fp4_tree_attention(const void* q, int64_t q_stride,
+                                const uint8_t* k_codes, const uint8_t* k_sf,
+                                const uint8_t* v_codes, const uint8_t* v_sf,
+                                const int32_t* page_table, const int32_t* context_lens,
+                                const int32_t* tree_lens, const uint64_t* tree_mask,
+                                void* o, float* lse, float scale,
+                                int64_t B, int64_t N, int64_t Hq, int64_t H, int64_t D,
+                                int64_t num_pages, int64_t page_size, int64_t max_pages,
+                                void* workspace, int64_t workspace_bytes, void* stream);
+/* A function of the sizes alone (no HIP call); 0 for sizes that are rejected. */
+int64_t dg_fp4_tree_attention_workspace_bytes(int64_t B, int64_t N, int64_t Hq, int64_t H,
+                                              int64_t D, int64_t page_size, int64_t max_pages);
+
+/*
  * A whole mixture-of-experts layer for a few tokens:
  *   y[t] = sum_j topk_weights[t, j] * W2_e (silu(W1_e[:I] x[t]) * (W1_e[I:] x[t])),
  *   e = topk_ids[t, j]

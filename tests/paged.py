@@ -121,3 +121,101 @@ def norm_rope_backward(dz, x, w, positions, inv_freq, eps, interleaved, out):
     # workgroups and 32 of those sums: what a term goes through
     e_dw = (e_dy * np.abs(n) + np.abs(dy) * e_n).sum((0, 1)) + (128 + rows / 4096) * U * each.sum((0, 1))
     return (dx, 1.01 * e_dx + HALF_STEP[out] * np.abs(dx) + LEAST[out]), ((dy * n).sum((0, 1)), 1.01 * e_dw + 1e-44)
+
+
+# ---- the FP4 cache -------------------------------------------------------------------------------
+
+E2M1 = np.array([0, 0.5, 1, 1.5, 2, 3, 4, 6, -0.0, -0.5, -1, -1.5, -2, -3, -4, -6])
+
+
+def quantise4(x):
+    """[..., D] rows -> (codes [..., D / 2], exponent bytes [..., D / 32]) by the cache's rule, block by
+    block in 64 bits."""
+    x = np.asarray(x, np.float64)
+    b = x.reshape(x.shape[:-1] + (-1, 32))
+    with np.errstate(all="ignore"):
+        bad = ~np.isfinite(b).all(-1)
+        b = np.where(bad[..., None], 0.0, b)
+        most = np.abs(b).max(-1)
+        e = np.full(most.shape, -125)
+        while True:                                    # the least exponent that will do
+            small = (most > 6 * np.ldexp(1.0, e)) & (e < 125)
+            if not small.any():
+                break
+            e += small
+        e = np.where(most == 0, 0, e)
+        y = np.ldexp(b, -e[..., None])
+    middles = (E2M1[1:8] + E2M1[:7]) / 2
+    code = np.zeros(y.shape, np.uint8)
+    for i, middle in enumerate(middles):               # ties to the even code
+        code += (np.abs(y) > middle) if i % 2 == 0 else (np.abs(y) >= middle)
+    code |= np.signbit(y).astype(np.uint8) << 3
+    code[bad] = 0
+    code = code.reshape(x.shape)
+    return code[..., ::2] | code[..., 1::2] << 4, np.where(bad, 255, e + 127).astype(np.uint8)
+
+
+def values4(codes, sf):
+    """[..., D / 2] codes, [..., D / 32] exponents -> [..., D] in 64 bits."""
+    codes = np.asarray(codes)
+    v = np.stack([E2M1[codes & 15], E2M1[codes >> 4]], -1).reshape(np.shape(sf) + (32,))
+    scale = np.where(np.asarray(sf) == 255, np.nan, np.ldexp(1.0, np.asarray(sf).astype(np.int64) - 127))
+    return (v * scale[..., None]).reshape(codes.shape[:-1] + (2 * codes.shape[-1],))
+
+
+def random_cache4(rng, pages, H, page, D):
+    """Random codes, scales of several sizes (a fifth of the cache's blocks far smaller)."""
+    out = []
+    for _ in range(2):
+        codes = rng.integers(0, 256, (pages, H, page, D // 2)).astype(np.uint8)
+        sf = (127 - 2 + rng.integers(-4, 3, (pages, H, page, D // 32))).astype(np.uint8)
+        sf[rng.random(sf.shape) < 0.2] -= 20
+        out.append((codes, sf))
+    return out
+
+
+def attention4(q, cache, table, ctx, lens, mask, scale, page):
+    """q [B, N, Hq, D] float; mask [B, N, N] bool.  Returns o, lse and the bounds of both; NaN where a
+    scale that is NaN reaches."""
+    (kc, ks), (vc, vs) = cache
+    P, H = kc.shape[:2]
+    B, N, Hq, D = q.shape
+    G, most, eps = Hq // H, table.shape[1] * page, 2.0 ** -23
+    o, bo = np.zeros((B, N, Hq, D)), np.zeros((B, N, Hq, D))
+    lse, bl = np.full((B, N, Hq), -np.inf), np.zeros((B, N, Hq))
+    for b in range(B):
+        c, n = min(max(int(ctx[b]), 0), most), min(max(int(lens[b]), 0), N)
+        L = min(c + n, most)
+        pos = np.arange(L)
+        pg = table[b, pos // page].astype(np.int64) if L else np.zeros(0, np.int64)
+        there = (pg >= 0) & (pg < P)
+        at = np.where(there, pg, 0)
+        for h in range(H):
+            keys, values = (values4(codes[at, h, pos % page], sf[at, h, pos % page]) for codes, sf in cache)
+            for i in range(n):
+                seen = there.copy()
+                for j in range(L - c):
+                    seen[c + j] &= bool(mask[b, i, j])
+                w = np.nonzero(seen)[0]
+                if len(w) == 0:
+                    continue
+                key, val = keys[w], values[w]
+                for g in range(G):
+                    x = q[b, i, h * G + g].astype(np.float64)
+                    with np.errstate(all="ignore"):
+                        s = key @ x * scale
+                        # a score's error: its sum's, and a few roundings of the scaled value
+                        es = np.max((D + 8) * eps * (np.abs(key) @ np.abs(x)) * abs(scale))
+                        m = s.max()
+                        p = np.exp(s - m)
+                        z = p.sum()
+                        o[b, i, h * G + g] = p @ val / z
+                        lse[b, i, h * G + g] = m + np.log(z)
+                        # the sums run over len(w) terms, of the weights and of the values
+                        rel = 2 * es + (len(w) + 64) * eps + 2.0 ** -20
+                        # a weight is kept to 16 bits; what is below 2^-92 of the largest may be nothing
+                        least = len(w) * 2.0 ** -92 * np.nanmax(np.abs(val), initial=0.0) + 2.0 ** -92
+                        bo[b, i, h * G + g] = (np.abs(p) @ np.abs(val) / z * (2.0 ** -16 + 2 * rel) + least
+                                               + 2.0 ** -8 * np.abs(o[b, i, h * G + g]))
+                        bl[b, i, h * G + g] = rel + 2.0 ** -20 + 4 * eps * abs(m)
+    return o, lse, bo, bl

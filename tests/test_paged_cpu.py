@@ -163,10 +163,132 @@ def test_reference_norm_rope():
         np.testing.assert_allclose(dw, b.grad.numpy(), atol=1e-12)
 
 
+# ---- the FP4 cache -------------------------------------------------------------------------------
+
+def write4(lib, k=A[0], v=A[1], dt=dg.DG_BF16, ks=1024, vs=1024, slots=A[2], kc=A[3], kf=A[4], vc=A[5], vf=A[6],
+           T=16, H=8, D=128, P=10, page=64):
+    return lib.dg_fp4_kv_cache_write(k, v, dt, ks, vs, slots, kc, kf, vc, vf, T, H, D, P, page, None)
+
+
+def read4(lib, kc=A[3], kf=A[4], vc=A[5], vf=A[6], slots=A[2], k=A[0], v=A[1], dt=dg.DG_BF16, T=16, H=8, D=128, P=10, page=64):
+    return lib.dg_fp4_kv_cache_read(kc, kf, vc, vf, slots, k, v, dt, T, H, D, P, page, None)
+
+
+def at(base, off):
+    return ctypes.c_void_p(base.value + off)
+
+
+CODES, SCALES = 10 * 8 * 64 * 64, 10 * 8 * 64 * 4        # bytes of the caches above
+
+
+@pytest.mark.parametrize("kw,needle", [
+    (dict(D=96), "D=96"), (dict(page=17), "page_size=17"), (dict(T=-1), "negative"), (dict(P=0), "num_pages=0"), (dict(P=1 << 26), "2^31"),
+    (dict(dt=3), "dtype"), (dict(ks=1016), "k_stride"), (dict(vs=1028), "16 bytes"), (dict(k=None), "k is NULL"),
+    (dict(v=BAD), "v is not 16-byte"), (dict(kf=BAD), "k_sf is not"), (dict(vc=A[3]), "overlap"), (dict(kf=at(A[3], CODES - 16)), "overlap"),
+    (dict(vf=at(A[4], SCALES - 16)), "overlap"), (dict(k=at(A[5], CODES - 16)), "overlap"), (dict(slots=at(A[6], SCALES - 16)), "overlap"),
+    (dict(T=BIG), "too large"), (dict(H=1 << 20), "H="),
+])
+def test_fp4_write_rejects(lib, kw, needle):
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are made up")
+    assert write4(lib, **kw) == INVALID
+    assert needle in err(lib)
+
+
+@pytest.mark.parametrize("kw,needle", [
+    (dict(D=32), "D=32"), (dict(page=100), "page_size=100"), (dict(T=-1), "negative"), (dict(P=0), "num_pages=0"), (dict(dt=0), "dtype"),
+    (dict(k=None), "k is NULL"), (dict(k=A[1]), "overlap"), (dict(v=at(A[3], CODES - 16)), "overlap"), (dict(slots=BAD), "slots is not"),
+])
+def test_fp4_read_rejects(lib, kw, needle):
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are made up")
+    assert read4(lib, **kw) == INVALID
+    assert needle in err(lib)
+
+
+def test_fp4_cache_without_work_or_device(lib):
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are made up")
+    assert write4(lib, T=0, k=None) == dg.DG_OK and read4(lib, T=0, k=None) == dg.DG_OK
+    assert write4(lib) in NO_DEVICE and read4(lib) in NO_DEVICE
+    # right behind one another, by the FP4 cache's sizes
+    assert write4(lib, kf=at(A[3], CODES), vf=at(A[3], CODES + SCALES)) in NO_DEVICE
+
+
+def attn4(lib, q=A[0], qs=4096, kc=A[1], kf=A[2], vc=A[3], vf=A[4], table=A[5], ctx=A[6], tree=A[7], mask=A[8],
+          o=A[9], lse=A[10], scale=0.1, B=4, N=3, Hq=32, H=8, D=128, P=50, page=64, MP=20, ws=A[11], ws_bytes=1 << 27):
+    return lib.dg_fp4_tree_attention(q, qs, kc, kf, vc, vf, table, ctx, tree, mask, o, lse, scale, B, N, Hq, H, D, P,
+                                     page, MP, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw,needle", [
+    (dict(B=-1), "B, N, Hq"), (dict(H=0), "H >= 1"), (dict(MP=0), "max_pages >= 1"), (dict(D=100), "D must be"),
+    (dict(page=48), "page_size"), (dict(Hq=33), "multiple of H"), (dict(MP=1 << 25), "2^30"), (dict(N=1 << 20), "2^20"),
+    (dict(P=0), "num_pages=0"), (dict(qs=4088), "q_stride=4088"), (dict(scale=float("nan")), "scale"), (dict(q=None), "q is NULL"),
+    (dict(kf=BAD), "k_sf is not"), (dict(table=None), "page_table is NULL"), (dict(mask=BAD), "tree_mask is not"), (dict(o=None), "o is NULL"),
+    (dict(ws_bytes=16), "needed"), (dict(ws=None), "workspace is NULL"), (dict(o=A[0]), "overlap"),
+    (dict(o=at(A[3], 50 * 8 * 64 * 64 - 16)), "overlaps the cache"), (dict(lse=at(A[4], 50 * 8 * 64 * 4 - 4)), "overlaps the cache"),
+])
+def test_fp4_attention_rejects(lib, kw, needle):
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are made up")
+    assert attn4(lib, **kw) == INVALID
+    assert needle in err(lib)
+
+
+def test_fp4_attention_workspace_is_a_function_of_the_sizes(lib):
+    f = lib.dg_fp4_tree_attention_workspace_bytes
+    assert f(32, 1, 32, 8, 128, 64, 128) > 0
+    assert f(0, 1, 32, 8, 128, 64, 128) == 0 and f(32, 1, 33, 8, 128, 64, 128) == 0 and f(32, 1, 32, 8, 96, 64, 128) == 0
+    assert f(1, 1, 8, 8, 128, 16, 1) == 0             # one step a head: never split
+    assert all(f(B, N, 64, 8, D, 64, 200) <= 1 << 28 for B in (1, 7, 64, 500) for N in (1, 16, 64, 200) for D in (64, 128, 256))
+    if not torch.cuda.is_available():
+        assert attn4(lib, B=0, q=None) == dg.DG_OK and attn4(lib) in NO_DEVICE and attn4(lib, tree=None, mask=None) in NO_DEVICE
+
+
+def test_reference_fp4_rows():
+    """Codes of a row of known values, the limit between two scales, and rows that are not finite."""
+    x = np.zeros((4, 64))
+    x[0, :9] = [6, -4, 3, 2, 1.5, 1, 0.5, 0.25, 0.26]
+    x[1, :3] = [6.01, 0.5, -1.5]                       # scale 2: 0.25 and -0.75, ties
+    x[2, 3], x[3, 40] = np.nan, np.inf
+    codes, sf = paged.quantise4(x)
+    v = paged.values4(codes, sf)
+    np.testing.assert_array_equal(v[0, :9], [6, -4, 3, 2, 1.5, 1, 0.5, 0, 0.5])
+    np.testing.assert_array_equal(v[1, :3], [6, 0, -2])
+    assert codes[0, 0] == 7 | 14 << 4 and sf[0, 0] == 127 and sf[1, 0] == 128 and (sf[:2, 1] == 127).all()
+    assert np.isnan(v[2, :32]).all() and not v[2, 32:].any() and np.isnan(v[3, 32:]).all() and sf[2, 0] == 255
+    every = paged.values4(np.arange(256, dtype=np.uint8).reshape(4, 64), np.full((4, 4), 127))
+    again, s = paged.quantise4(every)                  # every code is its own nearest
+    np.testing.assert_array_equal(paged.values4(again, s), every)
+
+
+def test_reference_attention4_closed_forms():
+    """Equal keys average what is seen; nothing seen gives 0 and -inf; a NaN scale of a value stays in
+    its 32 values."""
+    rng = np.random.default_rng(0)
+    D, page = 64, 16
+    cache = paged.random_cache4(rng, 2, 1, page, D)
+    cache[0][0][:] = 0
+    cache[1][1][1, 0, 2, 1] = 255
+    table = np.array([[1, 0]], np.int32)
+    q = rng.standard_normal((1, 2, 1, D))
+    mask = np.array([[[True, False], [False, False]]])
+    o, lse, bo, _ = paged.attention4(q, cache, table, [5], [2], mask, 0.3, page)
+    vals = paged.values4(cache[1][0][1, 0], cache[1][1][1, 0])
+    np.testing.assert_allclose(o[0, 0, 0, :32], vals[:6, :32].mean(0), atol=1e-12)
+    np.testing.assert_allclose(o[0, 1, 0, :32], vals[:5, :32].mean(0), atol=1e-12)
+    np.testing.assert_allclose(lse[0, :, 0], np.log([6, 5]), rtol=1e-12)
+    assert np.isnan(o[0, :, 0, 32:]).all() and np.isfinite(bo[0, :, 0, :32]).all()
+    o, lse, _, _ = paged.attention4(q, cache, table, [0], [2], mask, 0.3, page)
+    assert not o[0, 1].any() and np.isneginf(lse[0, 1]).all()
+
+
 # ---- the compiled kernels --------------------------------------------------------------------------
 
 @pytest.mark.skipif(not os.path.exists(HIPCC), reason="hipcc not available")
-@pytest.mark.parametrize("src,least", [("plan_kernel.hip", 2), ("norm_rope_kernel.hip", 49)])
+@pytest.mark.parametrize("src,least", [("plan_kernel.hip", 2), ("norm_rope_kernel.hip", 49), ("kv4_cache_kernel.hip", 12),
+                                       ("tree_attn4_kernel.hip", 23)])
 def test_no_vgpr_spill_no_scratch(src, least):
     reports = kernel_reports(src)
     assert len(reports) >= least, sorted(reports)
