@@ -41,7 +41,9 @@ namespace {
 constexpr int kWaves = 4;                 // of a workgroup where requests are split
 constexpr int kBrief = 24, kFew = 64;     // steps of requests that stay whole in a long table
 constexpr float kLazy = 4.0f;             // how far, in powers of two, scores pass m before m follows
-constexpr float kDown = 34.0f;             // powers of two that weights are less where O would overflow
+constexpr float kTop = 11.0f;             // weights are 2^kTop as large: up to 2^(kTop + kLazy), in fp16's range
+constexpr uint32_t kLeast = 0x6D6D6D6Du;   // E8M0 of 2^-18 in each byte: from there on 32 scales are in fp16's range
+constexpr float kDown = 45.0f;            // and 2^(kTop - kDown) where O would overflow
 
 // One step's share of the cache in a lane.
 template <int D>
@@ -120,11 +122,39 @@ __device__ __forceinline__ uint32_t e2m1x2_to_bf16x2(uint32_t w, float scale) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, B));
 }
 
+// The same as two fp16: exact for scales from 2^-23 to 2^13.
+template <int B>
+__device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t w, float scale) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, B));
+}
+
 // Eight values of a word as an MFMA fragment.
 __device__ __forceinline__ bf16x8_t e2m1x8_to_bf16x8(uint32_t w, float scale) {
     const u32x4_t r = {e2m1x2_to_bf16x2<0>(w, scale), e2m1x2_to_bf16x2<1>(w, scale), e2m1x2_to_bf16x2<2>(w, scale),
                        e2m1x2_to_bf16x2<3>(w, scale)};
     return __builtin_bit_cast(bf16x8_t, r);
+}
+
+// f(0), .., f(N - 1), each a constant.
+template <int N, typename F>
+__device__ __forceinline__ void for_bytes(F f) {
+    if constexpr (N > 1) for_bytes<N - 1>(f);
+    f(std::integral_constant<int, N - 1>());
+}
+
+// V's operands of D values 2 B and 2 B + 1 of a lane's D / 16: pairs of its 8 keys.
+template <int B, int D, typename F>
+__device__ __forceinline__ void pairs(const Keys4<D>& x, const uint32_t (&scale)[2][4], u32x4_t& even, u32x4_t& odd, F convert) {
+    constexpr std::integral_constant<int, B % 4> byte{};
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t a = convert(byte, x.v[u][2 * i][B / 4], scale[u][2 * i]);
+            const uint32_t b = convert(byte, x.v[u][2 * i + 1][B / 4], scale[u][2 * i + 1]);
+            even[2 * u + i] = __builtin_amdgcn_perm(b, a, 0x05040100u);
+            odd[2 * u + i] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+        }
 }
 
 // RT: row tiles, of each of a workgroup's W waves the same.
@@ -216,8 +246,10 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
     float m[RT], base[RT], l[RT];         // base: m + down, or 0 while nothing was seen, so that exp2 stays 0
     float down[RT];
 #pragma unroll
-    for (int t = 0; t < RT; ++t) down[t] = 0.0f;
-    for (int again = 0; again < 2; ++again) {
+    for (int t = 0; t < RT; ++t) down[t] = -kTop;
+    uint32_t out = 0;                     // a scale of a value was out of fp16's range
+    auto pass = [&](auto is_wide) {
+    constexpr bool WIDE = decltype(is_wide)::value;
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
         m[t] = -__builtin_inff();
@@ -335,6 +367,13 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
                 for (int i = 0; i < 4; ++i) sc[t][u][i] = p[i] * c2;
             }
         }
+        // whether fp16 holds the step's values
+        if (!WIDE && all) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < Keys::VS; ++i) out |= (x.vs[u][i] - kLeast) & 0xE0E0E0E0u;
+        }
         // scales of the lane's block of its 8 keys' values
         uint32_t vscale[2][4];
 #pragma unroll
@@ -366,7 +405,13 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (!at.live[u] || j0 + 16 * u + 4 * g + i >= L) vscale[u][i] = 0x3F800000u;
-            if (apart) {
+            if (!WIDE) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) out |= ((vscale[u][i] & 0x7F800000u) - (kLeast << 24 >> 1)) & 0xF0000000u;
+            }
+            if (WIDE && apart) {
                 bool bad = false;
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
@@ -433,58 +478,72 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
                 m[t] = mx[t];
             }
         }
-        bf16x8_t p_hi[RT], p_lo[RT];
+        float e[RT][2][4];
 #pragma unroll
-        for (int t = 0; t < RT; ++t) {
-            u32x4_t top, rest;
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float e0 = __builtin_amdgcn_exp2f(sc[t][u][2 * i] - base[t]);
-                    const float e1 = __builtin_amdgcn_exp2f(sc[t][u][2 * i + 1] - base[t]);
-                    l[t] += e0;
-                    l[t] += e1;
-                    const uint32_t b0 = __float_as_uint(e0), b1 = __float_as_uint(e1);
-                    top[2 * u + i] = __builtin_amdgcn_perm(b1, b0, 0x07060302u);
-                    rest[2 * u + i] = f32x2_to_bf16x2(e0 - __uint_as_float(b0 & 0xFFFF0000u), e1 - __uint_as_float(b1 & 0xFFFF0000u));
-                }
-            p_hi[t] = __builtin_bit_cast(bf16x8_t, top);
-            p_lo[t] = __builtin_bit_cast(bf16x8_t, rest);
-        }
-        __builtin_amdgcn_s_setprio(0);
-        // V^T: tile i takes D value r16 * DT + i of the lane's 8 keys
-        auto tiles = [&](auto byte) {
-            constexpr int B = decltype(byte)::value, word = B / 4;
-            u32x4_t even, odd;
+        for (int t = 0; t < RT; ++t)
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t ka = e2m1x2_to_bf16x2<B % 4>(x.v[u][2 * i][word], __uint_as_float(vscale[u][2 * i]));
-                    const uint32_t kb = e2m1x2_to_bf16x2<B % 4>(x.v[u][2 * i + 1][word], __uint_as_float(vscale[u][2 * i + 1]));
-                    even[2 * u + i] = __builtin_amdgcn_perm(kb, ka, 0x05040100u);
-                    odd[2 * u + i] = __builtin_amdgcn_perm(kb, ka, 0x07060302u);
+                for (int i = 0; i < 4; ++i) {
+                    e[t][u][i] = __builtin_amdgcn_exp2f(sc[t][u][i] - base[t]);
+                    l[t] += e[t][u][i];
                 }
+        if constexpr (!WIDE) {
+            f16x8_t pf[RT];
 #pragma unroll
             for (int t = 0; t < RT; ++t) {
-                acc[t][2 * B] = mfma_bf16(__builtin_bit_cast(bf16x8_t, even), p_lo[t], acc[t][2 * B]);
-                acc[t][2 * B + 1] = mfma_bf16(__builtin_bit_cast(bf16x8_t, odd), p_lo[t], acc[t][2 * B + 1]);
-                acc[t][2 * B] = mfma_bf16(__builtin_bit_cast(bf16x8_t, even), p_hi[t], acc[t][2 * B]);
-                acc[t][2 * B + 1] = mfma_bf16(__builtin_bit_cast(bf16x8_t, odd), p_hi[t], acc[t][2 * B + 1]);
+                u32x4_t w;
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) w[2 * u + i] = f32x2_to_f16x2(e[t][u][2 * i], e[t][u][2 * i + 1]);
+                pf[t] = __builtin_bit_cast(f16x8_t, w);
             }
-        };
-        tiles(std::integral_constant<int, 0>());
-        tiles(std::integral_constant<int, 1>());
-        if constexpr (D >= 128) {
-            tiles(std::integral_constant<int, 2>());
-            tiles(std::integral_constant<int, 3>());
-        }
-        if constexpr (D == 256) {
-            tiles(std::integral_constant<int, 4>());
-            tiles(std::integral_constant<int, 5>());
-            tiles(std::integral_constant<int, 6>());
-            tiles(std::integral_constant<int, 7>());
+            __builtin_amdgcn_s_setprio(0);
+            for_bytes<D / 32>([&](auto byte) {
+                constexpr int B = decltype(byte)::value;
+                u32x4_t even, odd;
+                pairs<B>(x, vscale, even, odd, [](auto b, uint32_t w, uint32_t sf) {
+                    return e2m1x2_to_f16x2<decltype(b)::value>(w, __uint_as_float(sf));
+                });
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                    acc[t][2 * B] = mfma_f16(__builtin_bit_cast(f16x8_t, even), pf[t], acc[t][2 * B]);
+                    acc[t][2 * B + 1] = mfma_f16(__builtin_bit_cast(f16x8_t, odd), pf[t], acc[t][2 * B + 1]);
+                }
+            });
+        } else {
+            bf16x8_t p_hi[RT], p_lo[RT];
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+                u32x4_t top, rest;
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float e0 = e[t][u][2 * i], e1 = e[t][u][2 * i + 1];
+                        const uint32_t b0 = __float_as_uint(e0), b1 = __float_as_uint(e1);
+                        top[2 * u + i] = __builtin_amdgcn_perm(b1, b0, 0x07060302u);
+                        rest[2 * u + i] = f32x2_to_bf16x2(e0 - __uint_as_float(b0 & 0xFFFF0000u), e1 - __uint_as_float(b1 & 0xFFFF0000u));
+                    }
+                p_hi[t] = __builtin_bit_cast(bf16x8_t, top);
+                p_lo[t] = __builtin_bit_cast(bf16x8_t, rest);
+            }
+            __builtin_amdgcn_s_setprio(0);
+            for_bytes<D / 32>([&](auto byte) {
+                constexpr int B = decltype(byte)::value;
+                u32x4_t even, odd;
+                pairs<B>(x, vscale, even, odd, [](auto b, uint32_t w, uint32_t sf) {
+                    return e2m1x2_to_bf16x2<decltype(b)::value>(w, __uint_as_float(sf));
+                });
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                    acc[t][2 * B] = mfma_bf16(__builtin_bit_cast(bf16x8_t, even), p_lo[t], acc[t][2 * B]);
+                    acc[t][2 * B + 1] = mfma_bf16(__builtin_bit_cast(bf16x8_t, odd), p_lo[t], acc[t][2 * B + 1]);
+                    acc[t][2 * B] = mfma_bf16(__builtin_bit_cast(bf16x8_t, even), p_hi[t], acc[t][2 * B]);
+                    acc[t][2 * B + 1] = mfma_bf16(__builtin_bit_cast(bf16x8_t, odd), p_hi[t], acc[t][2 * B + 1]);
+                }
+            });
         }
         __builtin_amdgcn_sched_barrier(0);
         fetch_v(next);
@@ -492,19 +551,25 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
         at = next;
     }
     }
-    // rows whose O is not finite take their steps again
-    bool off = false;
+    };
+    pass(std::false_type());
+    if (__any(out != 0)) {
+        // the same in bf16, and once more for rows whose O passed fp32's largest number
+        for (int again = 0; again < 2; ++again) {
+            pass(std::true_type());
+            bool off = false;
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-        float sum = 0.0f;                 // 0, or NaN
+            for (int t = 0; t < RT; ++t) {
+                float sum = 0.0f;         // 0, or NaN
 #pragma unroll
-        for (int i = 0; i < DT; ++i)
+                for (int i = 0; i < DT; ++i)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) sum = __builtin_fmaf(acc[t][i][k], 0.0f, sum);
-        down[t] = max_of_groups(sum == 0.0f ? 0.0f : kDown);
-        off |= down[t] > 0.0f;
-    }
-    if (!__any(off)) break;
+                    for (int k = 0; k < 4; ++k) sum = __builtin_fmaf(acc[t][i][k], 0.0f, sum);
+                down[t] = max_of_groups(sum == 0.0f ? -kTop : kDown - kTop);
+                off |= down[t] > 0.0f;
+            }
+            if (!__any(off)) break;
+        }
     }
 
     // The waves put down their O and meet: a thread then adds up four values of a

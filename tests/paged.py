@@ -213,9 +213,12 @@ def attention4(q, cache, table, ctx, lens, mask, scale, page):
                         lse[b, i, h * G + g] = m + np.log(z)
                         # the sums run over len(w) terms, of the weights and of the values
                         rel = 2 * es + (len(w) + 64) * eps + 2.0 ** -20
-                        # a weight is kept to 16 bits; what is below 2^-92 of the largest may be nothing
-                        least = len(w) * 2.0 ** -92 * np.nanmax(np.abs(val), initial=0.0) + 2.0 ** -92
-                        bo[b, i, h * G + g] = (np.abs(p) @ np.abs(val) / z * (2.0 ** -16 + 2 * rel) + least
+                        # A weight is kept to fp16's 11 bits, half a step of which is 2^-11, and to half of
+                        # fp16's least number 2^-24 in units of 2^-11 of the largest: 2^-36.  (Values out of
+                        # fp16's range: to 16 bits, and to 2^-92 of the values' unit.)
+                        with_nan = np.where(np.isnan(val), 0.0, np.abs(val))
+                        least = (2.0 ** -36 * with_nan.sum(0) + len(w) * 2.0 ** -92 * with_nan.max()) / z + 2.0 ** -92
+                        bo[b, i, h * G + g] = (np.abs(p) @ np.abs(val) / z * (2.0 ** -11 + 2 * rel) + least
                                                + 2.0 ** -8 * np.abs(o[b, i, h * G + g]))
                         bl[b, i, h * G + g] = rel + 2.0 ** -20 + 4 * eps * abs(m)
     return o, lse, bo, bl
