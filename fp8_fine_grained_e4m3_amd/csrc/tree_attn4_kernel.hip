@@ -48,11 +48,11 @@ constexpr float kDown = 45.0f;            // and 2^(kTop - kDown) where O would 
 // One step's share of the cache in a lane.
 template <int D>
 struct Keys4 {
-    static constexpr int VW = D == 256 ? 2 : 1, VS = D == 64 ? 2 : 4;
+    static constexpr int VW = D == 256 ? 2 : 1;
     uint32_t k[2][D / 32];
     uint32_t v[2][4][VW];
     uint32_t ks[2];
-    uint32_t vs[2][VS];
+    uint32_t vs[2];                       // of key 4 g + lane % 4 of each tile
 };
 
 // Where a step's two 16-key tiles lie (rows of the pool), uniform.
@@ -133,6 +133,21 @@ __device__ __forceinline__ bf16x8_t e2m1x8_to_bf16x8(uint32_t w, float scale) {
     const u32x4_t r = {e2m1x2_to_bf16x2<0>(w, scale), e2m1x2_to_bf16x2<1>(w, scale), e2m1x2_to_bf16x2<2>(w, scale),
                        e2m1x2_to_bf16x2<3>(w, scale)};
     return __builtin_bit_cast(bf16x8_t, r);
+}
+
+// A uniform place in memory, kept in scalar registers: what a lane adds to it (in 32 bits)
+// stays an offset of the load, and takes no 64-bit sums in vector registers.
+typedef const __attribute__((address_space(1))) uint8_t* Uniform;
+
+__device__ __forceinline__ Uniform uniform(const uint8_t* p) {
+    uint64_t u = reinterpret_cast<uintptr_t>(p);
+    asm("" : "+s"(u));                    // the compiler cannot take the sum apart again
+    return reinterpret_cast<Uniform>(u);
+}
+
+template <typename T>
+__device__ __forceinline__ T load_at(Uniform base, uint32_t place, int more = 0) {
+    return *reinterpret_cast<const __attribute__((address_space(1))) T*>(base + place + more);
 }
 
 // f(0), .., f(N - 1), each a constant.
@@ -221,16 +236,18 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
         for (int c = 0; c < D / 32; ++c) {
             u32x4_t w = {0, 0, 0, 0};
             if (r < rows) w = *reinterpret_cast<const u32x4_t*>(src + c * 8);
+            w ^= a.scale < 0.0f ? 0x80008000u : 0u;
             qf[t][c] = __builtin_bit_cast(bf16x8_t, w);
         }
         tok[t] = min(tok[t], a.N - 1);
     }
 
-    const int32_t* table = a.table + (int64_t)b * a.max_pages;
+    const Uniform pages_of = uniform(reinterpret_cast<const uint8_t*>(a.table + (int64_t)b * a.max_pages));
     // Lanes 2 n and 2 n + 1 ask for the pages of a step's two tiles: vector loads,
     // in the order of the others, two steps ahead.
     auto ask = [&](int step) {
-        return table[min((step * kStep + 16 * (lane & 1)) >> a.page_shift, a.max_pages - 1)];
+        const int page = min((step * kStep + 16 * (lane & 1)) >> a.page_shift, a.max_pages - 1);
+        return load_at<int32_t>(pages_of, 4 * page);
     };
     auto place = [&](int step, int pages) {
         Place w;
@@ -258,64 +275,58 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
 #pragma unroll
         for (int i = 0; i < DT; ++i) acc[t][i] = f32x4_t{0, 0, 0, 0};
     }
-    const float c2 = a.scale * kLog2e;
+    // Scores stay products until the exponential: with a scale that is not negative (the
+    // query's sign takes that) they are in the same order.  Above 0, so that -infinity stays.
+    const float c2 = __builtin_fmaxf(__builtin_fabsf(a.scale) * kLog2e, 0x1p-126f);
     const bool apart = a.N > 1;           // rows of several tokens: they may see different keys
     if (lo + wave < hi) {
     // uniform bases, a lane's place in 32 bits
-    const uint32_t k_off = r16 * (D / 2) + g * (D / 8), ks_off = r16 * (D / 32) + (D == 64 ? g / 2 : g * (D / 128));
-    const uint32_t v_off = 4 * g * (D / 2) + r16 * (D / 32), vs_off = 4 * g * (D / 32) + (D == 256 ? r16 / 8 * 4 : 0);
+    uint32_t k_off = r16 * (D / 2) + g * (D / 8), ks_off = r16 * (D / 32) + (D == 64 ? g / 2 : g * (D / 128));
+    uint32_t v_off = 4 * g * (D / 2) + r16 * (D / 32), vs_off = (4 * g + (r16 & 3)) * (D / 32) + (D == 256 ? r16 / 8 * 4 : 0);
     // rotation that brings the block's byte of a word of scales to the exponent's place
     const uint32_t turn = (8 * (D == 64 ? r16 / 8 : D == 128 ? r16 / 4 : r16 / 2 % 4) - 23) & 31;
     Keys x;
     const uint8_t* const k_sf = static_cast<const uint8_t*>(a.ks);
     const uint8_t* const v_sf = static_cast<const uint8_t*>(a.vs);
     auto fetch_k = [&](const Place& w, int t) {
-        const uint8_t* from = a.kc + w.row[t] * (D / 2) + k_off;
+        asm volatile("" : "+v"(k_off), "+v"(ks_off));
+        const Uniform from = uniform(a.kc + w.row[t] * (D / 2));
         if constexpr (D == 64) {
-            const u32x2_t v = *reinterpret_cast<const u32x2_t*>(from);
+            const u32x2_t v = load_at<u32x2_t>(from, k_off);
             x.k[t][0] = v.x;
             x.k[t][1] = v.y;
         } else {
 #pragma unroll
             for (int c = 0; c < D / 128; ++c) {
-                const u32x4_t v = reinterpret_cast<const u32x4_t*>(from)[c];
+                const u32x4_t v = load_at<u32x4_t>(from, k_off, 16 * c);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) x.k[t][4 * c + i] = v[i];
             }
         }
-        const uint8_t* sf = k_sf + w.row[t] * (D / 32) + ks_off;
-        if constexpr (D == 256) x.ks[t] = *reinterpret_cast<const uint16_t*>(sf);
-        else x.ks[t] = *sf;
+        const Uniform sf = uniform(k_sf + w.row[t] * (D / 32));
+        if constexpr (D == 256) x.ks[t] = load_at<uint16_t>(sf, ks_off);
+        else x.ks[t] = load_at<uint8_t>(sf, ks_off);
     };
     auto fetch_v = [&](const Place& w) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const uint8_t* from = a.vc + w.row[t] * (D / 2) + v_off;
+            asm volatile("" : "+v"(v_off), "+v"(vs_off));
+            const Uniform from = uniform(a.vc + w.row[t] * (D / 2));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if constexpr (D == 64) {
-                    x.v[t][i][0] = *reinterpret_cast<const uint16_t*>(from + i * (D / 2));
+                    x.v[t][i][0] = load_at<uint16_t>(from, v_off, i * (D / 2));
                 } else if constexpr (D == 128) {
-                    x.v[t][i][0] = *reinterpret_cast<const uint32_t*>(from + i * (D / 2));
+                    x.v[t][i][0] = load_at<uint32_t>(from, v_off, i * (D / 2));
                 } else {
-                    const u32x2_t v = *reinterpret_cast<const u32x2_t*>(from + i * (D / 2));
+                    const u32x2_t v = load_at<u32x2_t>(from, v_off, i * (D / 2));
                     x.v[t][i][0] = v.x;
                     x.v[t][i][1] = v.y;
                 }
             }
-            const uint8_t* sf = v_sf + w.row[t] * (D / 32) + vs_off;
-            if constexpr (D == 64) {
-                const u32x2_t v = *reinterpret_cast<const u32x2_t*>(sf);
-                x.vs[t][0] = v.x;
-                x.vs[t][1] = v.y;
-            } else if constexpr (D == 128) {
-                const u32x4_t v = *reinterpret_cast<const u32x4_t*>(sf);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) x.vs[t][i] = v[i];
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) x.vs[t][i] = *reinterpret_cast<const uint32_t*>(sf + i * (D / 32));
-            }
+            const Uniform sf = uniform(v_sf + w.row[t] * (D / 32));
+            if constexpr (D == 64) x.vs[t] = load_at<uint16_t>(sf, vs_off);
+            else x.vs[t] = load_at<uint32_t>(sf, vs_off);
         }
     };
     const int s_last = hi - 1;
@@ -364,25 +375,29 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) p = mfma_bf16(kf[c], qf[t][c], p);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sc[t][u][i] = p[i] * c2;
+                for (int i = 0; i < 4; ++i) sc[t][u][i] = p[i];
             }
         }
         // whether fp16 holds the step's values
         if (!WIDE && all) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int i = 0; i < Keys::VS; ++i) out |= (x.vs[u][i] - kLeast) & 0xE0E0E0E0u;
+            constexpr uint32_t least = D == 64 ? kLeast & 0xFFFF : kLeast;
+            out |= ((x.vs[0] - least) | (x.vs[1] - least)) & 0xE0E0E0E0u;
         }
-        // scales of the lane's block of its 8 keys' values
+        // Scales of the lane's block of its 8 keys' values, from the lanes of its quad.  These
+        // have the same block (for D = 256 two, of the word that they all have).
         uint32_t vscale[2][4];
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < 2; ++u) {
+            uint32_t own = x.vs[u];
+            if constexpr (D < 256) own = __builtin_amdgcn_alignbit(own, own, turn);
+            vscale[u][0] = __float_as_uint(of_quad<0>(__uint_as_float(own)));
+            vscale[u][1] = __float_as_uint(of_quad<1>(__uint_as_float(own)));
+            vscale[u][2] = __float_as_uint(of_quad<2>(__uint_as_float(own)));
+            vscale[u][3] = __float_as_uint(of_quad<3>(__uint_as_float(own)));
+            if constexpr (D == 256)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t w = x.vs[u][D == 64 ? i / 2 : i];
-                vscale[u][i] = __builtin_amdgcn_alignbit(w, w, D == 64 ? turn + 16 * (i & 1) : turn);
-            }
+                for (int i = 0; i < 4; ++i) vscale[u][i] = __builtin_amdgcn_alignbit(vscale[u][i], vscale[u][i], turn);
+        }
         if (!all) {
             const int mlane = fresh(lane), g = mlane >> 4;
 #pragma unroll
@@ -463,6 +478,7 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
             for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) mx[t] = __builtin_fmaxf(mx[t], sc[t][u][i]);
+            mx[t] *= c2;
             over |= mx[t] > m[t] + kLazy;
         }
         if (__any(over)) {
@@ -485,7 +501,7 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
             for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    e[t][u][i] = __builtin_amdgcn_exp2f(sc[t][u][i] - base[t]);
+                    e[t][u][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][u][i], c2, -base[t]));
                     l[t] += e[t][u][i];
                 }
         if constexpr (!WIDE) {
