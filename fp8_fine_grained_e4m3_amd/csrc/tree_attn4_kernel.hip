@@ -61,58 +61,84 @@ struct Place {
     bool live[2];                         // the tile has keys and a valid page
 };
 
+// floor(x / y) of whole numbers below 2^50.
+__device__ __forceinline__ int64_t floor_div(int64_t x, int64_t y) {
+    const int64_t q = (int64_t)((double)x / (double)y);
+    return q * y > x ? q - 1 : q;         // a quotient that was rounded up to the next whole number
+}
+
 // The requests and steps of a run.
 struct Span {
     int b, stride, end;                   // first request, from one to the next, past the last
-    int64_t s0, s1, start, total, runs;   // steps of all requests': the run's, where request b starts, all; runs in use
+    int ctx, n;                           // lengths of the first request, as given, where known
+    bool known;
+    int64_t s0, s1, start;                // the run's steps of all requests'; where request b starts
+    int64_t total, runs, per, more;       // all steps; runs in use, of which `more` have per + 1 steps, the others per
     bool none;                            // the run has nothing to do
+
+    __device__ __forceinline__ int64_t first_step(int64_t run) const { return per * run + min(run, more); }
+    __device__ __forceinline__ int64_t run_of(int64_t step) const {
+        const int64_t longer = more * (per + 1);
+        return step < longer ? floor_div(step, per + 1) : more + floor_div(step - longer, per);
+    }
 };
 
 // Several requests with no more than kBrief steps, or kFew where there are as many of
 // them as runs, stay whole and are dealt to the runs in turn.
 template <int W>
 __device__ __forceinline__ Span span_of(const AttnArgs& a, int run, int row0, int lane) {
-    Span s = {run, 1, a.B, 0, 1ll << 62, 0, 0, 1, false};
+    Span s = {run, 1, a.B, 0, 0, false, 0, 1ll << 62, 0, 0, 1, 1ll << 62, 0, false};
     if (a.whole) {
         s.end = run + 1;
-    } else {
-        // this run's steps of all requests', and the request that they start in
-        uint32_t upto = 0;                // of the lane's request and those before it of its 64, 2^31 at most
-        bool brief = a.B > 1, few = a.B >= a.runs;
-        for (int base = 0; base < a.B; base += 64) {
-            const int own = steps_of_lane(a, base + lane, row0);
-            brief = brief && !__any(own > kBrief);
-            few = few && !__any(own > kFew);
-            upto = sum_up_to_lane(own);
-            s.total += (uint32_t)__builtin_amdgcn_readlane(upto, 63);
-        }
-        if (brief || few) {
-            s.stride = a.runs;
-        } else {
-            s.runs = max((int64_t)1, min((int64_t)a.runs, s.total / W));
-            if (run >= s.runs) {
-                s.none = true;
-                return s;
-            }
-            s.s0 = s.total * run / s.runs;
-            s.s1 = s.total * (run + 1) / s.runs;
-            s.b = a.B;
-            for (int base = 0; base < a.B; base += 64) {
-                if (a.B > 64) upto = sum_up_to_lane(steps_of_lane(a, base + lane, row0));
-                const uint32_t before = __shfl_up(upto, 1);
-                const int64_t from = s.start + (lane > 0 ? before : 0u);
-                const uint64_t hit = __ballot(base + lane < a.B && (s.start + upto > s.s0 || from >= s.s0));
-                if (hit != 0) {
-                    const int at = __builtin_ctzll(hit);
-                    s.b = base + at;
-                    if (at > 0) s.start += (uint32_t)__builtin_amdgcn_readlane(upto, at - 1);
-                    break;
-                }
-                s.start += (uint32_t)__builtin_amdgcn_readlane(upto, 63);
-            }
-        }
+        return s;
     }
-
+    // this run's steps of all requests', and the request that they start in
+    uint32_t upto = 0;                    // of the lane's request and those before it of its 64, 2^31 at most
+    int ctx = 0, n = a.N;
+    auto steps = [&](int b) {
+        if (b >= a.B) return 0;
+        ctx = a.ctx[b];
+        n = a.tree ? a.tree[b] : a.N;
+        return request_of(a, ctx, n, row0).steps;
+    };
+    bool brief = a.B > 1, few = a.B >= a.runs;
+    for (int base = 0; base < a.B; base += 64) {
+        const int own = steps(base + lane);
+        brief = brief && !__any(own > kBrief);
+        few = few && !__any(own > kFew);
+        upto = sum_up_to_lane(own);
+        s.total += (uint32_t)__builtin_amdgcn_readlane(upto, 63);
+    }
+    if (brief || few) {
+        s.stride = a.runs;
+        return s;
+    }
+    s.runs = max((int64_t)1, min((int64_t)a.runs, s.total / W));
+    if (run >= s.runs) {
+        s.none = true;
+        return s;
+    }
+    s.per = floor_div(s.total, s.runs);
+    s.more = s.total - s.per * s.runs;
+    s.s0 = s.first_step(run);
+    s.s1 = s.first_step(run + 1);
+    s.b = a.B;
+    for (int base = 0; base < a.B; base += 64) {
+        if (a.B > 64) upto = sum_up_to_lane(steps(base + lane));
+        const uint32_t before = __shfl_up(upto, 1);
+        const int64_t from = s.start + (lane > 0 ? before : 0u);
+        const uint64_t hit = __ballot(base + lane < a.B && (s.start + upto > s.s0 || from >= s.s0));
+        if (hit != 0) {
+            const int at = __builtin_ctzll(hit);
+            s.b = base + at;
+            s.ctx = __builtin_amdgcn_readlane(ctx, at);
+            s.n = __builtin_amdgcn_readlane(n, at);
+            s.known = true;
+            if (at > 0) s.start += (uint32_t)__builtin_amdgcn_readlane(upto, at - 1);
+            break;
+        }
+        s.start += (uint32_t)__builtin_amdgcn_readlane(upto, 63);
+    }
     return s;
 }
 
@@ -196,19 +222,49 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
     const Span span = span_of<W>(a, run, row0, lane);
     if (span.none) return;
     int64_t start = span.start;           // of request b
+    // r / G of rows below 2^20: what the product is off by is less than half of 1 / G
+    const float one_of_g = 1.0f / (float)a.G;
+    auto token_of = [&](int r) { return (int)(((float)r + 0.5f) * one_of_g); };
     for (int b = span.b; b < span.end && (start < span.s1 || (run == span.runs - 1 && start == span.total)); b += span.stride) {
-    const Request rq = request(a, b, row0);
-    const int ctx = rq.ctx, rows = rq.n * a.G;
+    // What does not depend on the request's lengths is asked for before they are known:
+    // its first pages and queries.
+    const int lo = (int)max(span.s0 - start, (int64_t)0);
+    const Uniform pages_of = uniform(reinterpret_cast<const uint8_t*>(a.table + (int64_t)b * a.max_pages));
+    // Lanes 2 n and 2 n + 1 ask for the pages of a step's two tiles: vector loads,
+    // in the order of the others, two steps ahead.
+    auto ask = [&](int step) {
+        const int page = min((step * kStep + 16 * (lane & 1)) >> a.page_shift, a.max_pages - 1);
+        return load_at<int32_t>(pages_of, 4 * page);
+    };
+    int pages = ask(lo + wave), pages_next = ask(lo + wave + W), pages_after = ask(lo + wave + 2 * W);
+    // the lane's query row of each row tile, its D values in the keys' order
+    const int qlane = fresh(lane), qr16 = qlane & 15, qg = qlane >> 4;
+    u32x4_t query[RT][D / 32];
+    int tok[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        const int r = min(row0 + 16 * t + qr16, all_rows - 1);
+        tok[t] = token_of(r);
+        const int hq = h * a.G + r - tok[t] * a.G;
+        const uint16_t* src = a.q + ((int64_t)b * a.N + tok[t]) * a.q_stride + (int64_t)hq * D + qg * (D / 4);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) query[t][c] = *reinterpret_cast<const u32x4_t*>(src + c * 8);
+    }
     // a token alone that does not see itself is as good as past the end
     const bool blind = a.N == 1 && a.mask && !(uniform_input(reinterpret_cast<const int32_t*>(a.mask + b)) & 1);
+    const Request rq = span.known && b == span.b ? request_of(a, span.ctx, span.n, row0) : request(a, b, row0);
+    const int ctx = rq.ctx, rows = rq.n * a.G;
     const int L = blind ? min(ctx, rq.L) : rq.L;
-    const int lo = (int)max(span.s0 - start, (int64_t)0), hi = (int)min(span.s1 - start, (int64_t)rq.steps);
+    const int hi = (int)min(span.s1 - start, (int64_t)rq.steps);
     start += rq.steps;
-    auto out_row = [&](int r) { return ((int64_t)b * a.N + r / a.G) * Hq + h * a.G + r % a.G; };
+    auto out_row = [&](int r) {
+        const int token = token_of(r);
+        return ((int64_t)b * a.N + token) * Hq + h * a.G + r - token * a.G;
+    };
     const bool whole = lo == 0 && hi == rq.steps;
     if (lo == 0 && threadIdx.x == 0 && !a.whole && a.runs > 1) {
-        // the last run that starts at or before the request's last step
-        const int64_t last = whole ? run - 1 : (start * span.runs + span.total - 1) / span.total - 1;
+        // the run of the request's last step
+        const int64_t last = whole ? run - 1 : span.run_of(start - 1);
         a.split[((int64_t)b * a.H + h) * a.row_blocks + rb] = make_int2(run, (int)last);
     }
     if (rq.steps == 0) {                  // no row of the block sees anything
@@ -222,33 +278,6 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
         continue;
     }
 
-    // the lane's query row of each row tile, its D values in the keys' order
-    const int qlane = fresh(lane), qr16 = qlane & 15, qg = qlane >> 4;
-    bf16x8_t qf[RT][D / 32];
-    int tok[RT];
-#pragma unroll
-    for (int t = 0; t < RT; ++t) {
-        const int r = row0 + 16 * t + qr16;
-        tok[t] = r / a.G;
-        const int hq = h * a.G + r - tok[t] * a.G;
-        const uint16_t* src = a.q + ((int64_t)b * a.N + tok[t]) * a.q_stride + (int64_t)hq * D + qg * (D / 4);
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-            u32x4_t w = {0, 0, 0, 0};
-            if (r < rows) w = *reinterpret_cast<const u32x4_t*>(src + c * 8);
-            w ^= a.scale < 0.0f ? 0x80008000u : 0u;
-            qf[t][c] = __builtin_bit_cast(bf16x8_t, w);
-        }
-        tok[t] = min(tok[t], a.N - 1);
-    }
-
-    const Uniform pages_of = uniform(reinterpret_cast<const uint8_t*>(a.table + (int64_t)b * a.max_pages));
-    // Lanes 2 n and 2 n + 1 ask for the pages of a step's two tiles: vector loads,
-    // in the order of the others, two steps ahead.
-    auto ask = [&](int step) {
-        const int page = min((step * kStep + 16 * (lane & 1)) >> a.page_shift, a.max_pages - 1);
-        return load_at<int32_t>(pages_of, 4 * page);
-    };
     auto place = [&](int step, int pages) {
         Place w;
 #pragma unroll
@@ -259,6 +288,13 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
         }
         return w;
     };
+    bf16x8_t qf[RT][D / 32];
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c)
+            qf[t][c] = __builtin_bit_cast(bf16x8_t, row0 + 16 * t + qr16 < rows ? query[t][c] ^ (a.scale < 0.0f ? 0x80008000u : 0u)
+                                                                                : u32x4_t{0, 0, 0, 0});
     f32x4_t acc[RT][DT];
     float m[RT], base[RT], l[RT];         // base: m + down, or 0 while nothing was seen, so that exp2 stays 0
     float down[RT];
@@ -329,10 +365,8 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
             else x.vs[t] = load_at<uint32_t>(sf, vs_off);
         }
     };
-    const int s_last = hi - 1;
-    int pages = ask(min(lo + wave, s_last)), pages_next = ask(min(lo + wave + W, s_last));
-    Place at = place(min(lo + wave, s_last), pages);
-    pages = ask(min(lo + wave + 2 * W, s_last));
+    int ahead[2] = {pages_next, pages_after};     // pages of the two steps after this one
+    Place at = place(lo + wave, pages);
     fetch_k(at, 0);
     fetch_k(at, 1);
     __builtin_amdgcn_sched_barrier(0);
@@ -354,9 +388,9 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
     }
     for (int s = lo + wave; s < hi; s += W) {
         const int j0 = s * kStep;
-        const Place next = place(min(s + W, s_last), pages_next);
-        pages_next = pages;
-        pages = ask(min(s + 3 * W, s_last));
+        const Place next = place(s + W, ahead[0]);
+        ahead[0] = ahead[1];
+        ahead[1] = ask(s + 3 * W);
         __builtin_amdgcn_sched_barrier(0);
         const bool all = j0 + kStep <= ctx && at.live[0] && at.live[1];      // uniform: no mask here
         float sc[RT][2][4];
@@ -367,7 +401,7 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) kf[c] = e2m1x8_to_bf16x8(x.k[u][c], c < 4 ? s0 : s1);
             __builtin_amdgcn_sched_barrier(0);
-            fetch_k(next, u);
+
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int t = 0; t < RT; ++t) {
@@ -562,6 +596,8 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
             });
         }
         __builtin_amdgcn_sched_barrier(0);
+        fetch_k(next, 0);
+        fetch_k(next, 1);
         fetch_v(next);
         __builtin_amdgcn_sched_barrier(0);
         at = next;
