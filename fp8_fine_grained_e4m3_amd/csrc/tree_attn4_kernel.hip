@@ -17,20 +17,33 @@
 //    halves of words (v_perm) once they are bf16.  A key's scale of the block is a
 //    rotation of the word of its scales: the conversion looks at the eight bits of the
 //    exponent alone.
-//  * P is split into two bf16 parts, the first 8 bits and the next 8, each multiplied:
-//    16 bits, which the plain product's 8 would make the largest error of all.  bf16 has
-//    fp32's exponents, so no weight or value is out of range, whatever its scale.
-//    Where a row's O passes fp32's largest number all the same (values beyond 2^90), a wave
-//    takes its steps again with that row's weights 2^-kDown as large, which 2^30 weights of
-//    2^kLazy do not outgrow; always so, the exponentials' arguments would lose their last
-//    five bits.
+//  * P is rounded to fp16 for the second product: 11 bits, which bf16's 8 would make as
+//    large an error as the output's own rounding, and fp16 holds the values exactly while
+//    their scales are from 2^-18 to 2^13 (weights, 2^kTop as large, are kept to 2^-36 of the
+//    largest).  Each step's scales are looked at, a word a lane; where one is out of that
+//    range, or NaN, the wave takes its steps again in bf16, which has fp32's exponents and
+//    holds every value, with P in two parts, the first 8 bits and the next 8.  Where a row's
+//    O passes fp32's largest number even so (values beyond 2^90), once more with that row's
+//    weights 2^-kDown as large, which 2^30 weights of 2^kLazy do not outgrow; always so, the
+//    exponentials' arguments would lose their last five bits.  (Always two bf16 parts: 145 us
+//    against 124 for two trees of 16 over 100001.)
 //  * Maximum, sum and O are fp32; the maximum follows where a score passes it by 2^4.
 // Codes hold neither NaN nor infinity and a hidden key's weight is 0, so what a row
 // does not see reaches it only through a scale that is NaN.  Past the end of a request
 // scales are replaced; where rows of one request see different keys, a NaN of a value
 // is counted by a product of its own for the rows that see it.
 //
-// Work is cut into runs and joined as over the FP8 cache.
+// Bound: a few rows per key head leave the cache's bytes as the floor, half of the FP8
+// cache's; with many rows the VALU (widening keys and values, exponentials) is it.  The
+// cache goes from HBM straight to registers; a wave asks for its next step's keys and
+// values when it is done with the ones it has, and the other waves of its SIMD cover the
+// wait.  (Asked for during the step, or two steps ahead: the same times, and 10 to 40
+// registers more.)  Work is cut into runs and joined as over the FP8 cache.
+// Measured, in graphs (a batch "of n over c" goes from n tokens and c positions down to
+// half of them): 32 single tokens over 8192, 32 / 8 heads of 128, 215 MB, 52 us, 4.1 TB/s,
+// of which the first keys take 5 us to come (a loop over the same bytes alone: 38 us); one
+// over 1000, 9.3 us; two trees of 16 over 100001, 64 / 8 heads of 128, 164 MB and 66 GFLOP,
+// 123 us and 0.53 PFLOP/s; 7 trees of 24 over 3001, the last of them idle, 20 us.
 #include "tree_attn_common.h"
 
 #include <type_traits>
@@ -38,7 +51,6 @@
 namespace dg {
 namespace {
 
-constexpr int kWaves = 4;                 // of a workgroup where requests are split
 constexpr int kBrief = 24, kFew = 64;     // steps of requests that stay whole in a long table
 constexpr float kLazy = 4.0f;             // how far, in powers of two, scores pass m before m follows
 constexpr float kTop = 11.0f;             // weights are 2^kTop as large: up to 2^(kTop + kLazy), in fp16's range
@@ -678,7 +690,26 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
     }
 }
 
-// Row tiles, whole requests and runs by the same rules as over the FP8 cache.
+// Rows of a workgroup: 16 where there are no more (and for D = 256, whose O fills
+// the registers), else 32.  (64, with the query in LDS: 20 us against 33 for 7 trees of
+// 24 over 3001 with D = 64; D = 128 does not fit the registers, 182 us against 123.)
+// Whole requests, a workgroup each and no second kernel, where that is soon done
+// whatever the lengths turn out to be: up to 1024 positions (D = 256: 512), up to 2048
+// (two row tiles: 4096) where requests and heads make 128 workgroups, up to 12288 (4096)
+// where they make 256.  Split against whole, in graphs: 32 requests of 8192, 57.4 us
+// against 51.9; 128 of 8192, 189 against 177; 64 of 4000, 59 against 49; 7 trees of 24
+// over 3001, 27 against 20; but 16 of 8192, 33 against 43, 8 of 8192, 21 against 36, and one
+// of 1000 with D = 256, 11.3 against 13.3.
+// A whole request has eight waves, four where 16 steps are all (one of 1000: 9.3 us with
+// eight, 10.6 with four; 32 of 4000, 28 and 39), and as many fewer as are resident with all
+// the others, halved only where that leaves a wave 16 steps at most.
+// Runs: two workgroups of four waves a CU of 256, or one of eight where requests may be
+// long (fewer parts to join: one of 20000, 14.2 us against 16.1; 16 of 8192, 33 against
+// 35; 4 of 2000, 14.7 against 14.4).  D = 64 with two row tiles has room for a third wave a
+// SIMD only in workgroups of four (16 trees of 20 over 8000: 38 us against 44).  D = 256:
+// one workgroup a CU, of eight waves where each has 8 steps (16 of 8192, 55 us against 57;
+// one tree of 33 over 8192, 61 against 69; but 8 trees of 2 over 8000, 26 against 24).
+// From the sizes alone: lengths are on the device.
 Shape shape_of(int64_t B, int64_t N, int64_t Hq, int64_t H, int64_t D, int64_t max_pages, int64_t page_size) {
     const int64_t rows = N * (Hq / H);
     Shape s;
@@ -687,18 +718,19 @@ Shape shape_of(int64_t B, int64_t N, int64_t Hq, int64_t H, int64_t D, int64_t m
     const int64_t groups = H * s.row_blocks, most = (max_pages * page_size + kStep - 1) / kStep, steps = B * most;
     const int64_t workgroups = B * groups;
     s.whole = most <= (D == 256 ? 16 : 32) || (most <= (s.row_tiles == 2 ? 128 : 64) && workgroups >= 128) ||
-              (most <= 128 && workgroups >= 256);
+              (most <= (s.row_tiles == 2 ? 128 : 384) && workgroups >= 256);
     if (workgroups > (1 << 20)) s.whole = false;       // a grid has fewer than 2^32 threads
-    s.waves = kWaves;
     if (s.whole) {
-        const int64_t resident = 1024 * (D == 256 ? 1 : D == 128 ? 2 : 3);
-        s.waves = s.row_tiles == 2 ? 8 : 4;
+        const int64_t resident = 1024 * (D == 64 ? 3 : 2);
+        s.waves = s.row_tiles == 2 || most > 16 ? 8 : 4;
         while (s.waves > 1 && workgroups * s.waves > resident && 2 * most <= 16 * s.waves) s.waves /= 2;
+        s.runs = (int)B;
+        return s;
     }
-    s.runs = (int)B;
-    if (s.whole) return s;
-    const int64_t wanted = D == 256 ? 256 : 512;
-    s.runs = (int)std::max<int64_t>(1, std::min(wanted / groups, steps / kWaves));
+    if (D == 256) s.waves = steps * groups >= 256 * 64 ? 8 : 4;
+    else s.waves = most > 128 && (D == 128 || s.row_tiles == 1) ? 8 : 4;
+    const int64_t wanted = D == 256 || s.waves == 8 ? 256 : 512;
+    s.runs = (int)std::max<int64_t>(1, std::min(wanted / groups, steps / s.waves));
     return s;
 }
 
@@ -707,7 +739,7 @@ void launch_waves(const AttnArgs& a, int waves, dim3 grid, hipStream_t stream) {
     if (waves == 1) hipLaunchKernelGGL((tree_attn4_kernel<D, RT, 1>), grid, dim3(64), 0, stream, a);
     else if (waves == 2) hipLaunchKernelGGL((tree_attn4_kernel<D, RT, 2>), grid, dim3(128), 0, stream, a);
     else if (waves == 4) hipLaunchKernelGGL((tree_attn4_kernel<D, RT, 4>), grid, dim3(256), 0, stream, a);
-    else if constexpr (RT == 2) hipLaunchKernelGGL((tree_attn4_kernel<D, RT, 8>), grid, dim3(512), 0, stream, a);
+    else hipLaunchKernelGGL((tree_attn4_kernel<D, RT, 8>), grid, dim3(512), 0, stream, a);
 }
 
 template <int D>
