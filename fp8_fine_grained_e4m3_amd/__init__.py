@@ -800,7 +800,7 @@ def kv_cache_plan(page_table: torch.Tensor, context_lens: torch.Tensor, add_lens
                              f"{tuple(new_state.shape)}, want {shape} {shape} {(B,)} {(2,)}")
         _same_device(table, slots, positions, lens, new_state)
     _call("dg_kv_cache_plan", on, table.data_ptr(), ctx.data_ptr(), add.data_ptr(), pages.data_ptr(), state.data_ptr(),
-          slots.data_ptr(), positions.data_ptr(), lens.data_ptr(), new_state.data_ptr(), B, rows, int(padded), most, P,
+          slots.data_ptr(), positions.data_ptr(), lens.data_ptr(), new_state.data_ptr(), B, rows, padded, most, P,
           page_size)
     return slots, positions, lens, new_state
 
@@ -817,23 +817,24 @@ def _workspace(given: Optional[torch.Tensor], on: int, need) -> Tuple[torch.Tens
     return given, given.data_ptr(), given.numel()
 
 
-def _check_rows(given, like, weights, positions, inv_freq, on):
-    """What is wrong with the arguments of a norm and rotation: rows of both tensors,
-    weights, positions and frequencies."""
-    (q, k), dtype = like, like[0].dtype
+def _check_norm_rope(given, q, k, weights, positions, inv_freq):
+    """Finds what is wrong with the arguments of a norm and rotation: rows of both
+    tensors, weights, positions and frequencies."""
+    dtype, D = q.dtype, q.shape[2]
     if dtype not in _ROW_TYPES or any(t.dtype != dtype for t, _, _ in given):
         raise TypeError(f"{', '.join(name for _, _, name in given)} must all be bfloat16 or float32, got "
                         f"{[t.dtype for t, _, _ in given]}")
-    for t, shape, name in given:
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError(f"shape mismatch: {name} {tuple(t.shape)} must be {tuple(shape)}")
+    for t, like, name in given:
+        want = (q.shape[0], like.shape[1], D)
+        if tuple(t.shape) != want:
+            raise ValueError(f"shape mismatch: {name} {tuple(t.shape)} must be {want}")
         _rows(t, name)
     for w, name in zip(weights, ("q_weight", "k_weight")):
         if w is not None:
             if w.dtype not in _ROW_TYPES:
                 raise TypeError(f"{name} must be bfloat16 or float32, got {w.dtype}")
-            if tuple(_dev(w, name).shape) != (q.shape[2],):
-                raise ValueError(f"{name} {tuple(w.shape)} must be [{q.shape[2]}]")
+            if tuple(_dev(w, name).shape) != (D,):
+                raise ValueError(f"{name} {tuple(w.shape)} must be [{D}]")
     if weights[0] is not None and weights[1] is not None and weights[0].dtype != weights[1].dtype:
         raise TypeError(f"q_weight and k_weight must be of one type, got {weights[0].dtype} and {weights[1].dtype}")
     if tuple(_i32(positions, "positions").shape) != (q.shape[0],):
@@ -841,6 +842,19 @@ def _check_rows(given, like, weights, positions, inv_freq, on):
     if _f32(inv_freq, "inv_freq").dim() != 1:
         raise ValueError(f"inv_freq {tuple(inv_freq.shape)} must be [R / 2]")
     _same_device(q, k, *(t for t, _, _ in given), *weights, positions, inv_freq)
+
+
+def _norm_rope_right(q, k, wq, wk, positions, inv_freq, on) -> bool:
+    """Whether what both directions of the norm and rotation share is as it should be."""
+    T, _, D = q.shape
+    w = wk if wq is None else wq
+    return (on >= 0 and q.dtype in _ROW_TYPES and k.dtype is q.dtype and k.shape[0] == T and k.shape[2] == D
+            and k.get_device() == on and positions.dtype is _I32 and positions.shape == (T,) and positions.is_contiguous()
+            and positions.get_device() == on and inv_freq.dtype is _F32 and inv_freq.dim() == 1 and inv_freq.is_contiguous()
+            and inv_freq.get_device() == on
+            and (w is None or (w.dtype in _ROW_TYPES and w.shape == (D,) and w.is_contiguous() and w.get_device() == on))
+            and (wq is None or wk is None or (wk.dtype is w.dtype and wk.shape == (D,) and wk.is_contiguous()
+                                              and wk.get_device() == on)))
 
 
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tensor], k_weight: Optional[torch.Tensor],
@@ -854,24 +868,25 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tens
     those given but dense, or fills out, which may be q and k themselves."""
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} must be [T, heads, D]")
-    (T, Hq, D), H, on = q.shape, k.shape[1], q.get_device()
-    given = [(q, (T, Hq, D), "q"), (k, (T, H, D), "k")]
+    (T, Hq, D), H, on, wq, wk = q.shape, k.shape[1], q.get_device(), q_weight, k_weight
+    right = _norm_rope_right(q, k, wq, wk, positions, inv_freq, on)
     if out is not None:
-        given += [(out[0], (T, Hq, D), "out q"), (out[1], (T, H, D), "out k")]
-    wq, wk = q_weight, k_weight
-    w = wq if wq is not None else wk
-    if not (on >= 0 and q.dtype in _ROW_TYPES and positions.dtype is _I32 and positions.shape == (T,)
-            and inv_freq.dtype is _F32 and inv_freq.dim() == 1 and positions.is_contiguous() and inv_freq.is_contiguous()
-            and positions.get_device() == on and inv_freq.get_device() == on
-            and all(t.dtype is q.dtype and t.shape == shape and t.get_device() == on for t, shape, _ in given)
-            and all(x is None or (x.dtype is w.dtype and x.dtype in _ROW_TYPES and x.shape == (D,) and x.is_contiguous()
-                                  and x.get_device() == on) for x in (wq, wk))):
-        _check_rows(given, (q, k), (wq, wk), positions, inv_freq, on)
-    oq, ok = (q.new_empty((T, Hq, D)), k.new_empty((T, H, D))) if out is None else out
+        oq, ok = out
+        right = (right and oq.dtype is q.dtype and ok.dtype is q.dtype and oq.shape == q.shape and ok.shape == k.shape
+                 and oq.get_device() == on and ok.get_device() == on)
+    if not right:
+        _check_norm_rope([(q, q, "q"), (k, k, "k")] + ([] if out is None else [(out[0], q, "out q"), (out[1], k, "out k")]),
+                         q, k, (wq, wk), positions, inv_freq)
+    if out is None:
+        oq, ok = q.new_empty((T, Hq, D)), k.new_empty((T, H, D))
+        sq, sk = Hq * D, H * D
+    else:
+        sq, sk = _rows(oq, "out q"), _rows(ok, "out k")
+    w = wk if wq is None else wq
     _call("dg_qk_norm_rope", on, q.data_ptr(), k.data_ptr(), _ROW_TYPES[q.dtype], _rows(q, "q"), _rows(k, "k"),
           0 if wq is None else wq.data_ptr(), 0 if wk is None else wk.data_ptr(), DG_F32 if w is None else _ROW_TYPES[w.dtype],
-          positions.data_ptr(), inv_freq.data_ptr(), oq.data_ptr(), ok.data_ptr(), _rows(oq, "out q"), _rows(ok, "out k"),
-          eps, int(interleaved), T, Hq, H, D, 2 * inv_freq.shape[0])
+          positions.data_ptr(), inv_freq.data_ptr(), oq.data_ptr(), ok.data_ptr(), sq, sk, eps, interleaved, T, Hq, H, D,
+          2 * inv_freq.shape[0])
     return oq, ok
 
 
@@ -899,30 +914,30 @@ def qk_norm_rope_backward(dq: torch.Tensor, dk: torch.Tensor, q: torch.Tensor, k
     None, one is allocated for the call."""
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} must be [T, heads, D]")
-    (T, Hq, D), H, on = q.shape, k.shape[1], q.get_device()
-    given = [(q, (T, Hq, D), "q"), (k, (T, H, D), "k"), (dq, (T, Hq, D), "dq"), (dk, (T, H, D), "dk")]
+    (T, Hq, D), H, on, wq, wk = q.shape, k.shape[1], q.get_device(), q_weight, k_weight
+    right = (_norm_rope_right(q, k, wq, wk, positions, inv_freq, on) and dq.dtype is q.dtype and dk.dtype is q.dtype
+             and dq.shape == q.shape and dk.shape == k.shape and dq.get_device() == on and dk.get_device() == on)
     if out is not None:
-        given += [(out[0], (T, Hq, D), "out q"), (out[1], (T, H, D), "out k")]
-    wq, wk = q_weight, k_weight
-    w = wq if wq is not None else wk
-    if not (on >= 0 and q.dtype in _ROW_TYPES and positions.dtype is _I32 and positions.shape == (T,)
-            and inv_freq.dtype is _F32 and inv_freq.dim() == 1 and positions.is_contiguous() and inv_freq.is_contiguous()
-            and positions.get_device() == on and inv_freq.get_device() == on
-            and all(t.dtype is q.dtype and t.shape == shape and t.get_device() == on for t, shape, _ in given)
-            and all(x is None or (x.dtype is w.dtype and x.dtype in _ROW_TYPES and x.shape == (D,) and x.is_contiguous()
-                                  and x.get_device() == on) for x in (wq, wk))):
-        _check_rows(given, (q, k), (wq, wk), positions, inv_freq, on)
-    oq, ok = (q.new_empty((T, Hq, D)), k.new_empty((T, H, D))) if out is None else out
+        oq, ok = out
+        right = (right and oq.dtype is q.dtype and ok.dtype is q.dtype and oq.shape == q.shape and ok.shape == k.shape
+                 and oq.get_device() == on and ok.get_device() == on)
+    if not right:
+        _check_norm_rope([(q, q, "q"), (k, k, "k"), (dq, q, "dq"), (dk, k, "dk")]
+                         + ([] if out is None else [(out[0], q, "out q"), (out[1], k, "out k")]), q, k, (wq, wk), positions, inv_freq)
+    if out is None:
+        oq, ok = q.new_empty((T, Hq, D)), k.new_empty((T, H, D))
+        sq, sk = Hq * D, H * D
+    else:
+        sq, sk = _rows(oq, "out q"), _rows(ok, "out k")
     gq, gk = (None if x is None else x.new_empty(D, dtype=_F32) for x in (wq, wk))
-    ws, ws_bytes = 0, 0
+    w, ws, ws_bytes = wk if wq is None else wq, 0, 0
     if w is not None:
         workspace, ws, ws_bytes = _workspace(workspace, on, lambda: get_qk_norm_rope_backward_workspace_bytes(T, Hq, H, D))
     _call("dg_qk_norm_rope_backward", on, dq.data_ptr(), dk.data_ptr(), q.data_ptr(), k.data_ptr(), _ROW_TYPES[q.dtype],
           _rows(dq, "dq"), _rows(dk, "dk"), _rows(q, "q"), _rows(k, "k"), 0 if wq is None else wq.data_ptr(),
           0 if wk is None else wk.data_ptr(), DG_F32 if w is None else _ROW_TYPES[w.dtype], positions.data_ptr(),
-          inv_freq.data_ptr(), oq.data_ptr(), ok.data_ptr(), _rows(oq, "out q"), _rows(ok, "out k"),
-          0 if gq is None else gq.data_ptr(), 0 if gk is None else gk.data_ptr(), eps, int(interleaved), T, Hq, H, D,
-          2 * inv_freq.shape[0], ws, ws_bytes)
+          inv_freq.data_ptr(), oq.data_ptr(), ok.data_ptr(), sq, sk, 0 if gq is None else gq.data_ptr(),
+          0 if gk is None else gk.data_ptr(), eps, interleaved, T, Hq, H, D, 2 * inv_freq.shape[0], ws, ws_bytes)
     return oq, ok, gq, gk
 
 
