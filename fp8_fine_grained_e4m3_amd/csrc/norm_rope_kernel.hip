@@ -18,6 +18,12 @@
 // of their tokens once, into LDS, while its first rows are on their way.  The angle
 // is taken in 64 bits, in turns, and reduced to an eighth of a turn before it is
 // rounded to fp32, so far positions lose nothing.
+//
+// Measured: 16384 tokens of 32 + 8 heads of 128 in bf16, 336 MB, 66 us, 5.1 TB/s (a 2 GiB
+// copy: 4.9 to 5.3), with plain stores 71; their gradients, 503 MB, 107 us, 4.7 TB/s, of
+// which the sums of dw take 5.  Four rows a lane and step (gradients: two); with two, 71 us.
+// The gradients' grid is kBackwardGroups workgroups, each with a sum of dw: 512 take 118
+// us, 2048 take 112.  5 tokens: 3.6 us.
 #include "fp8_values.h"
 #include "row_access.h"
 #include "serve_internal.h"
@@ -78,6 +84,14 @@ __device__ __forceinline__ void values_of(const Raw<uint16_t>& r, float (&x)[8])
 __device__ __forceinline__ void values_of(const Raw<float>& r, float (&x)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(r.w[i]);
+}
+
+// Rows of a large problem are stored past the caches, which they would pass through
+// before they are read; those of a small one are read from there.
+template <int PASSES, typename T>
+__device__ __forceinline__ void store_row(T* p, const float (&x)[8]) {
+    if constexpr (PASSES > 1) store8(p, x);
+    else put8(p, x);
 }
 
 template <typename T>
@@ -183,7 +197,7 @@ __device__ __forceinline__ void turn(const Turn& t, const f32x2_t* angles, float
     }
 }
 
-// Cosines and sines of the tokens of rows [row0, row0 + count) into LDS.
+// Cosines and sines of tokens first to last into LDS.
 __device__ __forceinline__ void fill_angles(const RopeArgs& a, uint32_t first, uint32_t last, f32x2_t* angles) {
     const uint32_t n = (last - first + 1) * (uint32_t)a.half;
     for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
@@ -235,7 +249,7 @@ __global__ __launch_bounds__(kThreads) void norm_rope_kernel(RopeArgs a) {
             for (int i = 0; i < 8; ++i) x[i] *= r * w[i];
             turn<NEIGHBOURS>(t, sm_angles + (token[p] - first) * a.half, 1.0f, x, other, z);
             if (row0 + p * RPP + threadIdx.x / LPR < rows)
-                put8(static_cast<T*>(a.out[kind]) + token[p] * a.out_stride[kind] + head[p] * D + part * 8, z);
+                store_row<PASSES>(static_cast<T*>(a.out[kind]) + token[p] * a.out_stride[kind] + head[p] * D + part * 8, z);
         }
         __syncthreads();
     }
@@ -286,7 +300,7 @@ __global__ __launch_bounds__(kThreads) void norm_rope_backward_kernel(RopeArgs a
             gn = sum_of_row<LPR>(gn) * (1.0f / D);
 #pragma unroll
             for (int i = 0; i < 8; ++i) dy[i] = r * __builtin_fmaf(-x[i], gn, dy[i]);
-            if (live) put8(static_cast<T*>(a.out[kind]) + token[p] * a.out_stride[kind] + head[p] * D + part * 8, dy);
+            if (live) store_row<PASSES>(static_cast<T*>(a.out[kind]) + token[p] * a.out_stride[kind] + head[p] * D + part * 8, dy);
         }
         __syncthreads();
     }
