@@ -791,8 +791,8 @@ def kv_cache_plan(page_table: torch.Tensor, context_lens: torch.Tensor, add_lens
     if out is None:
         if rows < 0:
             raise ValueError(f"rows={rows} must not be negative")
-        slots, positions = table.new_empty(shape), table.new_empty(shape)
-        lens, new_state = table.new_empty(B), table.new_empty(2)
+        slots = table.new_empty(shape)
+        positions, lens, new_state = torch.empty_like(slots), torch.empty_like(ctx), torch.empty_like(state)
     else:
         slots, positions, lens, new_state = (_i32(t, f"out {name}") for t, name in zip(out, ("slots", "positions", "lens", "state")))
         if tuple(slots.shape) != shape or tuple(positions.shape) != shape or tuple(lens.shape) != (B,) or tuple(new_state.shape) != (2,):
