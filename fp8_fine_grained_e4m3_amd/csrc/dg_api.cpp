@@ -850,7 +850,7 @@ static dg_status norm_rope(dg::NormRope p, dg_dtype dtype, dg_dtype w_dtype, int
     const int64_t size = dtype == DG_F32 ? 4 : 2, heads[2] = {p.Hq, p.H};
     const bool any = p.T > 0 && (p.Hq > 0 || p.H > 0);
     Rows in[9], out[5];                    // x, dz and w of both, positions, inv_freq; out and dw of both, workspace
-    int ins = 0, outs = 0;
+    int ins = 0, outs = 0, own[5] = {-1, -1, -1, -1, -1};      // the input that an output is in place of
     for (int i = 0; i < 2; ++i) {
         const struct { const void* p; int64_t stride; const char* name; bool used, written; } rows[3] = {
             {p.x[i], p.x_stride[i], i ? "k" : "q", true, false},
@@ -864,6 +864,8 @@ static dg_status norm_rope(dg::NormRope p, dg_dtype dtype, dg_dtype w_dtype, int
             if (p.T == 0 || heads[i] == 0) continue;
             REQUIRE(r.p != nullptr, "%s is NULL", r.name);
             REQUIRE(aligned(r.p, 16), "%s is not 16-byte aligned", r.name);
+            // forward, a tensor's own input and output may be one: a row is written by the lanes that have read it
+            if (r.written && !p.backward && r.p == p.x[i] && r.stride == p.x_stride[i]) own[outs] = ins - 1;
             (r.written ? out[outs++] : in[ins++]) = Rows{r.p, ((p.T - 1) * r.stride + heads[i] * p.D) * size,
                                                          r.stride * size, heads[i] * p.D * size};
         }
@@ -890,14 +892,8 @@ static dg_status norm_rope(dg::NormRope p, dg_dtype dtype, dg_dtype w_dtype, int
         out[outs++] = Rows{workspace, need, 0, 0};
     }
     for (int i = 0; i < outs; ++i) {
-        for (int k = 0; k < ins; ++k) {
-            // forward in place: a row is written by the lanes that have read it
-            bool in_place = false;
-            for (int t = 0; t < 2; ++t)
-                in_place |= !p.backward && out[i].p == p.out[t] && in[k].p == p.x[t] && out[i].p == in[k].p &&
-                            out[i].stride == in[k].stride && out[i].width == in[k].width;
-            REQUIRE(in_place || rows_disjoint(out[i], in[k]), "an output or the workspace overlaps an input");
-        }
+        for (int k = 0; k < ins; ++k)
+            REQUIRE(own[i] == k || rows_disjoint(out[i], in[k]), "an output or the workspace overlaps an input");
         for (int k = 0; k < i; ++k) REQUIRE(rows_disjoint(out[i], out[k]), "the outputs or the workspace overlap");
     }
     p.f32 = dtype == DG_F32;

@@ -130,6 +130,10 @@ def test_rope_without_work_or_device(lib):
     side = dict(q=q, k=k, qs=6144, ks=6144)
     assert rope(lib, **side, qo=q, ko=k, qos=6144, kos=6144) in NO_DEVICE
     assert rope(lib, **side, qo=k, ko=q, qos=6144, kos=6144) == INVALID
+    # queries and keys that are one tensor: neither may be written over while the other is read
+    one = dict(q=q, k=q, qs=1024, ks=1024, Hq=8, qos=1024, kos=1024)
+    assert rope(lib, **one) in NO_DEVICE
+    assert rope(lib, **one, qo=q) == INVALID and rope(lib, **one, ko=q) == INVALID
     assert rope_grad(lib) in NO_DEVICE and rope_grad(lib, dwq=None, dwk=None, ws=None, ws_bytes=0) in NO_DEVICE
     assert rope_grad(lib, T=0, dwq=None, dwk=None) == dg.DG_OK and rope_grad(lib, T=0, ws=None) in NO_DEVICE
     f = lib.dg_qk_norm_rope_backward_workspace_bytes
