@@ -242,7 +242,8 @@ def test_fp4_attention_rejects(lib, kw, needle):
 
 def test_fp4_attention_workspace_is_a_function_of_the_sizes(lib):
     f = lib.dg_fp4_tree_attention_workspace_bytes
-    assert f(32, 1, 32, 8, 128, 64, 128) > 0
+    assert f(1, 1, 32, 8, 128, 64, 128) > 0 and f(32, 1, 32, 8, 128, 64, 400) > 0
+    assert f(32, 1, 32, 8, 128, 64, 128) == 0         # 256 workgroups of whole requests: nothing to join
     assert f(0, 1, 32, 8, 128, 64, 128) == 0 and f(32, 1, 33, 8, 128, 64, 128) == 0 and f(32, 1, 32, 8, 96, 64, 128) == 0
     assert f(1, 1, 8, 8, 128, 16, 1) == 0             # one step a head: never split
     assert all(f(B, N, 64, 8, D, 64, 200) <= 1 << 28 for B in (1, 7, 64, 500) for N in (1, 16, 64, 200) for D in (64, 128, 256))
