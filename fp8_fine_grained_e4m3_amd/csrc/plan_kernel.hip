@@ -14,8 +14,8 @@
 // the new pages and the returned ones of those requests, each found by a binary
 // search in LDS; a new page is read from the ring, not from the table that another
 // workgroup writes, so one launch does it all.  The ring's places that are read
-// (the free ones) and written (those behind them) are not the same ones, as there
-// are no more pages than places.
+// (the free ones) and written (those behind them, as far as there are any) are not the
+// same ones.
 //
 // Bound: latency, of the lengths' loads, the scans and a page's or the ring's load, one
 // after the other.  Measured, in graphs: 7 requests with a row each, 4.0 us; 256 requests
@@ -180,7 +180,7 @@ __global__ __launch_bounds__(THREADS) void kv_cache_plan_kernel(PlanArgs a) {
             const int j = sm_need[i] - (int)(sm_take[i] - (uint32_t)k);
             a.table[(int64_t)(base + i) * a.max_pages + j] = a.ring[in_ring(head + (uint32_t)k, P)];
         }
-        for (uint64_t k = (uint64_t)given + first; k < min(all[1], P); k += step) {
+        for (uint64_t k = (uint64_t)given + first; k < min(all[1], P - free); k += step) {
             const int i = first_above(sm_give, n, (uint32_t)k);
             const int j = sm_held[i] - (int)(sm_give[i] - (uint32_t)k);
             a.ring[in_ring(head + free + (uint32_t)k, P)] = a.table[(int64_t)(base + i) * a.max_pages + j];
@@ -199,7 +199,7 @@ __global__ __launch_bounds__(THREADS) void kv_cache_plan_kernel(PlanArgs a) {
     if (blockIdx.x == 0 && tid == 0) {
         const uint32_t last = a.B > 0 ? sm_last : 0;
         a.new_state[0] = (int)in_ring(head + last, P);
-        a.new_state[1] = (int)min(free - last + min(given, P), P);
+        a.new_state[1] = (int)(free - last + min(given, P - free));
     }
 }
 

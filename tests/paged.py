@@ -37,6 +37,7 @@ def plan(table, ctx, add, ring, state, page, rows, padded):
         tokens += new + [(-1, 0)] * (rows - len(new)) if padded else new
     if not padded:
         tokens = tokens[:rows] + [(-1, 0)] * (rows - len(tokens))
+    back = back[:P - free]
     for i, pg in enumerate(back):
         ring[(head + free + i) % P] = pg
     tokens = np.array(tokens, np.int64).reshape(-1, 2)

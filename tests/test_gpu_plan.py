@@ -95,6 +95,23 @@ def test_lengths_and_states_out_of_range():
     check(table, [0, 0, 0], [1, 16, 17], ring, [5, full + 100], 16, 40, False)
 
 
+@pytest.mark.parametrize("B", [2, 9, 700])
+def test_shared_pages_come_back_from_each_request(B):
+    """More pages come back than the ring has places for: the first ones are kept, and the free
+    pages that a growing request takes in the same call are not written over."""
+    announce(f"plan: shared pages B={B}")
+    rng = np.random.default_rng(B)
+    P, width = 3 * B, 8
+    ring = rng.permutation(P).astype(np.int32)
+    table = np.repeat(rng.permutation(P)[None, :width], B, 0).astype(np.int32)[:, :6].copy()
+    table = np.concatenate([table, np.full((B, 4), -1, np.int32)], 1)
+    ctx = np.full(B, 6 * 16, np.int32)
+    add = np.where(np.arange(B) % 2 == 0, -6 * 16, 16).astype(np.int32)
+    for free in (B // 2, P - 3, P):
+        _, _, state, _ = check(table, ctx, add, ring, [P - 2, free], 16, 16 * B, False)
+        assert state[1].item() <= P
+
+
 def test_no_requests():
     announce("plan: B = 0")
     pool = dg.make_kv_page_pool(5)
