@@ -413,8 +413,6 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) kf[c] = e2m1x8_to_bf16x8(x.k[u][c], c < 4 ? s0 : s1);
             __builtin_amdgcn_sched_barrier(0);
-
-            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int t = 0; t < RT; ++t) {
                 f32x4_t p = {0, 0, 0, 0};

@@ -497,6 +497,8 @@ dg_status dg_fp8_kv_cache_read(const uint8_t* k_codes, const float* k_sf,
  *   - A request that shrinks (drafts that were not accepted; -c when it is done)
  *     gives the pages behind its new end back, to the ring's end, requests in
  *     order; they can be taken by later calls.  Its table row stays as it is.
+ *     A page that several requests hold comes back from each; what passes the ring's
+ *     num_pages - n other places is left out.
  *   page_table    [B, max_pages] int32, changed in place
  *   context_lens  [B]            clamped to [0, max_pages * page_size]
  *   add_lens      [B]            new tokens, or (negative) dropped ones
@@ -654,8 +656,10 @@ dg_status dg_fp4_kv_cache_read(const uint8_t* k_codes, const uint8_t* k_sf,
 
 /*
  * Attention over the FP4 cache: dg_fp8_tree_attention with
- *   - weights kept to 16 bits, values and keys exact (nothing depends on the largest
- *     scale); terms below 2^-92 of the values' unit may count as 0;
+ *   - keys and values exact, and a weight, alone, kept to 11 bits and to 2^-36 of the
+ *     row's largest; where a value that is read with it has a scale outside 2^-18 to
+ *     2^13, to 16 bits and to 2^-92 of the largest.  What is less, and an o below
+ *     2^-92, may count as 0;
  *   - a NaN scale in a key that a token sees makes the token's o and lse NaN; one in a
  *     value makes the 32 values of o that it belongs to NaN;
  *   - any codes and scales past a request's last token and in hidden pages.
@@ -715,8 +719,8 @@ const char* dg_last_error(void);
  * dg_get_num_cus() returns the current cap (the device's CU count by
  * default, 0 if no device is visible); dg_set_num_cus(n) accepts
  * 1 <= n <= device CU count, or 0 to restore the default.  The casts, the
- * indexer's logits and the few-token calls are not persistent: they launch
- * what their sizes ask for, whatever the cap.
+ * indexer's logits, the plan, the norms with rotation and the few-token calls
+ * are not persistent: they launch what their sizes ask for, whatever the cap.
  */
 int dg_get_num_cus(void);
 dg_status dg_set_num_cus(int n);
