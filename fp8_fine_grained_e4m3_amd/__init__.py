@@ -17,9 +17,14 @@ it in.
 For steps of a few tokens there are the paged FP8 key/value cache
 (make_fp8_kv_cache, fp8_kv_cache_write, fp8_kv_cache_read), attention of drafted
 trees or single tokens over it (fp8_tree_attention) and a whole
-mixture-of-experts layer (fp8_moe_few_tokens).  These allocate what they return
+mixture-of-experts layer (fp8_moe_few_tokens).  Around a cache of either kind
+there are the plan that gives requests their pages and tokens their slots
+(make_kv_page_pool, kv_cache_plan), the norms of queries and keys with their
+rotation (qk_norm_rope, and qk_norm_rope_backward for training), and the cache in
+4 bits with its attention (make_fp4_kv_cache, fp4_kv_cache_write,
+fp4_kv_cache_read, fp4_tree_attention).  All these allocate what they return
 unless it is passed in, and take their workspace from torch's allocator unless
-one is given (make_fp8_*_workspace).
+one is given (make_*_workspace).
 """
 from __future__ import annotations
 
