@@ -212,7 +212,7 @@ __device__ __forceinline__ void pairs(const Keys4<D>& x, const uint32_t (&scale)
 
 // RT: row tiles, of each of a workgroup's W waves the same.
 template <int D, int RT, int W>
-__global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) void tree_attn4_kernel(AttnArgs a) {
+__global__ __launch_bounds__(W * 64, W == 16 ? 4 : D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) void tree_attn4_kernel(AttnArgs a) {
     constexpr int DT = D / 16;            // 16-row tiles of O^T
     constexpr int ROWS = 16 * RT;
     constexpr int PITCH = D + 4;          // of a row of O in LDS
@@ -707,6 +707,11 @@ __global__ __launch_bounds__(W * 64, D == 256 ? 1 : D == 128 || W == 8 ? 2 : 3) 
 // SIMD only in workgroups of four (16 trees of 20 over 8000: 38 us against 44).  D = 256:
 // one workgroup a CU, of eight waves where each has 8 steps (16 of 8192, 55 us against 57;
 // one tree of 33 over 8192, 61 against 69; but 8 trees of 2 over 8000, 26 against 24).
+// D = 64 with one row tile has registers for four waves a SIMD: sixteen a workgroup where
+// requests may be long and a CU has one of them (32 of 8192, 34 us against 42; 40 of
+// 8192, 45 against 47; split, 32 of 20000, 76 against 85; but 32 of 1000 in either table
+// 1 us more, and with fewer or more requests, 16 of 8192, 25.3 against 24.7, 8 of 1000 in a
+// table of 60000, 16 against 14, 256 of 300 in one of 20000, 38.6 against 36.2).
 // From the sizes alone: lengths are on the device.
 Shape shape_of(int64_t B, int64_t N, int64_t Hq, int64_t H, int64_t D, int64_t max_pages, int64_t page_size) {
     const int64_t rows = N * (Hq / H);
@@ -718,16 +723,19 @@ Shape shape_of(int64_t B, int64_t N, int64_t Hq, int64_t H, int64_t D, int64_t m
     s.whole = most <= (D == 256 ? 16 : 32) || (most <= (s.row_tiles == 2 ? 128 : 64) && workgroups >= 128) ||
               (most <= (s.row_tiles == 2 ? 128 : 384) && workgroups >= 256);
     if (workgroups > (1 << 20)) s.whole = false;       // a grid has fewer than 2^32 threads
+    const bool sixteen = D * s.row_tiles == 64 && most > 64 && workgroups >= 256 && workgroups < 512;
     if (s.whole) {
         const int64_t resident = 1024 * (D == 64 ? 3 : 2);
         s.waves = s.row_tiles == 2 || most > 16 ? 8 : 4;
+        if (sixteen) s.waves = 16;
         while (s.waves > 1 && workgroups * s.waves > resident && 2 * most <= 16 * s.waves) s.waves /= 2;
         s.runs = (int)B;
         return s;
     }
     if (D == 256) s.waves = steps * groups >= 256 * 64 ? 8 : 4;
     else s.waves = most > 128 && (D == 128 || s.row_tiles == 1) ? 8 : 4;
-    const int64_t wanted = D == 256 || s.waves == 8 ? 256 : 512;
+    if (sixteen) s.waves = 16;
+    const int64_t wanted = D == 256 || s.waves >= 8 ? 256 : 512;
     s.runs = (int)std::max<int64_t>(1, std::min(wanted / groups, steps / s.waves));
     return s;
 }
@@ -737,7 +745,8 @@ void launch_waves(const AttnArgs& a, int waves, dim3 grid, hipStream_t stream) {
     if (waves == 1) hipLaunchKernelGGL((tree_attn4_kernel<D, RT, 1>), grid, dim3(64), 0, stream, a);
     else if (waves == 2) hipLaunchKernelGGL((tree_attn4_kernel<D, RT, 2>), grid, dim3(128), 0, stream, a);
     else if (waves == 4) hipLaunchKernelGGL((tree_attn4_kernel<D, RT, 4>), grid, dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL((tree_attn4_kernel<D, RT, 8>), grid, dim3(512), 0, stream, a);
+    else if (waves == 8) hipLaunchKernelGGL((tree_attn4_kernel<D, RT, 8>), grid, dim3(512), 0, stream, a);
+    else if constexpr (D * RT == 64) hipLaunchKernelGGL((tree_attn4_kernel<D, RT, 16>), grid, dim3(1024), 0, stream, a);
 }
 
 template <int D>

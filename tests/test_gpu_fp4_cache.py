@@ -326,6 +326,17 @@ def test_whole_requests_in_a_long_table(B, N, H, G, D, most):
     check_attention(*attention_case(B, N, H, G, D, 16, ctx, lens, mask, B, room=5000))
 
 
+@pytest.mark.parametrize("B,N,G,most,room", [(33, 1, 2, 3000, 5000), (34, 4, 4, 2100, 9000), (33, 2, 4, 2000, 50000), (32, 1, 2, 6000, 20000)])
+def test_sixteen_waves_a_workgroup(B, N, G, most, room):
+    """Heads of 64 in tables of long requests: whole ones, short ones dealt to the runs, split ones."""
+    announce(f"fp4 sixteen waves B={B} N={N} G={G} room={room}")
+    rng = np.random.default_rng(room)
+    mask = np.stack([ft.random_tree(rng, N) for _ in range(B)])
+    ctx, lens = rng.integers(0, most + 1, B), rng.integers(0, N + 1, B)
+    ctx[0], ctx[B // 2], lens[0] = most - N, 0, N
+    check_attention(*attention_case(B, N, 8, G, 64, 16, ctx, lens, mask, B, room=room))
+
+
 @pytest.mark.parametrize("B,N,G,ctx", [(70, 1, 2, 1500), (1, 1, 4, 5000), (3, 1, 8, 2500), (70, 1, 2, 60), (2, 12, 8, 1500)])
 def test_requests_split_over_workgroups(B, N, G, ctx):
     announce(f"fp4 split B={B} N={N} G={G} ctx={ctx}")

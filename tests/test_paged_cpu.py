@@ -293,7 +293,7 @@ def test_reference_attention4_closed_forms():
 
 @pytest.mark.skipif(not os.path.exists(HIPCC), reason="hipcc not available")
 @pytest.mark.parametrize("src,least", [("plan_kernel.hip", 2), ("norm_rope_kernel.hip", 49), ("kv4_cache_kernel.hip", 12),
-                                       ("tree_attn4_kernel.hip", 23)])
+                                       ("tree_attn4_kernel.hip", 24)])
 def test_no_vgpr_spill_no_scratch(src, least):
     reports = kernel_reports(src)
     assert len(reports) >= least, sorted(reports)
