@@ -528,14 +528,18 @@ __global__ __launch_bounds__(W * 64, W == 16 ? 4 : D == 256 ? 1 : D == 128 || W 
         if (__any(over)) {
 #pragma unroll
             for (int t = 0; t < RT; ++t) {
-                mx[t] = __builtin_fmaxf(max_of_groups(mx[t]), m[t]);
-                const float from = base[t];
-                if (mx[t] != -__builtin_inff()) base[t] = mx[t] + down[t];
-                const float f = m[t] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(from - base[t]);
+                // each row by its own scores: what the others have takes no bits of it
+                mx[t] = max_of_groups(mx[t]);
+                float f = 1.0f;
+                if (mx[t] > m[t] + kLazy) {
+                    const float from = base[t];
+                    base[t] = mx[t] + down[t];
+                    f = m[t] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(from - base[t]);
+                    m[t] = mx[t];
+                }
                 l[t] *= f;
 #pragma unroll
                 for (int i = 0; i < DT; ++i) acc[t][i] *= f;
-                m[t] = mx[t];
             }
         }
         float e[RT][2][4];

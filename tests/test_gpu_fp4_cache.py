@@ -326,6 +326,19 @@ def test_whole_requests_in_a_long_table(B, N, H, G, D, most):
     check_attention(*attention_case(B, N, H, G, D, 16, ctx, lens, mask, B, room=5000))
 
 
+@pytest.mark.parametrize("B,N,H,G,D,most,room", [(2, 12, 2, 8, 64, 9000, 0), (2, 12, 2, 8, 128, 9000, 0), (10, 7, 2, 4, 128, 700, 9000),
+                                                  (6, 9, 2, 4, 64, 1900, 9000), (3, 5, 2, 8, 128, 4000, 9000), (130, 5, 2, 4, 64, 1500, 0),
+                                                  (130, 5, 2, 8, 128, 1500, 0), (40, 5, 8, 4, 64, 3500, 0)])
+def test_two_row_tiles(B, N, H, G, D, most, room):
+    """Tables long enough, or workgroups many enough, for 32 rows in each: split, dealt in turn, whole."""
+    announce(f"fp4 two row tiles B={B} N={N} H={H} G={G} D={D} room={room}")
+    rng = np.random.default_rng(B + D)
+    mask = np.stack([ft.random_tree(rng, N) for _ in range(B)])
+    ctx, lens = rng.integers(0, most + 1, B), rng.integers(0, N + 1, B)
+    ctx[0], ctx[B // 2], lens[0] = most - N, 0, N
+    check_attention(*attention_case(B, N, H, G, D, 16, ctx, lens, mask, B, room=room))
+
+
 @pytest.mark.parametrize("B,N,G,most,room", [(33, 1, 2, 3000, 5000), (34, 4, 4, 2100, 9000), (33, 2, 4, 2000, 50000), (32, 1, 2, 6000, 20000)])
 def test_sixteen_waves_a_workgroup(B, N, G, most, room):
     """Heads of 64 in tables of long requests: whole ones, short ones dealt to the runs, split ones."""
@@ -337,7 +350,7 @@ def test_sixteen_waves_a_workgroup(B, N, G, most, room):
     check_attention(*attention_case(B, N, 8, G, 64, 16, ctx, lens, mask, B, room=room))
 
 
-@pytest.mark.parametrize("B,N,G,ctx", [(70, 1, 2, 1500), (1, 1, 4, 5000), (3, 1, 8, 2500), (70, 1, 2, 60), (2, 12, 8, 1500)])
+@pytest.mark.parametrize("B,N,G,ctx", [(70, 1, 2, 1500), (1, 1, 4, 5000), (3, 1, 8, 2500), (70, 1, 2, 60), (2, 12, 8, 1500), (70, 1, 2, 4500)])
 def test_requests_split_over_workgroups(B, N, G, ctx):
     announce(f"fp4 split B={B} N={N} G={G} ctx={ctx}")
     rng = np.random.default_rng(B)
@@ -357,7 +370,7 @@ def test_many_short_requests(B, N, H, G, D):
     check_attention(*attention_case(B, N, H, G, D, 16, rng.integers(0, 120, B), rng.integers(0, N + 1, B), mask, B))
 
 
-@pytest.mark.parametrize("N,D,room", [(1, 128, 0), (6, 64, 0), (6, 128, 0), (6, 128, 5000), (20, 256, 0)])
+@pytest.mark.parametrize("N,D,room", [(1, 128, 0), (6, 64, 0), (6, 128, 0), (6, 128, 5000), (6, 128, 9000), (6, 64, 9000), (20, 256, 0)])
 def test_scales_that_are_nan(N, D, room):
     """NaN scales of keys and values in the context and in drafted tokens: what sees them, and of values
     the 32 that they belong to, is NaN and nothing else."""
@@ -382,10 +395,11 @@ def test_scales_that_are_nan(N, D, room):
 
 @pytest.mark.parametrize("N", [1, 5])
 @pytest.mark.parametrize("far", [60, 124])
-def test_values_of_very_different_sizes(N, far):
+@pytest.mark.parametrize("room", [5000, 9000])
+def test_values_of_very_different_sizes(N, far, room):
     """Scales of 2^far and 2^-far of values, some hidden from some rows: sums do not overflow, and small
     blocks keep their bits beside large ones."""
-    announce(f"fp4 large values N={N} far={far}")
+    announce(f"fp4 large values N={N} far={far} room={room}")
     rng = np.random.default_rng(far)
     mask = np.stack([ft.random_tree(rng, N) for _ in range(2)])
 
@@ -397,7 +411,7 @@ def test_values_of_very_different_sizes(N, far):
             vs[:, :, :, 1] = np.where(vs[:, :, :, 1] == 255, 255, 127 - far)
         vs[table[1, 2], 0, 9] = 127 + far              # one drafted token (position 41), all blocks
 
-    got, want = attention_case(2, N, 2, 4, 128, 16, [300, 40], [N, N], mask, far, change=change, room=5000 if N == 5 else 0)
+    got, want = attention_case(2, N, 2, 4, 128, 16, [300, 40], [N, N], mask, far, change=change, room=room if N == 5 else 0)
     check_attention(got, want)
 
 
@@ -413,6 +427,23 @@ def test_extreme_keys_and_queries():
     seen = hit & ~torch.isneginf(lse)
     assert seen.any() and o2[seen].isnan().all() and lse2[seen].isnan().all()
     assert same_bits(o2[~hit], o[~hit]) and same_bits(lse2[~hit], lse[~hit])
+
+
+@pytest.mark.parametrize("room", [0, 9000])
+@pytest.mark.parametrize("seed", range(6))
+def test_a_row_depends_on_its_own_query_alone(seed, room):
+    """Other queries of the same call changed, larger and not finite: a row keeps its bits."""
+    announce(f"fp4 rows apart seed={seed} room={room}")
+    q, cache, table, ctx, lens = random_call(seed=seed)
+    table = torch.cat([table, torch.full((table.shape[0], room // 16), -1, dtype=torch.int32, device="cuda")], 1)
+    o, lse = dg.fp4_tree_attention(q, cache, table, ctx, lens)
+    for change in (float("nan"), float("inf"), 30.0, -3.0):
+        other = q.clone()
+        other[:, ::2, ::3] *= change
+        o2, lse2 = dg.fp4_tree_attention(other, cache, table, ctx, lens)
+        same = torch.ones(q.shape[:3], dtype=torch.bool, device="cuda")
+        same[:, ::2, ::3] = False
+        assert same_bits(o2[same], o[same]) and same_bits(lse2[same], lse[same])
 
 
 def random_call(B=5, N=9, H=2, G=4, D=128, page=16, ctx=300, seed=0):
