@@ -693,15 +693,20 @@ __global__ __launch_bounds__(W * 64, W == 16 ? 4 : D == 256 ? 1 : D == 128 || W 
 }
 
 // Rows of a workgroup: 16 where there are no more (and for D = 256, whose O fills
-// the registers), else 32.  (64, with the query in LDS: 20 us against 33 for 7 trees of
-// 24 over 3001 with D = 64; D = 128 does not fit the registers, 182 us against 123.)
+// the registers), and where 32 would leave CUs without a workgroup and keys are few
+// enough to be widened twice; else 32.  16 against 32 rows, in graphs, D = 128: 8 trees
+// of 16 over 1000, 32 / 8 heads, 10.7 us against 15.4; over 8000, 37 against 42; but over
+// 14000, 59 against 54; 16 of 16 over 1000, 14.3 against 16.4; but over 3000, 30 against 27.
+// D = 64: 7 trees of 24 over 3001, 32 / 4 heads, 18.7 against 20.4.  (64, with the query in
+// LDS: 33 us for these; D = 128 does not fit the registers, 182 us against 123.)
 // Whole requests, a workgroup each and no second kernel, where that is soon done
 // whatever the lengths turn out to be: up to 1024 positions (D = 256: 512), up to 2048
-// (two row tiles: 4096) where requests and heads make 128 workgroups, up to 12288 (4096)
-// where they make 256.  Split against whole, in graphs: 32 requests of 8192, 57.4 us
-// against 51.9; 128 of 8192, 189 against 177; 64 of 4000, 59 against 49; 7 trees of 24
-// over 3001, 27 against 20; but 16 of 8192, 33 against 43, 8 of 8192, 21 against 36, and one
-// of 1000 with D = 256, 11.3 against 13.3.
+// where requests and heads make 32 workgroups (D = 256: 128), up to 4096 where they make
+// 128 (not D = 256), up to 12288 where they make 256 of 16 rows.  Split against whole: 8 of
+// 2000, 16.8 us against 13.4; 16 of 3000, 20.6 against 17.9; 24 of 4000, 25.5 against 22.0; 4
+// trees of 16 over 3000, 21.8 against 17.8; 32 of 8192, 57.4 against 51.9; 128 of 8192, 189
+// against 177; but 8 of 4000, 18.6 against 21.2, 16 of 8192, 33 against 43, and one of 1000
+// with D = 256, 11.3 against 13.3.
 // A whole request has eight waves, four where 16 steps are all (one of 1000: 9.3 us with
 // eight, 10.6 with four; 32 of 4000, 28 and 39), and as many fewer as are resident with all
 // the others, halved only where that leaves a wave 16 steps at most.
@@ -718,14 +723,16 @@ __global__ __launch_bounds__(W * 64, W == 16 ? 4 : D == 256 ? 1 : D == 128 || W 
 // table of 60000, 16 against 14, 256 of 300 in one of 20000, 38.6 against 36.2).
 // From the sizes alone: lengths are on the device.
 Shape shape_of(int64_t B, int64_t N, int64_t Hq, int64_t H, int64_t D, int64_t max_pages, int64_t page_size) {
-    const int64_t rows = N * (Hq / H);
+    const int64_t rows = N * (Hq / H), most = (max_pages * page_size + kStep - 1) / kStep;
+    const int64_t pairs = (rows + 31) / 32 * B * H;     // workgroups of two row tiles
     Shape s;
-    s.row_tiles = rows <= 16 || D == 256 ? 1 : 2;
+    s.row_tiles = rows <= 16 || D == 256 || (pairs < 256 && most <= 256) || (pairs < 512 && most <= 32) ? 1 : 2;
     s.row_blocks = (int)((rows + s.rows() - 1) / s.rows());
-    const int64_t groups = H * s.row_blocks, most = (max_pages * page_size + kStep - 1) / kStep, steps = B * most;
+    const int64_t groups = H * s.row_blocks, steps = B * most;
     const int64_t workgroups = B * groups;
-    s.whole = most <= (D == 256 ? 16 : 32) || (most <= (s.row_tiles == 2 ? 128 : 64) && workgroups >= 128) ||
-              (most <= (s.row_tiles == 2 ? 128 : 384) && workgroups >= 256);
+    s.whole = most <= (D == 256 ? 16 : 32) || (D <= 128 && most <= 64 && workgroups >= 32) ||
+              (most <= (D == 256 ? 64 : 128) && workgroups >= 128) ||
+              (s.row_tiles == 1 && most <= 384 && workgroups >= 256);
     if (workgroups > (1 << 20)) s.whole = false;       // a grid has fewer than 2^32 threads
     const bool sixteen = D * s.row_tiles == 64 && most > 64 && workgroups >= 256 && workgroups < 512;
     if (s.whole) {

@@ -220,7 +220,7 @@ def test_fp4_cache_without_work_or_device(lib):
 
 
 def attn4(lib, q=A[0], qs=4096, kc=A[1], kf=A[2], vc=A[3], vf=A[4], table=A[5], ctx=A[6], tree=A[7], mask=A[8],
-          o=A[9], lse=A[10], scale=0.1, B=4, N=3, Hq=32, H=8, D=128, P=50, page=64, MP=20, ws=A[11], ws_bytes=1 << 27):
+          o=A[9], lse=A[10], scale=0.1, B=4, N=3, Hq=32, H=8, D=128, P=50, page=64, MP=40, ws=A[11], ws_bytes=1 << 27):
     return lib.dg_fp4_tree_attention(q, qs, kc, kf, vc, vf, table, ctx, tree, mask, o, lse, scale, B, N, Hq, H, D, P,
                                      page, MP, ws, ws_bytes, None)
 
@@ -246,6 +246,7 @@ def test_fp4_attention_workspace_is_a_function_of_the_sizes(lib):
     assert f(32, 1, 32, 8, 128, 64, 128) == 0         # 256 workgroups of whole requests: nothing to join
     assert f(0, 1, 32, 8, 128, 64, 128) == 0 and f(32, 1, 33, 8, 128, 64, 128) == 0 and f(32, 1, 32, 8, 96, 64, 128) == 0
     assert f(1, 1, 8, 8, 128, 16, 1) == 0             # one step a head: never split
+    assert f(4, 3, 32, 8, 128, 64, 20) == 0 and f(4, 3, 32, 8, 128, 64, 40) > 0
     assert all(f(B, N, 64, 8, D, 64, 200) <= 1 << 28 for B in (1, 7, 64, 500) for N in (1, 16, 64, 200) for D in (64, 128, 256))
     if not torch.cuda.is_available():
         assert attn4(lib, B=0, q=None) == dg.DG_OK and attn4(lib) in NO_DEVICE and attn4(lib, tree=None, mask=None) in NO_DEVICE
