@@ -27,7 +27,9 @@
 //    weights 2^-kDown as large, which 2^30 weights of 2^kLazy do not outgrow; always so, the
 //    exponentials' arguments would lose their last five bits.  (Always two bf16 parts: 145 us
 //    against 124 for two trees of 16 over 100001.)
-//  * Maximum, sum and O are fp32; the maximum follows where a score passes it by 2^4.
+//  * Maximum, sum and O are fp32; the maximum follows where a score of the row passes it by
+//    2^4, whatever other rows do, so that a row's bits are its own (all rows together: 124 us
+//    against 126 for two trees of 16 over 100001).
 // Codes hold neither NaN nor infinity and a hidden key's weight is 0, so what a row
 // does not see reaches it only through a scale that is NaN.  Past the end of a request
 // scales are replaced; where rows of one request see different keys, a NaN of a value
@@ -43,7 +45,7 @@
 // half of them): 32 single tokens over 8192, 32 / 8 heads of 128, 215 MB, 52 us, 4.1 TB/s,
 // of which the first keys take 5 us to come (a loop over the same bytes alone: 38 us); one
 // over 1000, 9.3 us; two trees of 16 over 100001, 64 / 8 heads of 128, 164 MB and 66 GFLOP,
-// 123 us and 0.53 PFLOP/s; 7 trees of 24 over 3001, the last of them idle, 20 us.
+// 126 us and 0.52 PFLOP/s; 7 trees of 24 over 3001, the last of them idle, 16 us.
 #include "tree_attn_common.h"
 
 #include <type_traits>
