@@ -164,20 +164,31 @@ def values4(codes, sf):
     return (v * scale[..., None]).reshape(codes.shape[:-1] + (2 * codes.shape[-1],))
 
 
-def random_cache4(rng, pages, H, page, D):
-    """Random codes, scales of several sizes (a fifth of the cache's blocks far smaller)."""
+def random_cache4(rng, pages, H, page, D, values=None):
+    """Random codes, scales of several sizes (a fifth of the cache's blocks far smaller).  values: a
+    function of rng and a shape that gives the bytes of the values' scales instead."""
     out = []
-    for _ in range(2):
+    for kind in range(2):
         codes = rng.integers(0, 256, (pages, H, page, D // 2)).astype(np.uint8)
         sf = (127 - 2 + rng.integers(-4, 3, (pages, H, page, D // 32))).astype(np.uint8)
         sf[rng.random(sf.shape) < 0.2] -= 20
+        if kind and values:
+            sf = values(rng, sf.shape).astype(np.uint8)
         out.append((codes, sf))
     return out
 
 
-def attention4(q, cache, table, ctx, lens, mask, scale, page):
+def form4(sf):
+    """What the attention makes of values with these bytes of scales: "fp16" where all are from 2^-18 to
+    2^13, "bf16" where none is, else "both"."""
+    inside = (np.asarray(sf) >= 127 - 18) & (np.asarray(sf) <= 127 + 13)
+    return "fp16" if inside.all() else "both" if inside.any() else "bf16"
+
+
+def attention4(q, cache, table, ctx, lens, mask, scale, page, form=None):
     """q [B, N, Hq, D] float; mask [B, N, N] bool.  Returns o, lse and the bounds of both; NaN where a
-    scale that is NaN reaches."""
+    scale that is NaN reaches.  form: "fp16" or "bf16" where all values are read in it, for bounds of
+    each column by itself."""
     (kc, ks), (vc, vs) = cache
     P, H = kc.shape[:2]
     B, N, Hq, D = q.shape
@@ -221,5 +232,14 @@ def attention4(q, cache, table, ctx, lens, mask, scale, page):
                         least = (2.0 ** -36 * with_nan.sum(0) + len(w) * 2.0 ** -92 * with_nan.max()) / z + 2.0 ** -92
                         bo[b, i, h * G + g] = (np.abs(p) @ np.abs(val) / z * (2.0 ** -11 + 2 * rel) + least
                                                + 2.0 ** -8 * np.abs(o[b, i, h * G + g]))
+                        if form:
+                            # A weight is kept to fp16's half step, 2^-11, and to 2^-36 of the largest; or to 16
+                            # bits and (as a product) to 2^-92.  Its exponent, a power of two up to 45 beside
+                            # |s - m|, is rounded to 24 bits.
+                            fp16 = form == "fp16"
+                            each = (2.0 ** -11 if fp16 else 2.0 ** -16) + 2 * rel + 2.0 ** -24 * (np.abs(s - m) + 46)
+                            least = 2.0 ** -36 * with_nan.sum(0) if fp16 else 2.0 ** -92 * (with_nan.sum(0) + len(w))
+                            bo[b, i, h * G + g] = ((p * each) @ np.abs(val) / z + least / z + 2.0 ** -92
+                                                   + 2.0 ** -8 * np.abs(o[b, i, h * G + g]))
                         bl[b, i, h * G + g] = rel + 2.0 ** -20 + 4 * eps * abs(m)
     return o, lse, bo, bl
