@@ -88,3 +88,18 @@ def test_one_scale_around_the_range(D, byte):
         c = forms.case(2, 4, 2, 4, D, 16, 70, 0, forms.VALUES["fp16"], D + byte, change=change)
         c["ctx"][1], c["lens"][1] = 4, 2
         check(c, "fp16")
+
+
+@pytest.mark.parametrize("N", [1, 5])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("room", [0, 9000])
+def test_small_columns_beside_large_ones(D, N, room):
+    """Sums of a block of 2^124 pass fp32's range: the other blocks keep their 16 bits."""
+    announce(f"fp4 small beside large D={D} N={N} room={room}")
+
+    def change(rng, cache, table, ctx, lens):
+        sf = cache[1][1]
+        sf[..., 0] = 127 + 124
+
+    c = forms.case(2, N, 2, 4, D, 16, 300, room, forms.VALUES["fp16"], D + N, change=change)
+    check(c, "bf16")
