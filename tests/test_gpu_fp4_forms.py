@@ -103,3 +103,20 @@ def test_small_columns_beside_large_ones(D, N, room):
 
     c = forms.case(2, N, 2, 4, D, 16, 300, room, forms.VALUES["fp16"], D + N, change=change)
     check(c, "bf16")
+
+
+@pytest.mark.parametrize("N", [1, 5])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("room", [0, 9000])
+def test_smallest_and_largest_scales(D, N, room):
+    """Blocks of keys and values with the scales 2^-126 and 2^125, queries that bring all to one size."""
+    announce(f"fp4 ends of scales D={D} N={N} room={room}")
+
+    def change(rng, cache, table, ctx, lens):
+        for _, sf in cache:
+            sf[..., 0], sf[..., 1] = 1, 252
+
+    c = forms.case(3, N, 2, 4, D, 16, 200, room, forms.VALUES["fp16"], D + N, scale=0.05, change=change)
+    c["q"][..., :32] *= 2.0 ** 124
+    c["q"][..., 32:64] *= 2.0 ** -121
+    check(c, "bf16")
