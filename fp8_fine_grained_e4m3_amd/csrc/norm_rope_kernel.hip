@@ -153,7 +153,7 @@ __device__ __forceinline__ float scale_of_row(const float (&x)[8], float eps) {
 struct Turn {
     bool on;                              // they are turned
     int partner;                          // lane with the other halves (the same for neighbours)
-    int angle;                            // first of their angles
+    int angle;                            // first of their angles (of values not turned: any)
     float sign;                           // -1: first halves, 1: second ones
 };
 
@@ -163,36 +163,39 @@ __device__ __forceinline__ Turn turn_of(int half, int part, int lane) {
     t.on = part * 8 < 2 * half;
     if (NEIGHBOURS) {
         t.partner = lane;
-        t.angle = part * 4;
+        t.angle = t.on ? part * 4 : 0;
         t.sign = 0.0f;
     } else {
         const bool second = part * 8 >= half;
         t.partner = t.on ? (second ? lane - half / 8 : lane + half / 8) : lane;
-        t.angle = second ? part * 8 - half : part * 8;
+        t.angle = !t.on ? 0 : second ? part * 8 - half : part * 8;
         t.sign = second ? 1.0f : -1.0f;
     }
     return t;
 }
 
 // The lane's 8 values turned: own and, where pairs are halves, the partner's ones.
-// sign 1 turns by the angle, -1 back.
+// sign 1 turns by the angle, -1 back.  Values that are not turned pass as they are: a
+// product with a sine of 0 would make NaN of an infinity beside or at them.
 template <bool NEIGHBOURS>
 __device__ __forceinline__ void turn(const Turn& t, const f32x2_t* angles, float sign, const float (&own)[8],
                                      const float (&other)[8], float (&z)[8]) {
     if (NEIGHBOURS) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const f32x2_t cs = t.on ? angles[t.angle + i] : f32x2_t{1.0f, 0.0f};
+            const f32x2_t cs = angles[t.angle + i];
             const float s = sign * cs.y;
-            z[2 * i] = own[2 * i] * cs.x - own[2 * i + 1] * s;
-            z[2 * i + 1] = own[2 * i + 1] * cs.x + own[2 * i] * s;
+            const float a = own[2 * i] * cs.x - own[2 * i + 1] * s, b = own[2 * i + 1] * cs.x + own[2 * i] * s;
+            z[2 * i] = t.on ? a : own[2 * i];
+            z[2 * i + 1] = t.on ? b : own[2 * i + 1];
         }
     } else {
         const float way = sign * t.sign;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const f32x2_t cs = t.on ? angles[t.angle + i] : f32x2_t{1.0f, 0.0f};
-            z[i] = own[i] * cs.x + other[i] * (way * cs.y);
+            const f32x2_t cs = angles[t.angle + i];
+            const float a = own[i] * cs.x + other[i] * (way * cs.y);
+            z[i] = t.on ? a : own[i];
         }
     }
 }
@@ -365,7 +368,7 @@ hipError_t launch_passes(const RopeArgs& a, hipStream_t stream) {
     for (int i = 0; i < 2; ++i)
         if (a.groups[i] > 0) tokens = std::max(tokens, std::min(a.rows[i] / a.heads[i], (rows + a.heads[i] - 2) / a.heads[i] + 1));
     const dim3 grid((unsigned)(a.groups[0] + a.groups[1]));
-    const uint32_t lds = tokens * (uint32_t)a.half * 8;
+    const uint32_t lds = std::max(tokens * (uint32_t)a.half * 8, 64u);   // eight angles are read where none are turned
     if constexpr (BACKWARD)
         hipLaunchKernelGGL((norm_rope_backward_kernel<T, D, NEIGHBOURS, PASSES>), grid, dim3(kThreads), lds, stream, a);
     else
