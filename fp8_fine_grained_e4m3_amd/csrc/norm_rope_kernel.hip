@@ -246,10 +246,11 @@ __global__ __launch_bounds__(kThreads) void norm_rope_kernel(RopeArgs a) {
             if (!NEIGHBOURS) {
                 values_of(from_lane(raw[p], t.partner), other);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) other[i] *= r * wo[i];
+                for (int i = 0; i < 8; ++i) other[i] = other[i] * r * wo[i];
             }
+            // the row's factor first: r * w may leave fp32's range where n * w does not
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] *= r * w[i];
+            for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
             turn<NEIGHBOURS>(t, sm_angles + (token[p] - first) * a.half, 1.0f, x, other, z);
             if (row0 + p * RPP + threadIdx.x / LPR < rows)
                 store_row<PASSES>(static_cast<T*>(a.out[kind]) + token[p] * a.out_stride[kind] + head[p] * D + part * 8, z);

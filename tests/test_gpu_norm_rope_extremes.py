@@ -63,3 +63,15 @@ def test_infinite_gradients_stay_in_their_place(D, R, dtype, interleaved):
         rows = torch.ones(x[i].shape[:2], dtype=torch.bool)
         rows[4, 1] = False
         assert torch.equal(got[i][rows], clean[i][rows])
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("T", [6, 3001])
+@pytest.mark.parametrize("size,weight", [(1e37, 1e-6), (3e37, 1e-30), (1e-8, 1e34), (1.0, 1e36), (1.0, 1e-36)])
+def test_weights_that_undo_the_norm(size, weight, T, interleaved):
+    """Rows far from 1 and weights as far the other way or further: the norm is applied to the row first, and no
+    product on the way leaves fp32's range where the result does not."""
+    announce(f"norm rope size={size} weight={weight} T={T} {interleaved}")
+    x, w, positions, freq, d = case(T, 3, 2, 64, 32, "f32", 31, size=size)
+    w = [v * weight for v in w]
+    check_forward(x, w, positions, freq, "f32", eps=2.0 ** -60, interleaved=interleaved)
