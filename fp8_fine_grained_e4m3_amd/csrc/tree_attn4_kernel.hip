@@ -21,12 +21,14 @@
 //    large an error as the output's own rounding, and fp16 holds the values exactly while
 //    their scales are from 2^-18 to 2^13 (weights, 2^kTop as large, are kept to 2^-36 of the
 //    largest).  Each step's scales are looked at, a word a lane; where one is out of that
-//    range, or NaN, the wave takes its steps again in bf16, which has fp32's exponents and
-//    holds every value, with P in two parts, the first 8 bits and the next 8.  Where a row's
+//    range, or NaN, the wave takes its steps again for the rows that see it, in bf16, which
+//    has fp32's exponents and holds every value, with P in two parts, the first 8 bits and
+//    the next 8.  Rows that do not see it keep what they have, and their bits.  Where a row's
 //    O passes fp32's largest number even so (values beyond 2^90), once more with that row's
 //    weights 2^-kDown as large, which 2^30 weights of 2^kLazy do not outgrow; always so, the
 //    exponentials' arguments would lose their last five bits.  (Always two bf16 parts: 145 us
-//    against 124 for two trees of 16 over 100001.)
+//    against 124 for two trees of 16 over 100001.  Where all scales are out of fp16's range:
+//    248 us against 127 for these, 91 against 52 for 32 single tokens over 8192.)
 //  * Maximum, sum and O are fp32; the maximum follows where a score of the row passes it by
 //    2^4, whatever other rows do, so that a row's bits are its own (all rows together: 124 us
 //    against 126 for two trees of 16 over 100001).
@@ -166,6 +168,23 @@ __device__ __forceinline__ uint32_t e2m1x2_to_bf16x2(uint32_t w, float scale) {
 template <int B>
 __device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t w, float scale) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, B));
+}
+
+// The bits that any lane of l's group of 16 has.
+__device__ __forceinline__ uint32_t any_of_group(uint32_t v) {
+    v |= (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true);     // lane ^ 1
+    v |= (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true);     // lane ^ 2
+    v |= (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, true);    // the other four of eight
+    v |= (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, true);    // the other eight of sixteen
+    return v;
+}
+
+// The bits that any of lanes l, l ^ 16, l ^ 32 and l ^ 48 has.
+__device__ __forceinline__ uint32_t any_of_groups(uint32_t v) {
+    u32x2_t s = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = s.x | s.y;
+    s = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return s.x | s.y;
 }
 
 // Eight values of a word as an MFMA fragment.
@@ -314,7 +333,9 @@ __global__ __launch_bounds__(W * 64, W == 16 ? 4 : D == 256 ? 1 : D == 128 || W 
     float down[RT];
 #pragma unroll
     for (int t = 0; t < RT; ++t) down[t] = -kTop;
-    uint32_t out = 0;                     // a scale of a value was out of fp16's range
+    // Whether a scale of a value was out of fp16's range: in a step that all rows see, and, bit
+    // t, one that the lane's row of tile t sees.
+    uint32_t out = 0, out_seen = 0;
     auto pass = [&](auto is_wide) {
     constexpr bool WIDE = decltype(is_wide)::value;
 #pragma unroll
@@ -467,10 +488,33 @@ __global__ __launch_bounds__(W * 64, W == 16 ? 4 : D == 256 ? 1 : D == 128 || W 
                 for (int i = 0; i < 4; ++i)
                     if (!at.live[u] || j0 + 16 * u + 4 * g + i >= L) vscale[u][i] = 0x3F800000u;
             if (!WIDE) {
+                auto far = [&](int u, int i) { return ((vscale[u][i] & 0x7F800000u) - (kLeast << 24 >> 1)) & 0xF0000000u; };
+                uint32_t any = 0;
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) out |= ((vscale[u][i] & 0x7F800000u) - (kLeast << 24 >> 1)) & 0xF0000000u;
+                    for (int i = 0; i < 4; ++i) any |= far(u, i);
+                if (__any(any != 0)) {
+                    // One out of the range, or NaN, counts for the rows that see its key alone: those take
+                    // their steps again, and to the others it must not be more than 0 times a number.
+                    uint32_t off = 0;     // bit 4 u + i
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (far(u, i)) {
+                                off |= 1u << (4 * u + i);
+                                vscale[u][i] = 0x3F800000u;
+                            }
+                    off = any_of_group(off);       // of all blocks: the 16 lanes have different ones
+#pragma unroll
+                    for (int t = 0; t < RT; ++t)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if ((off >> (4 * u + i) & 1) && sc[t][u][i] != -__builtin_inff()) out_seen |= 1u << t;
+                }
             }
             if (WIDE && apart) {
                 bool bad = false;
@@ -621,9 +665,21 @@ __global__ __launch_bounds__(W * 64, W == 16 ? 4 : D == 256 ? 1 : D == 128 || W 
     }
     };
     pass(std::false_type());
-    if (__any(out != 0)) {
-        // the same in bf16, and once more for rows whose O passed fp32's largest number
-        for (int again = 0; again < 2; ++again) {
+    // the lane's values of O of its row of tile t, in the wave's LDS
+    auto o_of = [&](int t, int l) { return sm_o[wave] + (16 * t + (l & 15)) * PITCH + 4 * (l >> 4) * DT; };
+    if (__any(out | out_seen)) {
+        // The rows that saw such a scale take the steps again in bf16, and once more where O passed fp32's
+        // largest number; the others keep what they have, so that it hangs on what they see alone.
+        const uint32_t again = __any(out) ? ~0u : any_of_groups(out_seen);
+        float m16[RT], base16[RT], l16[RT];
+        const int put = fresh(lane);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            m16[t] = m[t], base16[t] = base[t], l16[t] = l[t];
+#pragma unroll
+            for (int i = 0; i < DT; ++i) *reinterpret_cast<f32x4_t*>(o_of(t, put) + 4 * i) = acc[t][i];
+        }
+        for (int n = 0; n < 2; ++n) {
             pass(std::true_type());
             bool off = false;
 #pragma unroll
@@ -638,6 +694,14 @@ __global__ __launch_bounds__(W * 64, W == 16 ? 4 : D == 256 ? 1 : D == 128 || W 
             }
             if (!__any(off)) break;
         }
+        const int get = fresh(lane);      // another copy: what was put down is not kept in registers
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            if (again >> t & 1) continue;
+            m[t] = m16[t], base[t] = base16[t], l[t] = l16[t];
+#pragma unroll
+            for (int i = 0; i < DT; ++i) acc[t][i] = *reinterpret_cast<const f32x4_t*>(o_of(t, get) + 4 * i);
+        }
     }
 
     // The waves put down their O and meet: a thread then adds up four values of a
@@ -650,7 +714,7 @@ __global__ __launch_bounds__(W * 64, W == 16 ? 4 : D == 256 ? 1 : D == 128 || W 
         const int k = __builtin_amdgcn_frexp_expf(l[t]), shift = -k - kSpare;
         const float top = m[t] == -__builtin_inff() ? m[t] : base[t] + (float)k;
         if (eg == 0) sm_ml[wave][16 * t + er16] = f32x2_t{top, __builtin_amdgcn_ldexpf(l[t], -k)};
-        float* mine = sm_o[wave] + (16 * t + er16) * PITCH + 4 * eg * DT;
+        float* mine = o_of(t, elane);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll

@@ -120,3 +120,24 @@ def test_smallest_and_largest_scales(D, N, room):
     c["q"][..., :32] *= 2.0 ** 124
     c["q"][..., 32:64] *= 2.0 ** -121
     check(c, "bf16")
+
+
+@pytest.mark.parametrize("D,N,G,room", [(64, 9, 2, 0), (128, 9, 4, 0), (256, 9, 4, 0), (128, 20, 4, 5000), (64, 12, 8, 9000), (128, 12, 8, 9000)])
+@pytest.mark.parametrize("byte", [100, 150, 240, 255])
+def test_a_hidden_values_scale_changes_no_bit(D, N, G, room, byte):
+    """The scale of a drafted token's value goes out of fp16's range, or NaN: rows that do not see the token keep
+    their bits, and those that see it are as the reference."""
+    announce(f"fp4 hidden scale 2^{byte - 127}, D={D} N={N} room={room}")
+    c = forms.case(3, N, 2, G, D, 16, 200, room, forms.VALUES["fp16"], D + N)
+    o, lse = run(c)
+    for token, block in ((N // 3, 0), (N // 3 + 1, D // 32 - 1)):
+        for b in range(3):
+            page, place = forms.at(c, b, int(c["ctx"][b]) + token)
+            if token < c["lens"][b]:
+                c["cache"][1][1][page, :, place, block] = byte
+    misses = ~c["mask"][:, :, [N // 3, N // 3 + 1]].any(-1)
+    assert misses[0].any() and not misses[0].all()
+    o2, lse2 = run(c)
+    keep = torch.from_numpy(misses).cuda()
+    assert torch.equal(o2[keep].view(torch.int16), o[keep].view(torch.int16)) and torch.equal(lse2[keep], lse[keep])
+    check(c, "fp16")
