@@ -347,8 +347,9 @@ __global__ __launch_bounds__(W * 64, W == 16 ? 4 : D == 256 ? 1 : D == 128 || W 
         for (int i = 0; i < DT; ++i) acc[t][i] = f32x4_t{0, 0, 0, 0};
     }
     // Scores stay products until the exponential: with a scale that is not negative (the
-    // query's sign takes that) they are in the same order.  Above 0, so that -infinity stays.
-    const float c2 = __builtin_fmaxf(__builtin_fabsf(a.scale) * kLog2e, 0x1p-126f);
+    // query's sign takes that) they are in the same order.  Above 0, so that -infinity stays, and
+    // so little that no product brings a score with the scale 0 to 2^-20.
+    const float c2 = __builtin_fmaxf(__builtin_fabsf(a.scale) * kLog2e, 0x1p-149f);
     const bool apart = a.N > 1;           // rows of several tokens: they may see different keys
     if (lo + wave < hi) {
     // uniform bases, a lane's place in 32 bits

@@ -141,3 +141,11 @@ def test_a_hidden_values_scale_changes_no_bit(D, N, G, room, byte):
     keep = torch.from_numpy(misses).cuda()
     assert torch.equal(o2[keep].view(torch.int16), o[keep].view(torch.int16)) and torch.equal(lse2[keep], lse[keep])
     check(c, "fp16")
+
+
+@pytest.mark.parametrize("scale", [0.0, 2.0 ** -140, -(2.0 ** -128)])
+def test_scales_of_scores_next_to_zero(scale):
+    """Products of queries and keys next to fp32's largest number, brought to little or nothing by the scale."""
+    announce(f"fp4 scale of scores {scale}")
+    c = forms.case(3, 5, 2, 4, 128, 16, 200, 0, forms.VALUES["fp16"], 3, q_scale=2.0 ** 119, scale=scale)
+    check(c, "fp16")
