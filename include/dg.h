@@ -497,13 +497,16 @@ dg_status dg_fp8_kv_cache_read(const uint8_t* k_codes, const float* k_sf,
  *   - A request that shrinks (drafts that were not accepted; -c when it is done)
  *     gives the pages behind its new end back, to the ring's end, requests in
  *     order; they can be taken by later calls.  Its table row stays as it is.
- *     A page that several requests hold comes back from each; what passes the ring's
- *     num_pages - n other places is left out.
+ *     A page that several requests hold comes back from each, and later calls may then
+ *     give it to two; what passes the ring's num_pages - n other places is left out.
+ *     Pages with more than one holder are the caller's to count: keep them out of rows
+ *     that shrink.
  *   page_table    [B, max_pages] int32, changed in place
  *   context_lens  [B]            clamped to [0, max_pages * page_size]
  *   add_lens      [B]            new tokens, or (negative) dropped ones
  *   pool_pages    [num_pages]    changed in place
- *   pool_state    [2]            head taken modulo num_pages, n clamped to [0, num_pages]
+ *   pool_state    [2]            head, as 32 bits without a sign, taken modulo num_pages;
+ *                                n clamped to [0, num_pages]
  *   slots, positions  padded == 1: [B, rows], token i of request b in row i;
  *                 padded == 0: [rows], the requests' tokens end to end (those past
  *                 rows are left out).  A token's position is c + i.  Its slot is -1
