@@ -768,7 +768,8 @@ def kv_cache_plan(page_table: torch.Tensor, context_lens: torch.Tensor, add_lens
     context_lens[b] tokens (int32 [B]) gets add_lens[b] more (int32 [B]); where that
     is negative it loses tokens at its end.  pool = (pages, state), as
     make_kv_page_pool makes it.  New pages go from the pool into page_table (int32
-    [B, max_pages]), pages behind a new end back into it; both are changed in place.
+    [B, max_pages]), pages behind a new end back into it; both are changed in place.  A
+    page that several requests hold would come back from each.
     Returns (slots, positions, lens, state): int32 [B, rows] where padded, else
     [rows], the requests' tokens end to end (rows without a token, and tokens of
     requests that the pool or the table has no room for, have the slot -1); the lengths
@@ -870,7 +871,8 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tens
     None: ones), then the rotation of the first R = 2 * len(inv_freq) values by
     positions (int32 [T]) times inv_freq (fp32 [R / 2], R a multiple of 16): values i and
     i + R / 2 are a pair, or 2 i and 2 i + 1 where interleaved.  Returns (q, k) like
-    those given but dense, or fills out, which may be q and k themselves."""
+    those given but dense, or fills out, which may be q and k themselves.  As elsewhere
+    here nothing is recorded for autograd: qk_norm_rope_backward has the gradients."""
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} must be [T, heads, D]")
     (T, Hq, D), H, on, wq, wk = q.shape, k.shape[1], q.get_device(), q_weight, k_weight
