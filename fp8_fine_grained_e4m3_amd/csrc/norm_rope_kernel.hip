@@ -19,11 +19,12 @@
 // is taken in 64 bits, in turns, and reduced to an eighth of a turn before it is
 // rounded to fp32, so far positions lose nothing.
 //
-// Measured: 16384 tokens of 32 + 8 heads of 128 in bf16, 336 MB, 66 us, 5.1 TB/s (a 2 GiB
-// copy: 4.9 to 5.3), with plain stores 71; their gradients, 503 MB, 107 us, 4.7 TB/s, of
-// which the sums of dw take 5.  Four rows a lane and step (gradients: two); with two, 71 us.
-// The gradients' grid is kBackwardGroups workgroups, each with a sum of dw: 512 take 118
-// us, 2048 take 112.  5 tokens: 3.6 us.
+// Measured: 16384 tokens of 32 + 8 heads of 128 in bf16, 336 MB, 63 us, 5.3 TB/s (a 2 GiB
+// copy: 4.9 to 5.3); their gradients, 503 MB, 104 us, 4.8 TB/s, of which the sums of dw take
+// 5.  8192 tokens in fp32, the same bytes: 67 and 107 us.  5 tokens: 3.6 us.  When these took
+// 66 and 107 us: plain stores 71; two rows a lane and step instead of four (gradients: of two)
+// 71; gradients, whose grid is kBackwardGroups workgroups, each with a sum of dw, in 512 of
+// them 118, in 2048 112.
 #include "fp8_values.h"
 #include "row_access.h"
 #include "serve_internal.h"

@@ -58,8 +58,8 @@ __device__ __forceinline__ int64_t pool_row(int slot, int h, int H, int page_shi
     return ((page * H + h) << page_shift) + at;
 }
 
-// The sum, and the largest bit pattern, of a value over the LPR lanes that hold a row
-// (4, 8, 16 or 32 lanes, on a multiple of that).
+// The value of another lane, by a DPP control; and the sum of a value over the LPR lanes
+// that hold a row (4, 8, 16 or 32 lanes, on a multiple of that).
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp(uint32_t v) {
     return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);

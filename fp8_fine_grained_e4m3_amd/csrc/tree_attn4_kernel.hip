@@ -38,13 +38,15 @@
 // is counted by a product of its own for the rows that see it.
 //
 // Bound: a few rows per key head leave the cache's bytes as the floor, half of the FP8
-// cache's; with many rows the VALU (widening keys and values, exponentials) is it.  The
+// cache's; with many rows each wave's chain of widening, product, exponentials and product
+// is it, which two waves a SIMD overlap in part (two trees of 16 over 100001: VALU 47% and
+// matrix unit 21% busy; the row blocks of a run widen the same keys, each for itself).  The
 // cache goes from HBM straight to registers; a wave asks for its next step's keys and
 // values when it is done with the ones it has, and the other waves of its SIMD cover the
 // wait.  (Asked for during the step, or two steps ahead: the same times, and 10 to 40
 // registers more.)  Work is cut into runs and joined as over the FP8 cache.
-// Measured, in graphs (a batch "of n over c" goes from n tokens and c positions down to
-// half of them): 32 single tokens over 8192, 32 / 8 heads of 128, 215 MB, 52 us, 4.1 TB/s,
+// Measured, in graphs, in tables as wide as the longest request (a batch "of n over c" goes
+// from n tokens and c positions down to half of them): 32 single tokens over 8192, 32 / 8 heads of 128, 215 MB, 52 us, 4.1 TB/s,
 // of which the first keys take 5 us to come (a loop over the same bytes alone: 38 us); one
 // over 1000, 9.3 us; two trees of 16 over 100001, 64 / 8 heads of 128, 164 MB and 66 GFLOP,
 // 126 us and 0.52 PFLOP/s; 7 trees of 24 over 3001, the last of them idle, 16 us.
@@ -762,10 +764,10 @@ __global__ __launch_bounds__(W * 64, W == 16 ? 4 : D == 256 ? 1 : D == 128 || W 
 // Rows of a workgroup: 16 where there are no more (and for D = 256, whose O fills
 // the registers), and where 32 would leave CUs without a workgroup and keys are few
 // enough to be widened twice; else 32.  16 against 32 rows, in graphs, D = 128: 8 trees
-// of 16 over 1000, 32 / 8 heads, 10.7 us against 15.4; over 8000, 37 against 42; but over
-// 14000, 59 against 54; 16 of 16 over 1000, 14.3 against 16.4; but over 3000, 30 against 27.
-// D = 64: 7 trees of 24 over 3001, 32 / 4 heads, 18.7 against 20.4.  (64, with the query in
-// LDS: 33 us for these; D = 128 does not fit the registers, 182 us against 123.)
+// of 16 over 1000, 32 / 8 heads, 11.7 us against 16.4; over 8000, 39 against 43; but over
+// 14000, 63 against 57; 16 of 16 over 1000, 14.7 against 16.6; but over 3000, 30 against 28.
+// D = 64: 7 trees of 24 over 3001, 32 / 4 heads, 16 against 21.  (64, with the query in
+// LDS: 33 us for these when 32 took 20; D = 128 does not fit the registers, 182 us against 123.)
 // Whole requests, a workgroup each and no second kernel, where that is soon done
 // whatever the lengths turn out to be: up to 1024 positions (D = 256: 512), up to 2048
 // where requests and heads make 32 workgroups (D = 256: 128), up to 4096 where they make
@@ -788,7 +790,9 @@ __global__ __launch_bounds__(W * 64, W == 16 ? 4 : D == 256 ? 1 : D == 128 || W 
 // 8192, 45 against 47; split, 32 of 20000, 76 against 85; but 32 of 1000 in either table
 // 1 us more, and with fewer or more requests, 16 of 8192, 25.3 against 24.7, 8 of 1000 in a
 // table of 60000, 16 against 14, 256 of 300 in one of 20000, 38.6 against 36.2).
-// From the sizes alone: lengths are on the device.
+// From the sizes alone: lengths are on the device.  All these figures are of tables as wide
+// as the longest request; short requests in a wider one are cut as if they were long (the
+// 7 trees of 24 in a table of 32768: 26 us against 16; 8 trees of 16 over 1000: 26 against 11.5).
 Shape shape_of(int64_t B, int64_t N, int64_t Hq, int64_t H, int64_t D, int64_t max_pages, int64_t page_size) {
     const int64_t rows = N * (Hq / H), most = (max_pages * page_size + kStep - 1) / kStep;
     const int64_t pairs = (rows + 31) / 32 * B * H;     // workgroups of two row tiles

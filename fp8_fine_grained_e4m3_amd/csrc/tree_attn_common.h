@@ -18,8 +18,9 @@ namespace dg {
 namespace {
 
 constexpr int kStep = 32;                 // keys of a wave's step
-// O is put down 2^kSpare too small: waves and parts, 8 x 768 at most, each with a sum
-// below 1, then add up without passing fp32's largest number, whatever the values.
+// O is put down 2^kSpare too small: waves and parts (at most 8 x 768 over the FP8 cache, 16 x
+// 256 over the FP4 one), each with a sum below 1, then add up without passing fp32's largest
+// number, whatever the values.
 constexpr int kSpare = 13;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
