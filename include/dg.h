@@ -664,8 +664,8 @@ dg_status dg_fp4_kv_cache_read(const uint8_t* k_codes, const uint8_t* k_sf,
  *     infinite, with byte 0 all as 0);
  *   - a weight, alone, kept to 11 bits and to 2^-36 of the row's largest; where a value
  *     that the token sees, read with it, has a scale outside 2^-18 to 2^13, to 16 bits and
- *     to 2^-92 of the largest.  What is less, and an o below 2^-92, may count as 0.  What a
- *     token does not see changes no bit of its o and lse;
+ *     to 2^-92 of the largest.  What is less, and an o below 2^-92, may count as 0.  Keys and
+ *     values that a token does not see change no bit of its o and lse;
  *   - a NaN scale in a key that a token sees makes the token's o and lse NaN; one in a
  *     value makes the 32 values of o that it belongs to NaN;
  *   - any codes and scales past a request's last token and in hidden pages.
