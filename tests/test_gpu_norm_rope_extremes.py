@@ -1,13 +1,11 @@
 """The norms with rotation and their gradients at weights and rows far from 1, and where a value is
 infinite: what the formula does not mix stays apart."""
-import numpy as np
 import pytest
 import torch
 
 import fp8_fine_grained_e4m3_amd as dg
-from tests import paged
-from tests.parity import announce, to64
-from tests.test_gpu_norm_rope import TYPES, case, check_backward, check_forward
+from tests.parity import announce
+from tests.test_gpu_norm_rope import case, check_forward
 
 pytestmark = pytest.mark.gpu
 
